@@ -19,6 +19,7 @@ STATUS = {
 TILE_ROW, TILE_COL, TILE_COL_TILED = 0, 1, 2
 LAYOUT = {"fprop": 0, "dgrad": 1, "wgrad": 2, "dgrad_t": 3, "fprop_tiled": 4, "dgrad_t_tiled": 5, "wgrad_tiled": 6}
 OUT_BF16, OUT_FP32 = 0, 1
+MOE_GATE = {"softmax": 0, "sigmoid": 1}
 
 # name -> (restype, argtypes); mirrors include/fp8bs.h
 _P = ctypes.c_void_p
@@ -54,6 +55,18 @@ SIGNATURES = {
     "fp8_pack_tokens": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P]),
     "fp8_unpack_tokens": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _I64, _P, _I64, _P]),
     "fp8_dequant_tokens": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _I64, _P]),
+    "fp8_layer_norm": (ctypes.c_int, [_P, _I64, _I64, _I64, ctypes.c_int, _P, _P, ctypes.c_int, _F, _P, _I64, _P,
+                                      _P, _P, _I64, _P, _I64, _P]),
+    "fp8_layer_norm_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _I64, _I64, ctypes.c_int, _P, _P, _P,
+                                               ctypes.c_int, _P, _I64, _P, _P, _P, _I64, _P]),
+    "fp8_layer_norm_backward_workspace": (_I64, [_I64, _I64]),
+    "fp8_moe_few_tokens": (ctypes.c_int, [_I64, _I64, _I64, _I32, _I32, _I32, _I32, _P, _I64, _P, _I64, _P,
+                                          ctypes.c_int, ctypes.c_int, _F, _P, _P, _P, _P, _P, ctypes.c_int, _I64,
+                                          _P, _P, _P, _I64, _P]),
+    "fp8_moe_few_tokens_workspace": (_I64, [_I64, _I64, _I64, _I32, _I32, _I32]),
+    "fp8_adapter_linear": (ctypes.c_int, [_I64, _I64, _I64, _I32, _I32, _P, _I64, _P, _P, _I64, _P, _P, _P, _P,
+                                          _P, ctypes.c_int, _I64, _P, _I64, _P]),
+    "fp8_adapter_linear_workspace": (_I64, [_I64, _I64, _I64, _I32, _I32]),
     "fp8_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "fp8_abi_version": (ctypes.c_int, []),
 }
@@ -78,7 +91,10 @@ class FP8Error(RuntimeError):
 
 
 def load_library(path: str | None = None):
-    """Load libfp8bs.so (once).  Raises OSError/RuntimeError if it is absent."""
+    """Load libfp8bs.so (once).  Raises OSError/RuntimeError if it is absent.
+
+    A library named by `path` may hold a part of the entry points (a host-only
+    build of one file of the ABI); the built library has to have them all."""
     global _lib
     with _lock:
         if _lib is not None:
@@ -90,6 +106,8 @@ def load_library(path: str | None = None):
                 "(there is no CPU fallback)")
         lib = ctypes.CDLL(p)
         for name, (res, args) in SIGNATURES.items():
+            if path is not None and not hasattr(lib, name):
+                continue
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args

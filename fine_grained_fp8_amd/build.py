@@ -20,7 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libfp8bs.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
-SOURCES = ["api.cpp", "quant.hip", "gemm.hip", "payload.hip", "accum.hip", "tiles.hip", "probe.hip", "fused.hip"]
+SOURCES = ["api.cpp", "quant.hip", "gemm.hip", "payload.hip", "accum.hip", "tiles.hip", "probe.hip", "fused.hip",
+           "api_layers.cpp", "norm.hip", "few.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

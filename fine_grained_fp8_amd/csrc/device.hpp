@@ -158,4 +158,45 @@ __device__ __forceinline__ void transpose4x4_bytes(uint32_t a0, uint32_t a1, uin
   o3 = __builtin_amdgcn_perm(t3, t2, 0x07060302u);
 }
 
+// 1x128 quantization of a lane's 8 BF16 values (packed in d): the 16 lanes
+// of a DPP row hold the tile.  The online rule, as in the row quantizer.
+__device__ __forceinline__ uint2 quant8_bf16(const uint4& d, float& s) {
+  const uint32_t t = row16_max_u32(absmax_bits8(d));
+  s = tile_scale(t);
+  uint2 out;
+  if (t < kBf16InfAbs) {
+    const float r = recip_online(s);
+    out.x = pack4_sat(div_by_scale(bf16_lo(d.x), s, r), div_by_scale(bf16_hi(d.x), s, r),
+                      div_by_scale(bf16_lo(d.y), s, r), div_by_scale(bf16_hi(d.y), s, r));
+    out.y = pack4_sat(div_by_scale(bf16_lo(d.z), s, r), div_by_scale(bf16_hi(d.z), s, r),
+                      div_by_scale(bf16_lo(d.w), s, r), div_by_scale(bf16_hi(d.w), s, r));
+  } else {
+    out.x = pack4_sat_nan(bf16_lo(d.x) / s, bf16_hi(d.x) / s, bf16_lo(d.y) / s, bf16_hi(d.y) / s);
+    out.y = pack4_sat_nan(bf16_lo(d.z) / s, bf16_hi(d.z) / s, bf16_lo(d.w) / s, bf16_hi(d.w) / s);
+  }
+  return out;
+}
+
+// The same rule on a lane's 8 FP32 values, given the tile's |y| max as FP32
+// bits (NaN patterns sort above infinity): s = max(fl32(amax / 448), floor).
+// r = fl32(1 / s) and one Newton-Markstein correction per quotient, three
+// operations in place of a full division; the quotient can be one FP32 ulp
+// from fl32(y / s), 2^-20 of a code's spacing.
+__device__ __forceinline__ uint2 quant8_f32(const float (&y)[8], uint32_t amax_bits, float& s) {
+  uint2 out;
+  if (amax_bits < 0x7F800000u) {
+    s = fmaxf(__uint_as_float(amax_bits) / 448.0f, scale_floor());
+    const float r = 1.0f / s;
+    out.x = pack4_sat(div_by_scale(y[0], s, r), div_by_scale(y[1], s, r), div_by_scale(y[2], s, r),
+                      div_by_scale(y[3], s, r));
+    out.y = pack4_sat(div_by_scale(y[4], s, r), div_by_scale(y[5], s, r), div_by_scale(y[6], s, r),
+                      div_by_scale(y[7], s, r));
+  } else {
+    s = __uint_as_float(amax_bits == 0x7F800000u ? amax_bits : kCanonicalNaN);
+    out.x = pack4_sat_nan(y[0] / s, y[1] / s, y[2] / s, y[3] / s);
+    out.y = pack4_sat_nan(y[4] / s, y[5] / s, y[6] / s, y[7] / s);
+  }
+  return out;
+}
+
 }  // namespace fp8bs

@@ -426,3 +426,228 @@ def quant_act_tiles(x: torch.Tensor, tile: int = 128, rank: int = 1, *, sat_coun
                                  _ptr(s), s.stride(0), _ptr(sat_count), _stream(stream))
     _lib.check("fp8_quant_act_tiles", st)
     return q, s
+
+
+_FLOATS = (torch.bfloat16, torch.float32)
+
+
+def _is_fp32(t: torch.Tensor) -> int:
+    return _lib.OUT_FP32 if t.dtype == torch.float32 else _lib.OUT_BF16
+
+
+def _check_vec(name, t, n, dtypes):
+    if t is None:
+        return
+    if t.dim() != 1 or t.numel() != n or not t.is_contiguous() or not t.is_cuda or t.dtype not in dtypes:
+        raise ValueError(f"{name}: a contiguous device vector of {n} elements of {dtypes} is required, got "
+                         f"{t.dtype} {tuple(t.shape)}")
+
+
+def _norm_affine(weight, bias, cols):
+    _check_vec("weight", weight, cols, _FLOATS)
+    _check_vec("bias", bias, cols, _FLOATS)
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError(f"weight is {weight.dtype} and bias {bias.dtype}: one type is required")
+    t = weight if weight is not None else bias
+    return _lib.OUT_BF16 if t is None else _is_fp32(t)
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: on {t.device}, the input is on {dev}")
+
+
+def _workspace(nbytes: int, device, stream):
+    """Scratch memory of one call.  It comes from the current stream's memory
+    pool; a call on another stream tells the pool, so that the memory is not
+    handed out again before that stream is done with it."""
+    ws = torch.empty(max(nbytes, 0), dtype=torch.uint8, device=device)   # -1: the call itself refuses
+    if stream is not None and stream != torch.cuda.current_stream(device):
+        ws.record_stream(stream)
+    return ws
+
+
+def layer_norm(x: torch.Tensor, weight=None, bias=None, *, eps: float = 1e-5, return_stats: bool = False,
+               out=None, stream=None):
+    """Layer norm over the rows of x [rows][cols] (bfloat16 or float32).
+
+    weight, bias: optional [cols] vectors of one type (bfloat16 or float32).
+    Returns y in x's type, or (y, mean, rstd) with the float32 row statistics
+    that layer_norm_backward takes.
+    """
+    lib = _lib.load_library()
+    _check_2d("x", x, _FLOATS)
+    rows, cols = x.shape
+    wt = _norm_affine(weight, bias, cols)
+    _same_device(x.device, weight=weight, bias=bias, out=out)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+    else:
+        _check_2d("out", out, (x.dtype,))
+        if out.shape != x.shape:
+            raise ValueError(f"out: expected {tuple(x.shape)}, got {tuple(out.shape)}")
+    mean = rstd = None
+    if return_stats:
+        mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=x.device)
+    st = lib.fp8_layer_norm(_ptr(x), rows, cols, x.stride(0), _is_fp32(x), _ptr(weight), _ptr(bias), wt, eps,
+                            _ptr(out), out.stride(0), _ptr(mean), _ptr(rstd), None, 0, None, 0, _stream(stream))
+    _lib.check("fp8_layer_norm", st)
+    return (out, mean, rstd) if return_stats else out
+
+
+def layer_norm_quant(x: torch.Tensor, weight=None, bias=None, *, eps: float = 1e-5, return_y: bool = False,
+                     return_stats: bool = False, stream=None):
+    """Layer norm of x [rows][cols] with the 1x128 quantization of the result
+    fused in: (q [rows][cols] uint8, s [cols/128][round_up(rows, 4)] float32),
+    the operand layout of quant_act_1x128(..., "row"), quantized from the FP32
+    result.  return_y appends y (x's type); return_stats appends mean, rstd.
+    """
+    lib = _lib.load_library()
+    _check_2d("x", x, _FLOATS)
+    rows, cols = x.shape
+    wt = _norm_affine(weight, bias, cols)
+    _same_device(x.device, weight=weight, bias=bias)
+    q = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+    s = torch.empty((cols // 128, round_up(rows, 4)), dtype=torch.float32, device=x.device)
+    y = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if return_y else None
+    mean = rstd = None
+    if return_stats:
+        mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=x.device)
+    st = lib.fp8_layer_norm(_ptr(x), rows, cols, x.stride(0), _is_fp32(x), _ptr(weight), _ptr(bias), wt, eps,
+                            _ptr(y), cols, _ptr(mean), _ptr(rstd), _ptr(q), cols, _ptr(s), s.stride(0),
+                            _stream(stream))
+    _lib.check("fp8_layer_norm", st)
+    return (q, s) + ((y,) if return_y else ()) + ((mean, rstd) if return_stats else ())
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor, weight=None, *,
+                        stream=None):
+    """Gradients of layer_norm: (dx in x's type, dweight, dbias float32 [cols]).
+
+    dy and x: [rows][cols] of one type; mean, rstd: the statistics that
+    layer_norm(..., return_stats=True) returned; weight: as in the forward.
+    """
+    lib = _lib.load_library()
+    _check_2d("x", x, _FLOATS)
+    _check_2d("dy", dy, (x.dtype,))
+    if dy.shape != x.shape:
+        raise ValueError(f"dy {tuple(dy.shape)} and x {tuple(x.shape)} differ")
+    rows, cols = x.shape
+    wt = _norm_affine(weight, None, cols)
+    _check_vec("mean", mean, rows, (torch.float32,))
+    _check_vec("rstd", rstd, rows, (torch.float32,))
+    _same_device(x.device, dy=dy, mean=mean, rstd=rstd, weight=weight)
+    dx = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+    dweight, dbias = torch.empty((2, cols), dtype=torch.float32, device=x.device)
+    nbytes = lib.fp8_layer_norm_backward_workspace(rows, cols)
+    ws = _workspace(nbytes, x.device, stream)
+    st = lib.fp8_layer_norm_backward(_ptr(dy), dy.stride(0), _ptr(x), x.stride(0), rows, cols, _is_fp32(x),
+                                     _ptr(mean), _ptr(rstd), _ptr(weight), wt, _ptr(dx), dx.stride(0),
+                                     _ptr(dweight), _ptr(dbias), _ptr(ws), nbytes, _stream(stream))
+    _lib.check("fp8_layer_norm_backward", st)
+    return dx, dweight, dbias
+
+
+def _check_codes(name, t, shape):
+    if t.dtype not in (torch.uint8, torch.float8_e4m3fn) or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous E4M3 codes {shape} required, got {t.dtype} {tuple(t.shape)}")
+
+
+def _check_scales(name, t, shape):
+    if t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous float32 {shape} required, got {t.dtype} {tuple(t.shape)}")
+
+
+def moe_few_tokens(x: torch.Tensor, router: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor, w2: torch.Tensor,
+                   s2: torch.Tensor, *, top_k: int, gate: str = "softmax", bias=None, normalize: bool = True,
+                   scale: float = 1.0, first_expert: int = 0, return_routing: bool = False,
+                   out_dtype=torch.bfloat16, out=None, stream=None):
+    """A whole mixture-of-experts layer for up to 64 tokens x [T][H] bfloat16.
+
+    router: bfloat16 [E][H]; gate: "softmax" or "sigmoid"; bias: optional
+    float32 [E] added to the sigmoid scores for the choice only; the chosen
+    scores are normalized to sum 1 (normalize) and multiplied by scale.
+    w13 [local][2 I][H], w2 [local][H][I]: operand-tiled codes, each expert
+    quantized by quant_weight_128x128(..., tiled=True) (w13: gate rows, then
+    up rows), with block scales s13 [local][2 I/128][H/128] and s2
+    [local][H/128][I/128].  The experts held are first_expert ..
+    first_expert + local - 1 of E; the others' contributions are left out.
+    Returns y [T][H] in out_dtype, or (y, ids int32 [T][top_k], gates float32
+    [T][top_k]) with return_routing.
+    """
+    lib = _lib.load_library()
+    _check_2d("x", x, (torch.bfloat16,))
+    _check_2d("router", router, (torch.bfloat16,))
+    T, H = x.shape
+    E = router.shape[0]
+    if router.shape[1] != H or w2.dim() != 3 or gate not in _lib.MOE_GATE:
+        raise ValueError(f"x {tuple(x.shape)}, router {tuple(router.shape)}, w2 {tuple(w2.shape)}, gate {gate!r}")
+    local, _, I = w2.shape
+    _check_codes("w13", w13, (local, 2 * I, H))
+    _check_codes("w2", w2, (local, H, I))
+    _check_scales("s13", s13, (local, 2 * I // 128, H // 128))
+    _check_scales("s2", s2, (local, H // 128, I // 128))
+    _check_vec("bias", bias, E, (torch.float32,))
+    _same_device(x.device, router=router, w13=w13, s13=s13, w2=w2, s2=s2, bias=bias, out=out)
+    if out is None:
+        out = torch.empty((T, H), dtype=out_dtype, device=x.device)
+    else:
+        _check_2d("out", out, _FLOATS)
+        if out.shape != x.shape:
+            raise ValueError(f"out: expected {tuple(x.shape)}, got {tuple(out.shape)}")
+    ids = gates = None
+    if return_routing:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=x.device)
+        gates = torch.empty((T, top_k), dtype=torch.float32, device=x.device)
+    nbytes = lib.fp8_moe_few_tokens_workspace(T, H, I, E, local, top_k)
+    ws = _workspace(nbytes, x.device, stream)
+    st = lib.fp8_moe_few_tokens(T, H, I, E, first_expert, local, top_k, _ptr(x), x.stride(0), _ptr(router),
+                                router.stride(0), _ptr(bias), _lib.MOE_GATE[gate], int(normalize), scale, _ptr(w13),
+                                _ptr(s13), _ptr(w2), _ptr(s2), _ptr(out), _is_fp32(out), out.stride(0), _ptr(ids),
+                                _ptr(gates), _ptr(ws), nbytes, _stream(stream))
+    _lib.check("fp8_moe_few_tokens", st)
+    return (out, ids, gates) if return_routing else out
+
+
+def adapter_linear(x: torch.Tensor, w: torch.Tensor, sw: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor,
+                   ids: torch.Tensor, *, scales=None, out_dtype=torch.bfloat16, out=None, stream=None):
+    """A shared FP8 projection with a low-rank adapter of its own per token:
+    y[t] = W_q . quant_1x128(x[t]) + scales[a] * lora_b[a] . (lora_a[a] . x[t])
+    with a = ids[t] (negative: no adapter).
+
+    x: bfloat16 [T][K]; w [N][K]: operand-tiled codes of
+    quant_weight_128x128(..., tiled=True), sw its block scales; lora_a bfloat16
+    [n][rank][K], lora_b bfloat16 [n][N][rank] (rank % 8 == 0, <= 128); ids int32
+    [T]; scales: optional float32 [n].  Returns y [T][N] in out_dtype.
+    """
+    lib = _lib.load_library()
+    _check_2d("x", x, (torch.bfloat16,))
+    _check_2d("sw", sw, (torch.float32,))
+    T, K = x.shape
+    if lora_a.dim() != 3 or lora_b.dim() != 3 or w.dim() != 2:
+        raise ValueError("w, lora_a, lora_b: expected [N][K], [n][rank][K], [n][N][rank]")
+    N = w.shape[0]
+    n, r, _ = lora_a.shape
+    _check_codes("w", w, (N, K))
+    if sw.shape[0] < N // 128 or sw.shape[1] < K // 128:
+        raise ValueError(f"sw: expected at least {(N // 128, K // 128)}, got {tuple(sw.shape)}")
+    for name, t, shape in (("lora_a", lora_a, (n, r, K)), ("lora_b", lora_b, (n, N, r))):
+        if t.dtype != torch.bfloat16 or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous bfloat16 {shape} required, got {t.dtype} {tuple(t.shape)}")
+    _check_vec("ids", ids, T, (torch.int32,))
+    _check_vec("scales", scales, n, (torch.float32,))
+    _same_device(x.device, w=w, sw=sw, lora_a=lora_a, lora_b=lora_b, ids=ids, scales=scales, out=out)
+    if out is None:
+        out = torch.empty((T, N), dtype=out_dtype, device=x.device)
+    else:
+        _check_2d("out", out, _FLOATS)
+        if tuple(out.shape) != (T, N):
+            raise ValueError(f"out: expected {(T, N)}, got {tuple(out.shape)}")
+    nbytes = lib.fp8_adapter_linear_workspace(T, N, K, r, n)
+    ws = _workspace(nbytes, x.device, stream)
+    st = lib.fp8_adapter_linear(T, N, K, r, n, _ptr(x), x.stride(0), _ptr(w), _ptr(sw), sw.stride(0), _ptr(lora_a),
+                                _ptr(lora_b), _ptr(ids), _ptr(scales), _ptr(out), _is_fp32(out), out.stride(0),
+                                _ptr(ws), nbytes, _stream(stream))
+    _lib.check("fp8_adapter_linear", st)
+    return out

@@ -435,6 +435,114 @@ fp8_status fp8_unpack_tokens(const uint8_t* msg, int64_t T, int64_t H, int64_t s
 fp8_status fp8_dequant_tokens(const uint8_t* msg, int64_t T, int64_t H, int64_t stride, void* y,
                               int64_t ldy, void* stream);
 
+/*
+ * Layer operators around the FP8 products.  Same conventions as above; a call
+ * that needs scratch memory takes it from the caller as `workspace`, a
+ * 16-byte aligned device buffer of at least the bytes its *_workspace function
+ * returns for the same sizes (-1: sizes the operator does not take; fewer
+ * bytes: FP8_ERR_SHAPE).  It holds nothing between calls.
+ */
+
+/*
+ * fp8_layer_norm - layer norm over the rows of x, and optionally the 1x128
+ * quantization of its result in the same pass:
+ *     mean = sum x / cols,  rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps)
+ *     y = (x - mean) * rstd * weight + bias
+ *  x       [rows][ldx >= cols] of x_dtype (BF16 or FP32)
+ *  weight, bias  [cols] of w_dtype, each optional (NULL: ones / zeros)
+ *  y       [rows][ldy >= cols] of x_dtype, rounded once; optional if q is set
+ *  mean, rstd  optional FP32 [rows] (the backward pass reads them)
+ *  q, scales   optional (both or neither): the codes [rows][ldq >= cols] and the
+ *          scales [cols/128][ld_s >= rows] of y's 1x128 row tiles, in the
+ *          operand layout of fp8_quant_act_1x128 ROW, formed from the FP32
+ *          values of y (not from BF16-rounded ones) by the same rule; the
+ *          quotient y / s may differ from the IEEE one by one FP32 ulp.
+ *          Requires cols % 128 == 0 and 16-byte aligned rows and vectors.
+ *  Without q any alignment to the element size and any cols up to 16384 is
+ *  taken (longer rows: FP8_ERR_UNSUPPORTED).  eps >= 0 (otherwise
+ *  FP8_ERR_SHAPE).  No output may overlap an input or another output.
+ *  Sums are FP32 in a fixed order.  rows == 0 or cols == 0 is a no-op.
+ */
+fp8_status fp8_layer_norm(const void* x, int64_t rows, int64_t cols, int64_t ldx, fp8_out_dtype x_dtype,
+                          const void* weight, const void* bias, fp8_out_dtype w_dtype, float eps, void* y,
+                          int64_t ldy, float* mean, float* rstd, uint8_t* q, int64_t ldq, float* scales,
+                          int64_t ld_s, void* stream);
+
+/*
+ * fp8_layer_norm_backward - gradients of fp8_layer_norm's y:
+ *     xhat = (x - mean) * rstd,  g = dy * weight
+ *     dx = rstd * (g - sum g / cols - xhat * sum(g * xhat) / cols)
+ *     dweight = sum over rows of dy * xhat,  dbias = sum over rows of dy
+ *  dy, x, dx  [rows][ld >= cols] of x_dtype; mean, rstd as the forward wrote them
+ *  dweight, dbias  FP32 [cols], each optional (NULL); rows == 0 writes zeros
+ *  Limits and alignment as for fp8_layer_norm without q.  The column sums are
+ *  FP32 in a fixed order: results repeat bit for bit.
+ */
+fp8_status fp8_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, int64_t rows,
+                                   int64_t cols, fp8_out_dtype x_dtype, const float* mean, const float* rstd,
+                                   const void* weight, fp8_out_dtype w_dtype, void* dx, int64_t lddx,
+                                   float* dweight, float* dbias, void* workspace, int64_t workspace_bytes,
+                                   void* stream);
+int64_t fp8_layer_norm_backward_workspace(int64_t rows, int64_t cols);
+
+/*
+ * fp8_moe_few_tokens - a whole mixture-of-experts layer for up to 64 tokens
+ * (a decode batch): router, choice of top_k experts, FP8 gate and up
+ * products, SiLU, FP8 down product, weighted sum.
+ *     l = x . router^T                                  (E logits, FP32)
+ *     score = softmax(l) or sigmoid(l)
+ *     chosen: the top_k largest l, or with `bias` the top_k largest score + bias
+ *             (equal values: the lower index; NaN counts as the smallest)
+ *     g_j = score_j [/ sum of the chosen scores if normalize] * gate_scale
+ *     a = W1_e Xq, u = W3_e Xq;  h = a * sigmoid(a) * u     (FP32)
+ *     y = sum over the chosen experts held here of g_j * (W2_e Hq)
+ *  Xq and Hq are the 1x128 online quantizations of x (BF16 in) and of h (FP32
+ *  in, not rounded to BF16 between).  Experts [first, first + local) of the E
+ *  routed ones are held here; the others' contributions are left out (a
+ *  token with none gets zeros), so that shares add up over GPUs.
+ *  x       BF16 [T][ldx >= H], T <= 64;  router  BF16 [E][ld_r >= H]
+ *  bias    optional FP32 [E], only with FP8_MOE_SIGMOID
+ *  w13     operand-tiled codes of [local][2 I][H]: expert by expert, the I gate
+ *          rows (W1) then the I up rows (W3); s13 FP32 [local][2 I/128][H/128]
+ *  w2      operand-tiled codes of [local][H][I]; s2 FP32 [local][H/128][I/128]
+ *          (fp8_quant_weight_128x128_tiled's outputs, contiguous)
+ *  y       [T][ldy >= H], BF16 or FP32
+ *  ids, gates  optional int32 / FP32 [T][top_k]: the chosen experts (best first) and g_j
+ *  H % 128 == 0, I % 128 == 0, 1 <= top_k <= min(16, E), E <= 1024; rows of x,
+ *  router and y 16-byte aligned.  T > 64: FP8_ERR_UNSUPPORTED (use the
+ *  quantizer and fp8_block_gemm_grouped).  T == 0 is a no-op.
+ */
+typedef enum { FP8_MOE_SOFTMAX = 0, FP8_MOE_SIGMOID = 1 } fp8_moe_gate;
+fp8_status fp8_moe_few_tokens(int64_t T, int64_t H, int64_t I, int32_t E, int32_t first, int32_t local,
+                              int32_t top_k, const void* x, int64_t ldx, const void* router, int64_t ld_r,
+                              const float* bias, fp8_moe_gate gate, int normalize, float gate_scale,
+                              const uint8_t* w13, const float* s13, const uint8_t* w2, const float* s2, void* y,
+                              fp8_out_dtype y_dtype, int64_t ldy, int32_t* ids, float* gates, void* workspace,
+                              int64_t workspace_bytes, void* stream);
+int64_t fp8_moe_few_tokens_workspace(int64_t T, int64_t H, int64_t I, int32_t E, int32_t local, int32_t top_k);
+
+/*
+ * fp8_adapter_linear - a shared FP8 projection with a low-rank adapter of its
+ * own for every token (a batch of requests that use different adapters):
+ *     C[t] = W_q . quant_1x128(x[t]) + scales[a] * B_a . (A_a . x[t]),  a = ids[t]
+ *  x       BF16 [T][ldx >= K];  any T: one token to a batch of prompts
+ *  W       operand-tiled codes of [N][K], sW FP32 [N/128][ld_sw >= K/128]
+ *  A, B    BF16 [adapters][rank][K] and [adapters][N][rank], contiguous
+ *  ids     int32 [T]; a negative id has no adapter, an id >= adapters gives a
+ *          row of NaN
+ *  scales  optional FP32 [adapters] (NULL: ones)
+ *  C       [T][ldc >= N], BF16 or FP32, rounded once from FP32 sums
+ *  N % 128 == 0, K % 128 == 0, rank % 8 == 0, rank <= 128.  Rows 16-byte
+ *  aligned.  Limits as for fp8_block_gemm.  Above 64 tokens the projection
+ *  runs on fp8_block_gemm's persistent kernel (and its per-stream workspace).
+ */
+fp8_status fp8_adapter_linear(int64_t T, int64_t N, int64_t K, int32_t rank, int32_t adapters, const void* x,
+                              int64_t ldx, const uint8_t* W, const float* sW, int64_t ld_sw, const void* A,
+                              const void* B, const int32_t* ids, const float* scales, void* C,
+                              fp8_out_dtype c_dtype, int64_t ldc, void* workspace, int64_t workspace_bytes,
+                              void* stream);
+int64_t fp8_adapter_linear_workspace(int64_t T, int64_t N, int64_t K, int32_t rank, int32_t adapters);
+
 /* Static string naming a status; never NULL. */
 const char* fp8_status_string(fp8_status s);
 

@@ -1,0 +1,542 @@
+"""The layer operators on the GPU against their FP64 definitions
+(oracle/layers.py).
+
+Tolerances, all derived from the arithmetic (u = 2^-24, a BF16 result adds at
+most half a BF16 ulp, 2^-9 of its value, taken as 2^-8):
+ - layer norm: a row sum passes at most 32 additions in a lane, 6 across the
+   lanes of a wave and 8 across waves, so mean and variance are within 64 u of
+   the sums of magnitudes; y and dx combine them in a few more roundings.
+ - dweight / dbias: at most `rows` additions and a few merges per column.
+ - products of codes: FP32 sums, plus the FP8 MFMA's truncation at 2^-12 of
+   each 8-product group's largest magnitude (at most 2^-9 of the sum of
+   magnitudes; normwise 1e-3 as for the block GEMM).
+ - codes formed from FP32 values: equal to the FP64 ones except where the
+   quotient lies within its own error of a rounding boundary.
+"""
+import numpy as np
+import pytest
+import torch
+
+import synthetic as syn
+from oracle import e4m3, layers, quant, tiling
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+def bf16_dev(bits):
+    return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).cuda().view(torch.bfloat16)
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def rand(shape, seed, dtype, mean=0.0, std=1.0):
+    g = np.random.default_rng(seed)
+    return torch.from_numpy((mean + std * g.standard_normal(shape)).astype(np.float32)).to(dtype).cuda()
+
+
+def out_ulp(dtype):
+    return 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -23
+
+
+# ------------------------------------------------------------- layer norm
+
+def norm_tolerance(x, w, b, mean, rstd, dtype, y):
+    w = np.ones(x.shape[1]) if w is None else np.abs(w)
+    b = np.zeros(x.shape[1]) if b is None else np.abs(b)
+    dmean = 64 * U * np.abs(x).mean(axis=1, keepdims=True)
+    d = np.abs(x - mean[:, None])
+    drstd = 72 * U + 0.5 * (dmean * rstd[:, None]) ** 2     # a mean off by dmean adds its square to the variance
+    t = rstd[:, None] * w * (dmean + drstd * (d + dmean)) + 4 * U * b
+    return t + out_ulp(dtype) * np.abs(y)
+
+
+def check_norm(fp8, x, w, b, eps=1e-5, out=None):
+    y, mean, rstd = fp8.layer_norm(x, w, b, eps=eps, return_stats=True, out=out)
+    X = host(x)
+    W = None if w is None else host(w)
+    B = None if b is None else host(b)
+    R, M, S = layers.layer_norm(X, W, B, eps)
+    assert y.dtype == x.dtype and mean.dtype == rstd.dtype == torch.float32
+    assert (np.abs(host(mean) - M) <= 64 * U * np.abs(X).mean(axis=1) + U).all()
+    assert (np.abs(host(rstd) - S) <= (72 * U + 0.5 * (64 * U * np.abs(X).mean(axis=1) * S) ** 2) * S).all()
+    tol = norm_tolerance(X, W, B, M, S, x.dtype, R)
+    err = np.abs(host(y) - R)
+    assert (err <= tol).all(), (tuple(x.shape), float((err / tol).max()))
+    return y
+
+
+COLS = [1, 2, 7, 8, 64, 127, 128, 129, 512, 520, 1000, 1024, 1025, 2048, 2056, 4096, 5001, 7168, 8200, 16384]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("cols", COLS)
+def test_layer_norm_forward(gpu_lib, cols, dtype):
+    rows = 37 if cols <= 1024 else 5
+    x = rand((rows, cols), 1, DT[dtype], mean=0.3)
+    w, b = rand(cols, 2, torch.float32, mean=1.0), rand(cols, 3, torch.float32)
+    check_norm(gpu_lib, x, w, b)
+
+
+@pytest.mark.parametrize("w_dtype,has_w,has_b", [("bf16", True, True), ("bf16", True, False), ("fp32", False, True),
+                                                 ("fp32", False, False)])
+def test_layer_norm_affine_types(gpu_lib, w_dtype, has_w, has_b):
+    x = rand((19, 768), 4, torch.bfloat16)
+    w = rand(768, 5, DT[w_dtype]) if has_w else None
+    b = rand(768, 6, DT[w_dtype]) if has_b else None
+    check_norm(gpu_lib, x, w, b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_layer_norm_strides_and_unaligned_bases(gpu_lib, dtype):
+    big = rand((23, 1030), 7, DT[dtype])
+    w = rand(1000, 8, torch.float32)
+    for off in (0, 1, 3, 8):
+        x = big[:, off:off + 1000]
+        out = torch.full((23, 1040), 7.0, dtype=DT[dtype], device="cuda")
+        check_norm(gpu_lib, x, w, None, out=out[:, 5:1005])
+        assert (out[:, :5] == 7).all() and (out[:, 1005:] == 7).all()   # nothing outside the view is written
+
+
+def test_layer_norm_hard_rows(gpu_lib):
+    x = rand((8, 4096), 9, torch.float32)
+    x[1] = 3.0                      # no variance: y = bias
+    x[2] = x[2] * 1e-3 + 1e3        # a mean a million standard deviations away
+    x[3] *= 1e15                    # squares near FP32's range
+    x[4, 5] = 2e4                   # one outlier
+    x[6] = 0
+    b = rand(4096, 10, torch.float32)
+    y = check_norm(gpu_lib, x, None, b)
+    assert torch.equal(y[1], b) and torch.equal(y[6], b)
+
+
+def test_layer_norm_nonfinite_rows_stay_apart(gpu_lib):
+    x = rand((9, 640), 11, torch.bfloat16)
+    clean = gpu_lib.layer_norm(x)
+    x[3, 17] = float("nan")
+    x[7, 639] = float("inf")
+    y, mean, rstd = gpu_lib.layer_norm(x, return_stats=True)
+    keep = [i for i in range(9) if i not in (3, 7)]
+    assert torch.equal(y[keep], clean[keep])
+    assert torch.isnan(y[3]).all() and torch.isnan(y[7]).all()
+    assert torch.isnan(mean[3]) and mean[7] == float("inf")
+
+
+def test_layer_norm_empty(gpu_lib):
+    assert gpu_lib.layer_norm(torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")).shape == (0, 64)
+    dx, dw, db = gpu_lib.layer_norm_backward(*(torch.empty(0, 72, device="cuda"),) * 2,
+                                             *(torch.empty(0, device="cuda"),) * 2)
+    assert dx.shape == (0, 72) and (dw == 0).all() and (db == 0).all()
+
+
+def codes_match(q, s, Y, dY):
+    """Codes and scales of an FP32 result against FP64 values Y, known to
+    within dY: exact but where a quotient is within its error of a boundary."""
+    qo, so, quot = layers.quant_tiles(Y)
+    tile = lambda a: np.repeat(a, 128, axis=1)
+    dmax = dY.reshape(dY.shape[0], -1, 128).max(axis=2)
+    sg = host(s)[:, :Y.shape[0]].T
+    assert (np.abs(sg - so) <= dmax / 448.0 + 2 * U * so).all()
+    dq = (dY + tile(dmax) * np.abs(quot) / 448.0) / tile(so.astype(np.float64)) + 4 * U * np.abs(quot)
+    near = layers.midpoint_distance(quot) <= dq
+    got, want = e4m3.decode(q.cpu().numpy()), e4m3.decode(qo)
+    differ = got != want
+    assert not (differ & ~near).any(), int((differ & ~near).sum())
+    assert (np.abs(got - want)[differ] <= layers.code_spacing(quot)[differ] * 1.001).all()
+    assert differ.mean() < 1e-3
+
+
+@pytest.mark.parametrize("rows,cols,dtype", [(1, 128, "bf16"), (50, 128, "fp32"), (33, 512, "bf16"), (7, 1024, "fp32"),
+                                             (6, 2048, "bf16"), (130, 7168, "bf16"), (3, 16384, "fp32")])
+def test_layer_norm_quant(gpu_lib, rows, cols, dtype):
+    x = rand((rows, cols), 12, DT[dtype])
+    w, b = rand(cols, 13, torch.bfloat16, mean=1.0, std=0.2), rand(cols, 14, torch.bfloat16, std=0.1)
+    q, s, y, mean, rstd = gpu_lib.layer_norm_quant(x, w, b, return_y=True, return_stats=True)
+    y2, mean2, rstd2 = gpu_lib.layer_norm(x, w, b, return_stats=True)
+    assert torch.equal(y, y2) and torch.equal(mean, mean2) and torch.equal(rstd, rstd2)
+    assert s.shape == (cols // 128, (rows + 3) // 4 * 4)
+    R, M, S = layers.layer_norm(host(x), host(w), host(b))
+    codes_match(q, s, R, norm_tolerance(host(x), host(w), host(b), M, S, torch.float32, R))
+    if dtype == "fp32":   # then y is the FP32 result itself, so the tile maxima are its own
+        amax = y.abs().view(rows, cols // 128, 128).amax(dim=2)
+        assert torch.equal(s[:, :rows].t(), (amax / torch.full_like(amax, 448.0)).clamp_min(1e-12))
+
+
+def test_layer_norm_quant_nonfinite_and_zero_tiles(gpu_lib):
+    x = rand((4, 256), 15, torch.float32)
+    w, b = torch.ones(256, device="cuda"), torch.zeros(256, device="cuda")
+    w[:128] = 0.0                     # the first tile of every row is the bias
+    b[7] = float("inf")
+    x[2, 200] = float("nan")
+    q, s = gpu_lib.layer_norm_quant(x, w, b)
+    q, s = q.cpu().numpy(), s.cpu().numpy()
+    for r in (0, 1, 3):
+        assert np.isinf(s[0, r]) and q[r, 7] == 0x7F          # Inf / Inf
+        assert ((np.delete(q[r, :128], 7) & 0x7F) == 0).all()   # finite / Inf
+        assert np.isfinite(s[1, r]) and s[1, r] > 0
+    assert np.isnan(s[:, 2]).all() and (q[2] == 0x7F).all()
+    b[7] = 0.0
+    q, s = gpu_lib.layer_norm_quant(x, w, b)
+    assert s[0, 0].item() == np.float32(1e-12) and ((q[0, :128] & 0x7F) == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (5, 7), (300, 64), (777, 128), (40, 500), (67, 1000), (33, 1024), (600, 2047),
+                                       (21, 4096), (530, 7168), (9, 8200), (3, 16384)])
+def test_layer_norm_backward(gpu_lib, rows, cols, dtype):
+    x, dy = rand((rows, cols), 16, DT[dtype], mean=0.2), rand((rows, cols), 17, DT[dtype], std=1e-2)
+    w = rand(cols, 18, torch.float32, mean=1.0)
+    _, mean, rstd = gpu_lib.layer_norm(x, w, return_stats=True)
+    dx, dw, db = gpu_lib.layer_norm_backward(dy, x, mean, rstd, w)
+    assert dx.dtype == x.dtype and dw.dtype == db.dtype == torch.float32
+    X, D, W, M, S = host(x), host(dy), host(w), host(mean), host(rstd)
+    RX, RW, RB = layers.layer_norm_backward(D, X, M, S, W)
+    xh, g = np.abs((X - M[:, None]) * S[:, None]), np.abs(D * W)
+    mg, mgx = g.mean(axis=1, keepdims=True), (g * xh).mean(axis=1, keepdims=True)
+    tol = 72 * U * S[:, None] * (g + mg + xh * mgx) + out_ulp(x.dtype) * np.abs(RX)
+    assert (np.abs(host(dx) - RX) <= tol).all(), float((np.abs(host(dx) - RX) / tol).max())
+    n = rows + 8
+    assert (np.abs(host(dw) - RW) <= n * U * (np.abs(D) * xh).sum(axis=0) + 1e-30).all()
+    assert (np.abs(host(db) - RB) <= n * U * np.abs(D).sum(axis=0) + 1e-30).all()
+    again = gpu_lib.layer_norm_backward(dy, x, mean, rstd, w)
+    assert all(torch.equal(a, b) for a, b in zip(again, (dx, dw, db)))
+
+
+def test_layer_norm_backward_against_differences(gpu_lib):
+    """dx, dweight and dbias against central differences of the FP64 forward."""
+    x, dy = rand((6, 24), 19, torch.float32), rand((6, 24), 20, torch.float32)
+    w, b = rand(24, 21, torch.float32, mean=1.0), rand(24, 22, torch.float32)
+    _, mean, rstd = gpu_lib.layer_norm(x, w, b, return_stats=True)
+    dx, dw, db = (host(t) for t in gpu_lib.layer_norm_backward(dy, x, mean, rstd, w))
+    X, D, W, B = host(x), host(dy), host(w), host(b)
+    loss = lambda X_, W_, B_: (D * layers.layer_norm(X_, W_, B_)[0]).sum(axis=1)
+    h = 1e-5
+    for c in range(24):
+        e = np.zeros(24)
+        e[c] = h
+        # truncation h^2 times third derivatives of order 10, FP64 rounding 1e-16 / h, FP32 results
+        assert np.allclose((loss(X + e, W, B) - loss(X - e, W, B)) / (2 * h), dx[:, c], atol=2e-5, rtol=2e-5)
+        assert np.isclose((loss(X, W + e, B) - loss(X, W - e, B)).sum() / (2 * h), dw[c], atol=2e-5, rtol=2e-5)
+        assert np.isclose((loss(X, W, B + e) - loss(X, W, B - e)).sum() / (2 * h), db[c], atol=2e-5, rtol=2e-5)
+
+
+def test_layer_norm_backward_strides_and_one_output(gpu_lib):
+    big_x, big_d = rand((31, 410), 23, torch.bfloat16), rand((31, 403), 24, torch.bfloat16)
+    x, dy = big_x[:, 3:403], big_d[:, 1:401]
+    _, mean, rstd = gpu_lib.layer_norm(x, return_stats=True)
+    got = gpu_lib.layer_norm_backward(dy, x, mean, rstd)
+    want = gpu_lib.layer_norm_backward(dy.contiguous(), x.contiguous(), mean, rstd)
+    for a, b in zip(got, want):
+        # the aligned form adds the columns of a lane in another order
+        assert torch.allclose(a.double(), b.double(), rtol=2.0 ** -7, atol=1e-5)
+
+
+# ------------------------------------------------------------- experts
+
+def tile_codes(q):
+    return tiling.tile_codes(q).reshape(q.shape)
+
+
+def make_experts(local, H, I, seed):
+    w13 = [quant.quant_weight(syn.gaussian((2 * I, H), seed=seed + 2 * e, std=0.05)) for e in range(local)]
+    w2 = [quant.quant_weight(syn.gaussian((H, I), seed=seed + 2 * e + 1, std=0.05)) for e in range(local)]
+    d = dict(w13=dev(np.stack([tile_codes(q) for q, _ in w13])), s13=dev(np.stack([s for _, s in w13])),
+             w2=dev(np.stack([tile_codes(q) for q, _ in w2])), s2=dev(np.stack([s for _, s in w2])))
+    return w13, w2, d
+
+
+def check_moe(y, Y, mag, slack, out_dtype=torch.bfloat16):
+    got = host(y)
+    tol = out_ulp(out_dtype) * np.abs(Y) + 2.0 ** -9 * mag + slack
+    err = np.abs(got - Y)
+    assert (err <= tol).all(), float((err / np.maximum(tol, 1e-300)).max())
+    if np.abs(Y).max() > 0:
+        # half a BF16 ulp (2^-9 of each value), the products' 1e-3, and moved codes
+        allowed = (2.0 ** -9 if out_dtype == torch.bfloat16 else 0) + 1e-3 + np.linalg.norm(slack) / np.linalg.norm(Y)
+        assert np.linalg.norm(got - Y) <= allowed * np.linalg.norm(Y)
+
+
+MOE = [  # T, H, I, E, first, local, k, gate, bias, normalize
+    (1, 128, 128, 2, 0, 2, 1, "softmax", False, True),
+    (1, 1024, 384, 8, 0, 8, 8, "softmax", False, True),
+    (3, 512, 256, 7, 2, 3, 2, "sigmoid", False, True),
+    (16, 256, 128, 16, 0, 16, 4, "sigmoid", True, True),
+    (17, 384, 640, 5, 0, 5, 3, "softmax", False, False),
+    (33, 256, 256, 70, 60, 10, 6, "sigmoid", True, True),
+    (64, 512, 128, 4, 0, 4, 4, "softmax", False, True),
+    (64, 128, 256, 130, 1, 64, 16, "softmax", False, True),
+]
+
+
+@pytest.mark.parametrize("case", MOE, ids=[f"T{c[0]}-H{c[1]}-I{c[2]}-E{c[3]}-k{c[6]}" for c in MOE])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_moe_few_tokens(gpu_lib, case, out_dtype):
+    T, H, I, E, first, local, k, gate, has_bias, normalize = case
+    xb = syn.activation_with_outliers(T, H, seed=31)
+    rb = syn.gaussian((E, H), seed=32, std=H ** -0.5)
+    bias = np.random.default_rng(33).standard_normal(E).astype(np.float32) * 0.05 if has_bias else None
+    w13, w2, d = make_experts(local, H, I, 40)
+    R = quant.bf16_to_f32(rb).astype(np.float64)
+    routing = dict(gate=gate, bias=bias, normalize=normalize, scale=1.5)
+    y, ids_g, gates_g = gpu_lib.moe_few_tokens(bf16_dev(xb), bf16_dev(rb), **d, top_k=k, gate=gate,
+                                               bias=None if bias is None else dev(bias), normalize=normalize, scale=1.5,
+                                               first_expert=first, return_routing=True, out_dtype=out_dtype)
+    # FP32 logits are within 2^-18 of their magnitude (fewer than 64 roundings):
+    # only experts whose values lie that near may change places
+    ids_g = ids_g.cpu().numpy()
+    X = quant.bf16_to_f32(xb).astype(np.float64)
+    dl = 2.0 ** -18 * (np.abs(X) @ np.abs(R).T).max()
+    ids, _ = layers.route(X @ R.T, k, **routing)
+    value = X @ R.T if bias is None else 1 / (1 + np.exp(-(X @ R.T))) + bias
+    assert (np.abs(np.take_along_axis(value, ids_g, 1) - np.take_along_axis(value, ids, 1)) <= 2 * dl + 4 * U).all()
+    assert all(len(set(r)) == k for r in ids_g)
+    Y, _, gates, mag, slack = layers.moe(xb, R, w13, w2, k, first, ids=ids_g, **routing)
+    # a score moves by the logits' error, relative to itself, and so does the sum that divides it
+    assert (np.abs(host(gates_g) - gates) <= (4 * dl + 32 * U) * np.abs(gates)).all()
+    check_moe(y, Y, mag + (4 * dl + 32 * U) * 2.0 ** 9 * mag, slack, out_dtype)
+    y2 = gpu_lib.moe_few_tokens(bf16_dev(xb), bf16_dev(rb), **d, top_k=k, gate=gate,
+                                bias=None if bias is None else dev(bias), normalize=normalize, scale=1.5,
+                                first_expert=first, out_dtype=out_dtype)
+    assert torch.equal(y, y2)
+
+
+def test_moe_ties_go_to_the_lowest_index(gpu_lib):
+    T, H, I, E, k = 5, 128, 128, 9, 4
+    xb = syn.gaussian((T, H), seed=50)
+    rb = syn.gaussian((E, H), seed=51, std=0.1)
+    rb[:] = rb[0]                               # nine equal experts
+    _, _, d = make_experts(E, H, I, 52)
+    _, ids, gates = gpu_lib.moe_few_tokens(bf16_dev(xb), bf16_dev(rb), **d, top_k=k, return_routing=True)
+    assert (ids.cpu().numpy() == np.arange(k)).all()
+    assert np.allclose(host(gates), 0.25, rtol=1e-6)
+    rb[4:] = 0                                   # logits 0 and -0
+    xb0 = xb & np.uint16(0x8000)                 # x = +-0
+    _, ids, _ = gpu_lib.moe_few_tokens(bf16_dev(xb0), bf16_dev(rb), **d, top_k=k, return_routing=True)
+    assert (ids.cpu().numpy() == np.arange(k)).all()
+
+
+def test_moe_tokens_without_a_held_expert_get_zeros(gpu_lib):
+    T, H, I, E = 6, 256, 128, 12
+    xb = syn.gaussian((T, H), seed=60)
+    rb = syn.gaussian((E, H), seed=61, std=0.2)
+    w13, w2, d = make_experts(1, H, I, 62)
+    R = quant.bf16_to_f32(rb).astype(np.float64)
+    for first in range(E):
+        Y, ids, _, mag, slack = layers.moe(xb, R, w13, w2, 2, first)
+        y = gpu_lib.moe_few_tokens(bf16_dev(xb), bf16_dev(rb), **d, top_k=2, first_expert=first,
+                                   out=torch.full((T, H), float("nan"), dtype=torch.bfloat16, device="cuda"))
+        none = ~(ids == first).any(axis=1)
+        assert (host(y)[none] == 0).all() and not np.isnan(host(y)).any()
+        check_moe(y, Y, mag * 1.01, slack)
+
+
+def test_moe_nonfinite_tokens_stay_apart(gpu_lib):
+    T, H, I, E, k = 20, 256, 128, 6, 2
+    xb = syn.gaussian((T, H), seed=70)
+    rb = syn.gaussian((E, H), seed=71, std=0.1)
+    _, _, d = make_experts(E, H, I, 72)
+    clean = gpu_lib.moe_few_tokens(bf16_dev(xb), bf16_dev(rb), **d, top_k=k)
+    bad = xb.copy()
+    bad[3, 9] = 0x7FC0
+    bad[18, 200] = 0x7F80
+    y, ids, _ = gpu_lib.moe_few_tokens(bf16_dev(bad), bf16_dev(rb), **d, top_k=k, return_routing=True)
+    keep = [t for t in range(T) if t not in (3, 18)]
+    assert torch.equal(y[keep], clean[keep])
+    assert torch.isnan(y[3]).all() and torch.isnan(y[18]).all()
+    i = ids.cpu().numpy()
+    assert (i[3] == [0, 1]).all()                # NaN logits: the lowest indexes
+    assert ((i >= 0) & (i < E)).all() and all(len(set(r)) == k for r in i)
+
+
+def test_moe_strided_rows_and_another_stream(gpu_lib):
+    T, H, I, E, k = 9, 256, 256, 4, 2
+    xb, rb = syn.gaussian((T, H), seed=80), syn.gaussian((E, H), seed=81, std=0.1)
+    _, _, d = make_experts(E, H, I, 82)
+    x, r = bf16_dev(xb), bf16_dev(rb)
+    want = gpu_lib.moe_few_tokens(x, r, **d, top_k=k)
+    xs = torch.zeros(T, H + 24, dtype=torch.bfloat16, device="cuda")
+    rs = torch.zeros(E, H + 8, dtype=torch.bfloat16, device="cuda")
+    xs[:, 8:8 + H], rs[:, :H] = x, r
+    out = torch.full((T, H + 16), 3.0, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    gpu_lib.moe_few_tokens(xs[:, 8:8 + H], rs[:, :H], **d, top_k=k, out=out[:, 8:8 + H], stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(out[:, 8:8 + H], want)
+    assert (out[:, :8] == 3).all() and (out[:, 8 + H:] == 3).all()
+
+
+# ------------------------------------------------------------- adapters
+
+def make_adapters(N, K, n, r, seed):
+    wq, ws = quant.quant_weight(syn.gaussian((N, K), seed=seed, std=0.02))
+    A, B = syn.gaussian((n, r, K), seed=seed + 1, std=K ** -0.5), syn.gaussian((n, N, r), seed=seed + 2, std=0.1)
+    sc = (0.5 + np.random.default_rng(seed + 3).random(n)).astype(np.float32)
+    return wq, ws, A, B, sc
+
+
+def check_adapters(y, Y, mag, low, out_dtype=torch.bfloat16):
+    got = host(y)
+    ok = ~np.isnan(Y).any(axis=1)
+    assert np.isnan(got[~ok]).all()
+    got, Y, mag, low = got[ok], Y[ok], mag[ok], low[ok]
+    err = np.abs(got - Y)
+    # the adapter's sums keep z to 2^-17 and add K + r products in FP32
+    tol = out_ulp(out_dtype) * np.abs(Y) + 2.0 ** -9 * mag + 2.0 ** -16 * low
+    assert (err <= tol).all(), float((err / tol).max())
+    bound = (2.0 ** -9 if out_dtype == torch.bfloat16 else 0.0) + 1e-3
+    assert np.linalg.norm(err) <= bound * np.linalg.norm(Y)
+
+
+ADAPTERS = [  # T, N, K, n, r, ids
+    (1, 128, 128, 1, 8, "one"), (1, 384, 1024, 4, 16, "one"), (5, 256, 384, 3, 24, "mixed"),
+    (16, 128, 256, 16, 64, "distinct"), (17, 256, 512, 2, 128, "mixed"), (48, 384, 256, 48, 32, "distinct"),
+    (64, 256, 128, 5, 40, "mixed"), (65, 256, 128, 5, 40, "mixed"), (130, 384, 640, 4, 16, "segments"),
+    (300, 640, 256, 7, 56, "mixed"), (513, 256, 384, 3, 8, "none"), (257, 128, 128, 300, 16, "distinct"),
+]
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("case", ADAPTERS, ids=[f"T{c[0]}-N{c[1]}-K{c[2]}-r{c[4]}-{c[5]}" for c in ADAPTERS])
+def test_adapter_linear(gpu_lib, case, out_dtype):
+    T, N, K, n, r, kind = case
+    wq, ws, A, B, sc = make_adapters(N, K, n, r, 90)
+    xb = syn.activation_with_outliers(T, K, seed=91)
+    g = np.random.default_rng(92)
+    ids = {"one": np.full(T, n - 1), "mixed": g.integers(-1, n, T), "distinct": g.permutation(max(n, T))[:T] % n,
+           "segments": np.repeat(g.integers(-1, n, (T + 49) // 50), 50)[:T], "none": np.full(T, -1)}[kind].astype(np.int32)
+    f64 = lambda bits: quant.bf16_to_f32(bits).astype(np.float64)
+    Y, mag, low = layers.adapters(xb, wq, ws, f64(A), f64(B), ids, sc)
+    args = (bf16_dev(xb), dev(tile_codes(wq)), dev(ws), bf16_dev(A), bf16_dev(B), dev(ids))
+    y = gpu_lib.adapter_linear(*args, scales=dev(sc), out_dtype=out_dtype)
+    check_adapters(y, Y, mag, low, out_dtype)
+    assert torch.equal(y, gpu_lib.adapter_linear(*args, scales=dev(sc), out_dtype=out_dtype))
+    if kind == "none" and out_dtype == torch.bfloat16:
+        q, s, _ = gpu_lib.quant_act_1x128(args[0])
+        assert torch.equal(y, gpu_lib.block_gemm("fprop_tiled", q, s, args[1], args[2]))
+
+
+@pytest.mark.parametrize("T", [20, 100])
+def test_adapter_linear_ids_past_the_last_and_nonfinite_tokens(gpu_lib, T):
+    N, K, n, r = 256, 256, 3, 16
+    wq, ws, A, B, _ = make_adapters(N, K, n, r, 95)
+    xb = syn.gaussian((T, K), seed=96)
+    ids = np.arange(T, dtype=np.int32) % n
+    args = lambda xb_, ids_: (bf16_dev(xb_), dev(tile_codes(wq)), dev(ws), bf16_dev(A), bf16_dev(B), dev(ids_))
+    clean = gpu_lib.adapter_linear(*args(xb, ids))
+    ids2, bad = ids.copy(), xb.copy()
+    ids2[4], ids2[5], ids2[6] = n, 2 ** 31 - 1, -(2 ** 31)
+    bad[7, 3] = 0x7FC0
+    bad[8, 3] = 0xFF80
+    y = gpu_lib.adapter_linear(*args(bad, ids2))
+    keep = [t for t in range(T) if t not in (4, 5, 6, 7, 8)]
+    assert torch.equal(y[keep], clean[keep])
+    assert torch.isnan(y[4]).all() and torch.isnan(y[5]).all() and torch.isnan(y[7]).all()
+    assert torch.isnan(y[8]).any() and not torch.isnan(y[6]).any()
+
+
+@pytest.mark.parametrize("T", [3, 90])
+def test_adapter_linear_strided_rows_and_another_stream(gpu_lib, T):
+    N, K, n, r = 256, 384, 2, 32
+    wq, ws, A, B, sc = make_adapters(N, K, n, r, 97)
+    x = bf16_dev(syn.gaussian((T, K), seed=98))
+    ids = dev(np.arange(T, dtype=np.int32) % n)
+    rest = (dev(tile_codes(wq)), dev(ws), bf16_dev(A), bf16_dev(B), ids)
+    want = gpu_lib.adapter_linear(x, *rest, scales=dev(sc))
+    wide = torch.zeros(T, K + 40, dtype=torch.bfloat16, device="cuda")
+    wide[:, 16:16 + K] = x
+    out = torch.full((T, N + 8), 3.0, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    scd = dev(sc)
+    side.wait_stream(torch.cuda.current_stream())
+    gpu_lib.adapter_linear(wide[:, 16:16 + K], *rest, scales=scd, out=out[:, :N], stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(out[:, :N], want) and (out[:, N:] == 3).all()
+
+
+# ------------------------------------------------------------- graphs, refusals
+
+def test_operators_replay_from_a_graph(gpu_lib):
+    """Captured once, replayed with new inputs, each replay against an eager call."""
+    T, H, I, E, n, r = 7, 256, 128, 4, 3, 16
+    _, _, d = make_experts(E, H, I, 100)
+    wq, ws, A, B, _ = make_adapters(H, H, n, r, 101)
+    rest = (dev(tile_codes(wq)), dev(ws), bf16_dev(A), bf16_dev(B), dev(np.arange(T, dtype=np.int32) % n))
+    router = bf16_dev(syn.gaussian((E, H), seed=102, std=0.1))
+    x = bf16_dev(syn.gaussian((T, H), seed=103))
+
+    def block(v):
+        y = gpu_lib.layer_norm(v)
+        a = gpu_lib.adapter_linear(y, *rest)
+        m = gpu_lib.moe_few_tokens(a, router, **d, top_k=2)
+        _, mean, rstd = gpu_lib.layer_norm(m, return_stats=True)
+        return (m,) + gpu_lib.layer_norm_backward(a, m, mean, rstd)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        block(x)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = block(x)
+    for seed in (104, 105, 106, 107):
+        x.copy_(bf16_dev(syn.gaussian((T, H), seed=seed)))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, block(x)))
+
+
+def test_refusals(gpu_lib):
+    fp8 = gpu_lib
+    x = rand((4, 256), 1, torch.bfloat16)
+    with pytest.raises(TypeError):
+        fp8.layer_norm(x.half())
+    with pytest.raises(ValueError):
+        fp8.layer_norm(x.t())
+    with pytest.raises(ValueError):
+        fp8.layer_norm(x, torch.ones(255, device="cuda"))
+    with pytest.raises(fp8.FP8Error):
+        fp8.layer_norm(x, eps=-1.0)
+    with pytest.raises(fp8.FP8Error):
+        fp8.layer_norm(x, out=x)
+    with pytest.raises(fp8.FP8Error):
+        fp8.layer_norm(torch.zeros(1, 16385, device="cuda"))
+    with pytest.raises(fp8.FP8Error):
+        fp8.layer_norm_quant(rand((2, 200), 1, torch.bfloat16))
+    with pytest.raises(fp8.FP8Error):
+        fp8.layer_norm_quant(rand((2, 264), 1, torch.bfloat16)[:, 1:257])
+    with pytest.raises(TypeError):
+        fp8.layer_norm_backward(x.float(), x, *torch.zeros(2, 4, device="cuda"))
+    with pytest.raises(ValueError):
+        fp8.layer_norm_backward(x, x, *torch.zeros(2, 5, device="cuda"))
+    _, _, d = make_experts(2, 256, 128, 110)
+    router = rand((4, 256), 2, torch.bfloat16)
+    with pytest.raises(fp8.FP8Error):
+        fp8.moe_few_tokens(rand((65, 256), 1, torch.bfloat16), router, **d, top_k=2)
+    for bad in (dict(top_k=5), dict(top_k=0), dict(top_k=2, first_expert=3), dict(top_k=2, first_expert=-1),
+                dict(top_k=2, bias=torch.zeros(4, device="cuda"))):
+        with pytest.raises(fp8.FP8Error):
+            fp8.moe_few_tokens(x, router, **d, **bad)
+    with pytest.raises(ValueError):
+        fp8.moe_few_tokens(x, router, **d, top_k=2, gate="other")
+    with pytest.raises(ValueError):
+        fp8.moe_few_tokens(x, router, **dict(d, s2=d["s2"][:1]), top_k=2)
+    wq, ws, A, B, _ = make_adapters(256, 256, 2, 16, 111)
+    rest = [dev(tile_codes(wq)), dev(ws), bf16_dev(A), bf16_dev(B), torch.zeros(4, dtype=torch.int32, device="cuda")]
+    with pytest.raises(ValueError):
+        fp8.adapter_linear(x, *rest[:4], rest[4].long())
+    with pytest.raises(ValueError):
+        fp8.adapter_linear(x, *rest[:4], rest[4][:3])
+    with pytest.raises(fp8.FP8Error):
+        fp8.adapter_linear(x, rest[0], rest[1], bf16_dev(A[:, :12]), bf16_dev(B[:, :, :12]), rest[4])
+    with pytest.raises(ValueError):
+        fp8.adapter_linear(x, rest[0], rest[1], rest[2], rest[3][:, :128].contiguous(), rest[4])
