@@ -96,6 +96,8 @@ def load_library(path: str | None = None):
     A library named by `path` may hold a part of the entry points (a host-only
     build of one file of the ABI); the built library has to have them all."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -179,24 +179,26 @@ __device__ __forceinline__ uint2 quant8_bf16(const uint4& d, float& s) {
 
 // The same rule on a lane's 8 FP32 values, given the tile's |y| max as FP32
 // bits (NaN patterns sort above infinity): s = max(fl32(amax / 448), floor).
-// r = fl32(1 / s) and one Newton-Markstein correction per quotient, three
-// operations in place of a full division; the quotient can be one FP32 ulp
-// from fl32(y / s), 2^-20 of a code's spacing.
+// fl32(amax / 448) is the Markstein form of div448_bf16, which equals the IEEE
+// quotient for every FP32 mantissa (a result below FP32's normal range lies
+// under the floor).  The values were rounded to FP32 themselves, so the
+// quotient is y r with r = 1 / s, within two FP32 ulp of fl32(y / s) (2^-18 of
+// a code's spacing) for a tenth of a division's operations; 448 (1 + 2^-22)
+// still rounds to the code of 448.
 __device__ __forceinline__ uint2 quant8_f32(const float (&y)[8], uint32_t amax_bits, float& s) {
-  uint2 out;
   if (amax_bits < 0x7F800000u) {
-    s = fmaxf(__uint_as_float(amax_bits) / 448.0f, scale_floor());
-    const float r = 1.0f / s;
-    out.x = pack4_sat(div_by_scale(y[0], s, r), div_by_scale(y[1], s, r), div_by_scale(y[2], s, r),
-                      div_by_scale(y[3], s, r));
-    out.y = pack4_sat(div_by_scale(y[4], s, r), div_by_scale(y[5], s, r), div_by_scale(y[6], s, r),
-                      div_by_scale(y[7], s, r));
-  } else {
-    s = __uint_as_float(amax_bits == 0x7F800000u ? amax_bits : kCanonicalNaN);
-    out.x = pack4_sat_nan(y[0] / s, y[1] / s, y[2] / s, y[3] / s);
-    out.y = pack4_sat_nan(y[4] / s, y[5] / s, y[6] / s, y[7] / s);
+    s = fmaxf(div448_bf16(__uint_as_float(amax_bits)), scale_floor());
+    const float r = recip_online(s);
+    int lo = 0, hi = 0;
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] * r, y[1] * r, lo, false);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[2] * r, y[3] * r, lo, true);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[4] * r, y[5] * r, hi, false);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[6] * r, y[7] * r, hi, true);
+    return make_uint2((uint32_t)lo, (uint32_t)hi);
   }
-  return out;
+  s = __uint_as_float(amax_bits == 0x7F800000u ? amax_bits : kCanonicalNaN);
+  return make_uint2(pack4_sat_nan(y[0] / s, y[1] / s, y[2] / s, y[3] / s),
+                    pack4_sat_nan(y[4] / s, y[5] / s, y[6] / s, y[7] / s));
 }
 
 }  // namespace fp8bs

@@ -17,8 +17,11 @@ FP8_DTYPE = torch.uint8
 
 
 def _stream(stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the raw handle: building the Stream object takes longer than a short
+    # kernel's launch (2.8 us against 0.1 us)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ptr(t):
@@ -463,7 +466,7 @@ def _workspace(nbytes: int, device, stream):
     pool; a call on another stream tells the pool, so that the memory is not
     handed out again before that stream is done with it."""
     ws = torch.empty(max(nbytes, 0), dtype=torch.uint8, device=device)   # -1: the call itself refuses
-    if stream is not None and stream != torch.cuda.current_stream(device):
+    if stream is not None and stream.cuda_stream != _stream():
         ws.record_stream(stream)
     return ws
 
@@ -489,7 +492,8 @@ def layer_norm(x: torch.Tensor, weight=None, bias=None, *, eps: float = 1e-5, re
             raise ValueError(f"out: expected {tuple(x.shape)}, got {tuple(out.shape)}")
     mean = rstd = None
     if return_stats:
-        mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=x.device)
+        mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
     st = lib.fp8_layer_norm(_ptr(x), rows, cols, x.stride(0), _is_fp32(x), _ptr(weight), _ptr(bias), wt, eps,
                             _ptr(out), out.stride(0), _ptr(mean), _ptr(rstd), None, 0, None, 0, _stream(stream))
     _lib.check("fp8_layer_norm", st)
@@ -513,7 +517,8 @@ def layer_norm_quant(x: torch.Tensor, weight=None, bias=None, *, eps: float = 1e
     y = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if return_y else None
     mean = rstd = None
     if return_stats:
-        mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=x.device)
+        mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
     st = lib.fp8_layer_norm(_ptr(x), rows, cols, x.stride(0), _is_fp32(x), _ptr(weight), _ptr(bias), wt, eps,
                             _ptr(y), cols, _ptr(mean), _ptr(rstd), _ptr(q), cols, _ptr(s), s.stride(0),
                             _stream(stream))
@@ -539,7 +544,8 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
     _check_vec("rstd", rstd, rows, (torch.float32,))
     _same_device(x.device, dy=dy, mean=mean, rstd=rstd, weight=weight)
     dx = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-    dweight, dbias = torch.empty((2, cols), dtype=torch.float32, device=x.device)
+    dweight = torch.empty(cols, dtype=torch.float32, device=x.device)
+    dbias = torch.empty_like(dweight)
     nbytes = lib.fp8_layer_norm_backward_workspace(rows, cols)
     ws = _workspace(nbytes, x.device, stream)
     st = lib.fp8_layer_norm_backward(_ptr(dy), dy.stride(0), _ptr(x), x.stride(0), rows, cols, _is_fp32(x),
