@@ -294,10 +294,9 @@ fp8_status fp8_adapter_linear(int64_t T, int64_t N, int64_t K, int32_t rank, int
   g.B = W; g.ldb = K; g.sB = sW; g.ld_sb = ld_sw;
   g.C = C; g.ldc = ldc; g.out_fp32 = p.out_fp32;
   g.b_tiled = 1;
+  g.adapters = fp8bs::AdapterEpilogue{ids, p.z, p.B, p.r, p.n};
   fp8bs::attach_gemm_workspace(g, s);
-  err = fp8bs::launch_gemm(g, s);
-  if (err == hipSuccess) err = fp8bs::launch_adapter_expand(p, s);
-  return launched(err);
+  return launched(fp8bs::launch_gemm(g, s));
 }
 
 }  // extern "C"

@@ -13,6 +13,7 @@ namespace fp8bs {
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr uint32_t kCanonicalNaN = 0x7FC00000u;
 constexpr uint32_t kScaleFloorBits = 0x2B8CBCCCu;   // fl32(1e-12)
@@ -199,6 +200,23 @@ __device__ __forceinline__ uint2 quant8_f32(const float (&y)[8], uint32_t amax_b
   s = __uint_as_float(amax_bits == 0x7F800000u ? amax_bits : kCanonicalNaN);
   return make_uint2(pack4_sat_nan(y[0] / s, y[1] / s, y[2] / s, y[3] / s),
                     pack4_sat_nan(y[4] / s, y[5] / s, y[6] / s, y[7] / s));
+}
+
+// One 16x16x32 BF16 MFMA with FP32 accumulation: lane l holds 8 consecutive k
+// (from 8 (l / 16)) of row / column l % 16 of each operand.
+__device__ __forceinline__ v4f mfma_bf16_16x16x32(const v8bf& a, const v8bf& b, const v4f& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// 8 FP32 values as two BF16 terms each, v = hi + lo up to 2^-17 of v: a product
+// with both terms loses nothing that FP32 sums would keep.
+__device__ __forceinline__ void split_bf16(const float (&v)[8], v8bf& hi, v8bf& lo) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    hi[i] = (__bf16)v[i];
+    const float d = v[i] - (float)hi[i];
+    lo[i] = (__bf16)(d == d ? d : 0.f);   // Inf and NaN sit in hi
+  }
 }
 
 }  // namespace fp8bs

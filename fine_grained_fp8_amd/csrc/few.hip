@@ -19,14 +19,10 @@ namespace {
 
 typedef int fv4i __attribute__((ext_vector_type(4)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr int kB = 512;        // threads of every workgroup here
 constexpr int kW = kB / 64;    // waves
 
-__device__ __forceinline__ v4f mfma_bf16_16x16x32(const v8bf& a, const v8bf& b, const v4f& c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
 __device__ __forceinline__ v8bf as_bf16x8(const fv4i& v) { return __builtin_bit_cast(v8bf, v); }
 
 // 8 E4M3 codes (two dwords) as BF16, exactly
@@ -496,17 +492,6 @@ __global__ __launch_bounds__(kB) void adapter_shrink_kernel(AdapterProblem p) {
   shrink_chunk(p, (int64_t)blockIdx.x * 16, blockIdx.y, 0, 1, part);
 }
 
-// 8 values of z as two BF16 terms, z = hi + lo up to 2^-17 of z, so that the
-// expand's products lose nothing that its FP32 sums would keep
-__device__ __forceinline__ void split_bf16(const float* z, v8bf& hi, v8bf& lo) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    hi[i] = (__bf16)z[i];
-    const float d = z[i] - (float)hi[i];
-    lo[i] = (__bf16)(d == d ? d : 0.f);
-  }
-}
-
 // acc += B_a z for 16 output rows (row n0 + l & 15 of adapter a) and 16 tokens
 // (this lane's column: z row `zt`, `on` if its id is a)
 __device__ __forceinline__ v4f expand_add(const AdapterProblem& p, int a, int64_t n0, const float* zt, bool on,
@@ -591,40 +576,6 @@ __global__ __launch_bounds__(kB) void adapter_project_kernel(AdapterProblem p) {
   }
 }
 
-// C += B z for any number of tokens: workgroup of 16 tokens x 512 columns,
-// each wave 64 of them.
-__global__ __launch_bounds__(kB) void adapter_expand_kernel(AdapterProblem p) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lrow = lane & 15, lgrp = lane >> 4;
-  const int64_t t0 = (int64_t)blockIdx.x * 16;
-  const bool in = t0 + lrow < p.T;
-  const int id = in ? p.ids[t0 + lrow] : -1;
-  const float* zt = p.z + (in ? t0 + lrow : t0) * p.r;
-  const uint32_t any = (uint32_t)(__ballot(id >= 0) & 0xFFFFull);
-  if (any == 0) return;
-  for (int i = 0; i < 4; ++i) {
-    const int64_t n0 = (int64_t)blockIdx.y * 512 + wave * 64 + i * 16;
-    if (n0 >= p.N) return;
-    const int64_t at = (t0 + lrow) * p.ldc + n0 + lgrp * 4;
-    v4f acc = {0.f, 0.f, 0.f, 0.f};
-    if (in) {
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        acc[v] = p.out_fp32 ? static_cast<const float*>(p.C)[at + v]
-                            : __uint_as_float((uint32_t) static_cast<const uint16_t*>(p.C)[at + v] << 16);
-    }
-    uint32_t left = any;
-    while (left != 0) {
-      const int a = __shfl(id, __builtin_ctz(left));
-      left &= ~(uint32_t)__ballot(id == a);
-      acc = expand_add(p, a, n0, zt, id == a, lane, acc);
-    }
-    if (in && id >= 0) {
-#pragma unroll
-      for (int v = 0; v < 4; ++v) store_out((const int*)nullptr, p.C, at + v, p.out_fp32, acc[v]);
-    }
-  }
-}
-
 }  // namespace
 
 hipError_t launch_moe_few_tokens(const MoeProblem& p, hipStream_t stream) {
@@ -660,12 +611,6 @@ hipError_t launch_adapter_few(const AdapterProblem& p, hipStream_t stream) {
 
 hipError_t launch_adapter_shrink(const AdapterProblem& p, hipStream_t stream) {
   hipLaunchKernelGGL(adapter_shrink_kernel, dim3((unsigned)((p.T + 15) / 16), (unsigned)((p.r + 15) / 16)), dim3(kB),
-                     0, stream, p);
-  return hipGetLastError();
-}
-
-hipError_t launch_adapter_expand(const AdapterProblem& p, hipStream_t stream) {
-  hipLaunchKernelGGL(adapter_expand_kernel, dim3((unsigned)((p.T + 15) / 16), (unsigned)((p.N + 511) / 512)), dim3(kB),
                      0, stream, p);
   return hipGetLastError();
 }

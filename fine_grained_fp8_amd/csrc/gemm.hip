@@ -597,7 +597,7 @@ constexpr int kDScaleStage = 2048;
 constexpr int kDOutStage = 16384;              // epilogue staging per wave: 128 x 64 BF16 or 64 x 64 FP32
 constexpr int kDWOps = 8;                      // weight loads per block
 
-template <int kLayout, bool kOutF32, bool kGrouped, bool kTiledB>
+template <int kLayout, bool kOutF32, bool kGrouped, bool kTiledB, bool kAdapters = false>
 __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProblem p, int64_t total_tiles) {
   static_assert(kLayout != kDgrad, "Dgrad reads the weights transposed through LDS");
   __shared__ __attribute__((aligned(1024))) uint8_t lds_a0[kDStage];
@@ -1155,6 +1155,98 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
       }
     }
   };
+  // ---- epilogue with low-rank adapters: C = acc + B_a z ----
+  // The wave's FP32 sums go through its staging area in two halves of 64 rows
+  // (the registers of the accumulators are not touched again, and the loops
+  // below need not be unrolled over them).  The adapters of the 64 rows are
+  // taken in the order of their first row; for each, the 16x16 subtiles that
+  // hold one of its rows are read back, and B_a z is added by the BF16 matrix
+  // unit: z (FP32) as two BF16 terms, the rows of other adapters as zero
+  // columns.  Then whole row segments are rounded and stored, as above.
+  auto store_tile_adapters = [&](int64_t em0, int64_t em_end, int64_t en0) {
+    const AdapterEpilogue& ad = p.adapters;
+    const int64_t n0w = en0 + wave * 64;
+    uint8_t* ob = wave == 0 ? lds_z0 : wave == 1 ? lds_z1 : wave == 2 ? lds_z2 : lds_z3;
+    if (n0w >= p.N) return;   // N is a multiple of 128: the wave's 64 columns are all in or all out
+    const uint16_t* bcol = ad.B + (n0w + lrow) * ad.r;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int64_t mh = em0 + half * 64;
+#pragma unroll
+      for (int j = 0; j < DNJ / 2; ++j) {
+#pragma unroll
+        for (int i = 0; i < DNI; ++i) {
+          const int m = j * 16 + lrow, ch = i * 4 + lgrp;
+          const v4f& r = acc[i][half * (DNJ / 2) + j];
+          *reinterpret_cast<float4*>(ob + m * 256 + ((ch ^ (m & 15)) << 4)) = make_float4(r[0], r[1], r[2], r[3]);
+        }
+      }
+      const int id = mh + lane < em_end ? ad.ids[mh + lane] : -1;
+      uint64_t left = __ballot(id >= 0);
+#pragma unroll 1
+      while (left != 0) {
+        const int a = __builtin_amdgcn_readlane(id, (int)__builtin_ctzll(left));
+        const uint64_t in = __ballot(id == a);
+        left &= ~in;
+        const uint16_t* ba = bcol + (int64_t)(a < ad.n ? a : 0) * p.N * ad.r;
+#pragma unroll 1
+        for (int r0 = 0; r0 < ad.r; r0 += 32) {
+          const int r = r0 + lgrp * 8;
+          v8bf bw[DNI];
+#pragma unroll
+          for (int i = 0; i < DNI; ++i) {
+            const v4i none = {0, 0, 0, 0};
+            bw[i] = __builtin_bit_cast(
+                v8bf, r < ad.r ? *reinterpret_cast<const v4i*>(ba + (int64_t)i * 16 * ad.r + r) : none);
+          }
+#pragma unroll 1
+          for (int j = 0; j < DNJ / 2; ++j) {
+            const uint32_t rows = (uint32_t)(in >> (16 * j)) & 0xFFFFu;
+            if (rows == 0) continue;
+            float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (((rows >> lrow) & 1) && r < ad.r) {
+              const float4* zp = reinterpret_cast<const float4*>(ad.z + (mh + j * 16 + lrow) * ad.r + r);
+              const float4 u = zp[0], v = zp[1];
+              z[0] = u.x; z[1] = u.y; z[2] = u.z; z[3] = u.w;
+              z[4] = v.x; z[5] = v.y; z[6] = v.z; z[7] = v.w;
+            }
+            v8bf hi, lo;
+            split_bf16(z, hi, lo);
+#pragma unroll
+            for (int i = 0; i < DNI; ++i) {
+              const int m = j * 16 + lrow, ch = i * 4 + lgrp;
+              v4f* at = reinterpret_cast<v4f*>(ob + m * 256 + ((ch ^ (m & 15)) << 4));
+              *at = mfma_bf16_16x16x32(bw[i], lo, mfma_bf16_16x16x32(bw[i], hi, *at));
+            }
+          }
+        }
+      }
+      if constexpr (kOutF32) {
+#pragma unroll 4
+        for (int t = 0; t < 16; ++t) {
+          const int row = t * 4 + (lane >> 4), ch = lane & 15;
+          const v4i v = *reinterpret_cast<const v4i*>(ob + row * 256 + ((ch ^ (row & 15)) << 4));
+          float* dst = reinterpret_cast<float*>(p.C) + (mh + row) * p.ldc + n0w + ch * 4;
+          if (mh + row < em_end) __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(dst));
+        }
+      } else {
+#pragma unroll 4
+        for (int t = 0; t < 8; ++t) {
+          const int row = t * 8 + (lane >> 3), ch = 2 * (lane & 7);
+          const v4f u = *reinterpret_cast<const v4f*>(ob + row * 256 + ((ch ^ (row & 15)) << 4));
+          const v4f w = *reinterpret_cast<const v4f*>(ob + row * 256 + (((ch + 1) ^ (row & 15)) << 4));
+          v8bf h;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            h[k] = (__bf16)u[k];
+            h[k + 4] = (__bf16)w[k];
+          }
+          uint16_t* dst = reinterpret_cast<uint16_t*>(p.C) + (mh + row) * p.ldc + n0w + ch * 4;
+          if (mh + row < em_end) __builtin_nontemporal_store(__builtin_bit_cast(v4i, h), reinterpret_cast<v4i*>(dst));
+        }
+      }
+    }
+  };
   zero_state();
   issue_prologue();
   // Each work item decodes the next one first.  Its last round (padded
@@ -1285,10 +1377,12 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
     if (tid == 0) p.ws_count[et] = 0u;
     // the split path ends here and never reaches the K loop again (the
     // compiler's wait analysis would otherwise carry its loads into the loop)
-    store_tile(em0, em_end, en0, erows_m, erows_n);
+    if constexpr (kAdapters) store_tile_adapters(em0, em_end, en0);
+    else store_tile(em0, em_end, en0, erows_m, erows_n);
     return;
   }
-  store_tile(em0, em_end, en0, erows_m, erows_n);
+  if constexpr (kAdapters) store_tile_adapters(em0, em_end, en0);
+  else store_tile(em0, em_end, en0, erows_m, erows_n);
   if (!more) {
     wait_vm<0>();   // the reloads streamed by the last round land before the workgroup ends
     break;
@@ -1311,6 +1405,17 @@ hipError_t launch_typed(const GemmProblem& p, hipStream_t stream, int64_t grid, 
     }
   } else {
     grid = persistent_grid(grid);
+    if constexpr (kLayout == kFprop && !kGrouped) {
+      if (p.adapters.ids != nullptr) {
+        if (p.out_fp32)
+          hipLaunchKernelGGL((block_gemm_direct_kernel<kFprop, true, false, true, true>), dim3((unsigned)grid),
+                             dim3(kThreads), 0, stream, p, total);
+        else
+          hipLaunchKernelGGL((block_gemm_direct_kernel<kFprop, false, false, true, true>), dim3((unsigned)grid),
+                             dim3(kThreads), 0, stream, p, total);
+        return hipGetLastError();
+      }
+    }
     if (p.b_tiled) {
       if (p.out_fp32) {
         hipLaunchKernelGGL((block_gemm_direct_kernel<kLayout, true, kGrouped, true>), dim3((unsigned)grid),

@@ -56,6 +56,16 @@ hipError_t launch_recip_online_probe(const float* s, float* r, int64_t n, hipStr
 
 enum GemmLayout { kFprop = 0, kDgrad = 1, kWgrad = 2, kDgradT = 3 };
 
+// Low-rank adapters added to an Fprop product in its epilogue (ids == null:
+// none): C[m] += B_a z[m] with a = ids[m].  A negative id adds nothing; an id
+// >= n adds B_0 z[m] (the caller has made that z NaN).
+struct AdapterEpilogue {
+  const int32_t* ids;    // [M]
+  const float* z;        // [M][r]
+  const uint16_t* B;     // BF16 [n][N][r]
+  int r, n;              // r % 8 == 0
+};
+
 struct GemmProblem {
   int layout;            // GemmLayout
   int64_t M, N, K;
@@ -80,6 +90,7 @@ struct GemmProblem {
   float* ws_partial;
   uint32_t* ws_count;
   int64_t ws_slots;
+  AdapterEpilogue adapters;   // FPROP with tiled B, not grouped
 };
 
 hipError_t launch_gemm(const GemmProblem& p, hipStream_t stream);

@@ -106,9 +106,8 @@ struct AdapterProblem {
 };
 // the few-token form (T <= kAdapterFewTokens): quantization, shrink, projection and expand
 hipError_t launch_adapter_few(const AdapterProblem& p, hipStream_t stream);
-// z[t] = scale A x, and C[t] += B z for any number of tokens
+// z[t] = scale A x for any number of tokens
 hipError_t launch_adapter_shrink(const AdapterProblem& p, hipStream_t stream);
-hipError_t launch_adapter_expand(const AdapterProblem& p, hipStream_t stream);
 
 // The split-K workspace of the persistent GEMM on `stream` (api.cpp)
 void attach_gemm_workspace(GemmProblem& p, hipStream_t stream);

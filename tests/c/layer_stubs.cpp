@@ -10,7 +10,6 @@ int64_t layer_norm_grad_parts(int64_t rows, int64_t) { return rows < 512 ? rows 
 hipError_t launch_moe_few_tokens(const MoeProblem&, hipStream_t) { return hipErrorInvalidDeviceFunction; }
 hipError_t launch_adapter_few(const AdapterProblem&, hipStream_t) { return hipErrorInvalidDeviceFunction; }
 hipError_t launch_adapter_shrink(const AdapterProblem&, hipStream_t) { return hipErrorInvalidDeviceFunction; }
-hipError_t launch_adapter_expand(const AdapterProblem&, hipStream_t) { return hipErrorInvalidDeviceFunction; }
 hipError_t launch_quant_rows(const uint16_t*, int64_t, int64_t, int64_t, uint8_t*, int64_t, float*, int64_t,
                              const float*, float*, uint32_t*, hipStream_t) { return hipErrorInvalidDeviceFunction; }
 hipError_t launch_gemm(const GemmProblem&, hipStream_t) { return hipErrorInvalidDeviceFunction; }
