@@ -28,12 +28,13 @@ T* at(void* ws, int64_t off) {
 }
 
 struct MoeLayout {
-  int64_t logits, xq, xs, expert, gate, h, hq, hs, lists, bytes;
+  int64_t logits, value, xq, xs, expert, gate, h, hq, hs, counts, lists, bytes;
 };
 MoeLayout moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t local, int64_t k) {
   Carver c;
   MoeLayout l{};
   l.logits = c.take(T * E * 4);
+  l.value = c.take(T * E * 4);
   l.xq = c.take(T * H);
   l.xs = c.take(T * (H / 128) * 4);
   l.expert = c.take(T * k * 4);
@@ -41,7 +42,8 @@ MoeLayout moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t local, 
   l.h = c.take(T * k * I * 4);
   l.hq = c.take(T * k * I);
   l.hs = c.take(T * k * (I / 128) * 4);
-  l.lists = c.take((3 + 2 * local + T * k) * 4);
+  l.counts = c.take(local * 4);
+  l.lists = c.take(local * fp8bs::kMoeMaxTokens * 4);
   l.bytes = c.used;
   return l;
 }
@@ -225,6 +227,7 @@ fp8_status fp8_moe_few_tokens(int64_t T, int64_t H, int64_t I, int32_t E, int32_
   p.w13 = w13; p.s13 = s13; p.w2 = w2; p.s2 = s2;
   p.y = y; p.ldy = ldy; p.y_fp32 = e == 4;
   p.logits = at<float>(workspace, l.logits);
+  p.value = bias ? at<float>(workspace, l.value) : p.logits;
   p.xq = at<uint8_t>(workspace, l.xq);
   p.xs = at<float>(workspace, l.xs);
   p.slot_expert = ids ? ids : at<int32_t>(workspace, l.expert);
@@ -232,6 +235,7 @@ fp8_status fp8_moe_few_tokens(int64_t T, int64_t H, int64_t I, int32_t E, int32_
   p.h = at<float>(workspace, l.h);
   p.hq = at<uint8_t>(workspace, l.hq);
   p.hs = at<float>(workspace, l.hs);
+  p.counts = at<int32_t>(workspace, l.counts);
   p.lists = at<int32_t>(workspace, l.lists);
   return launched(fp8bs::launch_moe_few_tokens(p, reinterpret_cast<hipStream_t>(stream)));
 }
@@ -281,11 +285,10 @@ fp8_status fp8_adapter_linear(int64_t T, int64_t N, int64_t K, int32_t rank, int
   p.C = C; p.ldc = ldc; p.out_fp32 = e == 4;
   p.xq = at<uint8_t>(workspace, l.xq);
   p.xs = at<float>(workspace, l.xs);
-  p.z = at<float>(workspace, l.z);
+  p.z = at<uint16_t>(workspace, l.z);
   if (T <= fp8bs::kAdapterFewTokens) return launched(fp8bs::launch_adapter_few(p, s));
   const int64_t ld_s = (T + 3) / 4 * 4;
-  hipError_t err = fp8bs::launch_quant_rows(p.x, T, K, ldx, p.xq, K, p.xs, ld_s, nullptr, nullptr, nullptr, s);
-  if (err == hipSuccess) err = fp8bs::launch_adapter_shrink(p, s);
+  const hipError_t err = fp8bs::launch_adapter_prompt(p, ld_s, s);
   if (err != hipSuccess) return launched(err);
   fp8bs::GemmProblem g{};
   g.layout = fp8bs::kFprop;

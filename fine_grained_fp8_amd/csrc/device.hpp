@@ -159,10 +159,9 @@ __device__ __forceinline__ void transpose4x4_bytes(uint32_t a0, uint32_t a1, uin
   o3 = __builtin_amdgcn_perm(t3, t2, 0x07060302u);
 }
 
-// 1x128 quantization of a lane's 8 BF16 values (packed in d): the 16 lanes
-// of a DPP row hold the tile.  The online rule, as in the row quantizer.
-__device__ __forceinline__ uint2 quant8_bf16(const uint4& d, float& s) {
-  const uint32_t t = row16_max_u32(absmax_bits8(d));
+// 1x128 quantization of a lane's 8 BF16 values (packed in d), given the max
+// of its tile as BF16 magnitude bits: the online rule, as in the row quantizer.
+__device__ __forceinline__ uint2 quant8_bf16_tile(const uint4& d, uint32_t t, float& s) {
   s = tile_scale(t);
   uint2 out;
   if (t < kBf16InfAbs) {
@@ -176,6 +175,10 @@ __device__ __forceinline__ uint2 quant8_bf16(const uint4& d, float& s) {
     out.y = pack4_sat_nan(bf16_lo(d.z) / s, bf16_hi(d.z) / s, bf16_lo(d.w) / s, bf16_hi(d.w) / s);
   }
   return out;
+}
+// the same where the 16 lanes of a DPP row hold the tile
+__device__ __forceinline__ uint2 quant8_bf16(const uint4& d, float& s) {
+  return quant8_bf16_tile(d, row16_max_u32(absmax_bits8(d)), s);
 }
 
 // The same rule on a lane's 8 FP32 values, given the tile's |y| max as FP32
@@ -206,17 +209,6 @@ __device__ __forceinline__ uint2 quant8_f32(const float (&y)[8], uint32_t amax_b
 // (from 8 (l / 16)) of row / column l % 16 of each operand.
 __device__ __forceinline__ v4f mfma_bf16_16x16x32(const v8bf& a, const v8bf& b, const v4f& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-
-// 8 FP32 values as two BF16 terms each, v = hi + lo up to 2^-17 of v: a product
-// with both terms loses nothing that FP32 sums would keep.
-__device__ __forceinline__ void split_bf16(const float (&v)[8], v8bf& hi, v8bf& lo) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    hi[i] = (__bf16)v[i];
-    const float d = v[i] - (float)hi[i];
-    lo[i] = (__bf16)(d == d ? d : 0.f);   // Inf and NaN sit in hi
-  }
 }
 
 }  // namespace fp8bs

@@ -1161,7 +1161,7 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
   // below need not be unrolled over them).  The adapters of the 64 rows are
   // taken in the order of their first row; for each, the 16x16 subtiles that
   // hold one of its rows are read back, and B_a z is added by the BF16 matrix
-  // unit: z (FP32) as two BF16 terms, the rows of other adapters as zero
+  // unit (z comes as two BF16 terms), the rows of other adapters as zero
   // columns.  Then whole row segments are rounded and stored, as above.
   auto store_tile_adapters = [&](int64_t em0, int64_t em_end, int64_t en0) {
     const AdapterEpilogue& ad = p.adapters;
@@ -1169,6 +1169,8 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
     uint8_t* ob = wave == 0 ? lds_z0 : wave == 1 ? lds_z1 : wave == 2 ? lds_z2 : lds_z3;
     if (n0w >= p.N) return;   // N is a multiple of 128: the wave's 64 columns are all in or all out
     const uint16_t* bcol = ad.B + (n0w + lrow) * ad.r;
+    const int id0 = em0 + lane < em_end ? ad.ids[em0 + lane] : -1;
+    const int id1 = em0 + 64 + lane < em_end ? ad.ids[em0 + 64 + lane] : -1;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int64_t mh = em0 + half * 64;
@@ -1181,7 +1183,7 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
           *reinterpret_cast<float4*>(ob + m * 256 + ((ch ^ (m & 15)) << 4)) = make_float4(r[0], r[1], r[2], r[3]);
         }
       }
-      const int id = mh + lane < em_end ? ad.ids[mh + lane] : -1;
+      const int id = half == 0 ? id0 : id1;
       uint64_t left = __ballot(id >= 0);
 #pragma unroll 1
       while (left != 0) {
@@ -1191,32 +1193,30 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
         const uint16_t* ba = bcol + (int64_t)(a < ad.n ? a : 0) * p.N * ad.r;
 #pragma unroll 1
         for (int r0 = 0; r0 < ad.r; r0 += 32) {
+          // all loads of the step first: one round trip
           const int r = r0 + lgrp * 8;
-          v8bf bw[DNI];
+          const v4i none = {0, 0, 0, 0};
+          v4i bw[DNI], zh[DNJ / 2], zl[DNJ / 2];
 #pragma unroll
-          for (int i = 0; i < DNI; ++i) {
-            const v4i none = {0, 0, 0, 0};
-            bw[i] = __builtin_bit_cast(
-                v8bf, r < ad.r ? *reinterpret_cast<const v4i*>(ba + (int64_t)i * 16 * ad.r + r) : none);
-          }
-#pragma unroll 1
+          for (int i = 0; i < DNI; ++i)
+            bw[i] = r < ad.r ? *reinterpret_cast<const v4i*>(ba + (int64_t)i * 16 * ad.r + r) : none;
+#pragma unroll
           for (int j = 0; j < DNJ / 2; ++j) {
-            const uint32_t rows = (uint32_t)(in >> (16 * j)) & 0xFFFFu;
-            if (rows == 0) continue;
-            float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (((rows >> lrow) & 1) && r < ad.r) {
-              const float4* zp = reinterpret_cast<const float4*>(ad.z + (mh + j * 16 + lrow) * ad.r + r);
-              const float4 u = zp[0], v = zp[1];
-              z[0] = u.x; z[1] = u.y; z[2] = u.z; z[3] = u.w;
-              z[4] = v.x; z[5] = v.y; z[6] = v.z; z[7] = v.w;
-            }
-            v8bf hi, lo;
-            split_bf16(z, hi, lo);
+            const bool on = ((in >> (16 * j + lrow)) & 1) && r < ad.r;
+            const uint16_t* zp = ad.z + (mh + j * 16 + lrow) * 2 * ad.r + 2 * r;
+            zh[j] = on ? *reinterpret_cast<const v4i*>(zp) : none;
+            zl[j] = on ? *reinterpret_cast<const v4i*>(zp + 8) : none;
+          }
+#pragma unroll
+          for (int j = 0; j < DNJ / 2; ++j) {
+            if (((in >> (16 * j)) & 0xFFFFu) == 0) continue;
+            const v8bf hi = __builtin_bit_cast(v8bf, zh[j]), lo = __builtin_bit_cast(v8bf, zl[j]);
 #pragma unroll
             for (int i = 0; i < DNI; ++i) {
               const int m = j * 16 + lrow, ch = i * 4 + lgrp;
               v4f* at = reinterpret_cast<v4f*>(ob + m * 256 + ((ch ^ (m & 15)) << 4));
-              *at = mfma_bf16_16x16x32(bw[i], lo, mfma_bf16_16x16x32(bw[i], hi, *at));
+              const v8bf b = __builtin_bit_cast(v8bf, bw[i]);
+              *at = mfma_bf16_16x16x32(b, lo, mfma_bf16_16x16x32(b, hi, *at));
             }
           }
         }

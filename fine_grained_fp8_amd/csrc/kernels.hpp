@@ -61,7 +61,7 @@ enum GemmLayout { kFprop = 0, kDgrad = 1, kWgrad = 2, kDgradT = 3 };
 // >= n adds B_0 z[m] (the caller has made that z NaN).
 struct AdapterEpilogue {
   const int32_t* ids;    // [M]
-  const float* z;        // [M][r]
+  const uint16_t* z;     // [M][r / 8][16]: BF16 terms hi[8], lo[8] of every 8 ranks, z = hi + lo
   const uint16_t* B;     // BF16 [n][N][r]
   int r, n;              // r % 8 == 0
 };

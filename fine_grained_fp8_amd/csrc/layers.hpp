@@ -70,6 +70,7 @@ struct MoeProblem {
   int y_fp32;
   // workspace
   float* logits;              // [T][E]
+  float* value;               // [T][E]: what experts are chosen by (logits, if there is no bias)
   uint8_t* xq;                // [T][H]
   float* xs;                  // [T][H / 128]
   int32_t* slot_expert;       // [T][top_k]: chosen experts, best first
@@ -77,7 +78,8 @@ struct MoeProblem {
   float* h;                   // [T top_k][I]
   uint8_t* hq;                // [T top_k][I]
   float* hs;                  // [T top_k][I / 128]
-  int32_t* lists;             // [2 + 2 local + 1 + T top_k]: see moe_mid_kernel
+  int32_t* counts;            // [local]: slots that chose each held expert
+  int32_t* lists;             // [local][kMoeMaxTokens]: those slots (token top_k + place), in token order
 };
 hipError_t launch_moe_few_tokens(const MoeProblem& p, hipStream_t stream);
 
@@ -102,12 +104,12 @@ struct AdapterProblem {
   // workspace
   uint8_t* xq;                // [T][K]
   float* xs;                  // few: [T][K / 128]; otherwise [K / 128][round_up(T, 4)]
-  float* z;                   // [T][r]
+  uint16_t* z;                // [T][r / 8][16]: A x as BF16 terms hi[8], lo[8] for every 8 ranks
 };
 // the few-token form (T <= kAdapterFewTokens): quantization, shrink, projection and expand
 hipError_t launch_adapter_few(const AdapterProblem& p, hipStream_t stream);
-// z[t] = scale A x for any number of tokens
-hipError_t launch_adapter_shrink(const AdapterProblem& p, hipStream_t stream);
+// codes and scales of x (MN-major, leading dimension ld_s) and z for any number of tokens
+hipError_t launch_adapter_prompt(const AdapterProblem& p, int64_t ld_s, hipStream_t stream);
 
 // The split-K workspace of the persistent GEMM on `stream` (api.cpp)
 void attach_gemm_workspace(GemmProblem& p, hipStream_t stream);

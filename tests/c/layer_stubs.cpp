@@ -9,9 +9,7 @@ hipError_t launch_layer_norm_backward(const LayerNormGradProblem&, hipStream_t) 
 int64_t layer_norm_grad_parts(int64_t rows, int64_t) { return rows < 512 ? rows : 512; }
 hipError_t launch_moe_few_tokens(const MoeProblem&, hipStream_t) { return hipErrorInvalidDeviceFunction; }
 hipError_t launch_adapter_few(const AdapterProblem&, hipStream_t) { return hipErrorInvalidDeviceFunction; }
-hipError_t launch_adapter_shrink(const AdapterProblem&, hipStream_t) { return hipErrorInvalidDeviceFunction; }
-hipError_t launch_quant_rows(const uint16_t*, int64_t, int64_t, int64_t, uint8_t*, int64_t, float*, int64_t,
-                             const float*, float*, uint32_t*, hipStream_t) { return hipErrorInvalidDeviceFunction; }
+hipError_t launch_adapter_prompt(const AdapterProblem&, int64_t, hipStream_t) { return hipErrorInvalidDeviceFunction; }
 hipError_t launch_gemm(const GemmProblem&, hipStream_t) { return hipErrorInvalidDeviceFunction; }
 void attach_gemm_workspace(GemmProblem&, hipStream_t) {}
 
