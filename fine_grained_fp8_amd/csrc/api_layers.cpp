@@ -28,13 +28,12 @@ T* at(void* ws, int64_t off) {
 }
 
 struct MoeLayout {
-  int64_t logits, value, xq, xs, expert, gate, h, hq, hs, counts, lists, bytes;
+  int64_t logits, xq, xs, expert, gate, h, hq, hs, counts, lists, plan, bytes;
 };
 MoeLayout moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t local, int64_t k) {
   Carver c;
   MoeLayout l{};
-  l.logits = c.take(T * E * 4);
-  l.value = c.take(T * E * 4);
+  l.logits = c.take(fp8bs::dot_splits(H, fp8bs::kMoeSplits) * T * E * 4);
   l.xq = c.take(T * H);
   l.xs = c.take(T * (H / 128) * 4);
   l.expert = c.take(T * k * 4);
@@ -44,18 +43,21 @@ MoeLayout moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t local, 
   l.hs = c.take(T * k * (I / 128) * 4);
   l.counts = c.take(local * 4);
   l.lists = c.take(local * fp8bs::kMoeMaxTokens * 4);
+  l.plan = c.take((2 + 2 * (T * k + T * k / 16) + 2 * T * k) * 4);
   l.bytes = c.used;
   return l;
 }
 
 struct AdapterLayout {
-  int64_t xq, xs, z, bytes;
+  int64_t xq, xs, zp, z, bytes;
 };
 AdapterLayout adapter_layout(int64_t T, int64_t K, int64_t r) {
   Carver c;
   AdapterLayout l{};
+  if (T == 0) return l;
   l.xq = c.take(T * K);
   l.xs = c.take((K / 128) * ((T + 3) / 4 * 4) * 4);
+  l.zp = c.take(fp8bs::adapter_splits(T, K) * T * r * 4);
   l.z = c.take(T * r * 4);
   l.bytes = c.used;
   return l;
@@ -227,7 +229,7 @@ fp8_status fp8_moe_few_tokens(int64_t T, int64_t H, int64_t I, int32_t E, int32_
   p.w13 = w13; p.s13 = s13; p.w2 = w2; p.s2 = s2;
   p.y = y; p.ldy = ldy; p.y_fp32 = e == 4;
   p.logits = at<float>(workspace, l.logits);
-  p.value = bias ? at<float>(workspace, l.value) : p.logits;
+  p.splits = fp8bs::dot_splits(H, fp8bs::kMoeSplits);
   p.xq = at<uint8_t>(workspace, l.xq);
   p.xs = at<float>(workspace, l.xs);
   p.slot_expert = ids ? ids : at<int32_t>(workspace, l.expert);
@@ -237,6 +239,7 @@ fp8_status fp8_moe_few_tokens(int64_t T, int64_t H, int64_t I, int32_t E, int32_
   p.hs = at<float>(workspace, l.hs);
   p.counts = at<int32_t>(workspace, l.counts);
   p.lists = at<int32_t>(workspace, l.lists);
+  p.plan = at<int32_t>(workspace, l.plan);
   return launched(fp8bs::launch_moe_few_tokens(p, reinterpret_cast<hipStream_t>(stream)));
 }
 
@@ -285,6 +288,8 @@ fp8_status fp8_adapter_linear(int64_t T, int64_t N, int64_t K, int32_t rank, int
   p.C = C; p.ldc = ldc; p.out_fp32 = e == 4;
   p.xq = at<uint8_t>(workspace, l.xq);
   p.xs = at<float>(workspace, l.xs);
+  p.splits = fp8bs::adapter_splits(T, K);
+  p.zp = at<float>(workspace, l.zp);
   p.z = at<uint16_t>(workspace, l.z);
   if (T <= fp8bs::kAdapterFewTokens) return launched(fp8bs::launch_adapter_few(p, s));
   const int64_t ld_s = (T + 3) / 4 * 4;

@@ -20,11 +20,9 @@ namespace {
 typedef int fv4i __attribute__((ext_vector_type(4)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
-constexpr int kB = 512;         // threads of the streaming kernels
-constexpr int kW = kB / 64;     // and their waves
-constexpr int kPB = 1024;       // threads of the kernels that prepare and combine
-constexpr int kPW = kPB / 64;
-// 16-row tiles from which on a workgroup takes two of them
+constexpr int kB = 512;         // threads of a workgroup
+constexpr int kW = kB / 64;     // and its waves
+// 16-row tiles from which on a workgroup of the projection takes two of them
 constexpr int64_t kWideTiles = 1024;
 
 __device__ __forceinline__ v8bf as_bf16x8(const fv4i& v) { return __builtin_bit_cast(v8bf, v); }
@@ -71,52 +69,70 @@ __device__ __forceinline__ v4f block_product(const Bf16Block& a, const Bf16Block
 
 __device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
 
-// Selection order of routing values: larger first, NaN last, equal values by
-// index.  Keys are never 0 for an index below 2^32 - 1.
+// Selection order of routing values as unsigned numbers: larger first, NaN
+// last (1; 0 is left for "none").
 __device__ __forceinline__ uint32_t order_bits(float v) {
-  if (v != v) return 0u;
+  if (v != v) return 1u;
   const uint32_t u = __float_as_uint(v + 0.0f);   // -0 counts as +0
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);   // -infinity: 0x007FFFFF
 }
-__device__ __forceinline__ uint64_t order_key(float v, int index) {
-  return ((uint64_t)order_bits(v) << 32) | (uint64_t)(0xFFFFFFFFu - (uint32_t)index);
+
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = row16_max_u32(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(b[0], b[1]);
+}
+
+// max (NaN left out) and sum over the wave, in every lane
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, 16));
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) v += __shfl_xor(v, d, 16);
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
 // Dot products of 16 BF16 rows (row l & 15 of the lane at `a`, 16-byte
-// aligned) with 16 BF16 token rows (at `b`), K % 128 == 0, the K blocks
-// dealt to the workgroup's kPW waves in turn; this wave's partial sums.  Two
-// blocks' loads are in flight at a time: one round trip to memory takes longer
-// than all the arithmetic.
-__device__ __forceinline__ v4f dot_rows_bf16(const uint16_t* a, const uint16_t* b, int K, int wave, int lgrp) {
+// aligned) with 16 BF16 token rows (at `b`) over K blocks [kb0, kb1), dealt to
+// the workgroup's kW waves in turn; this wave's partial sums.
+__device__ __forceinline__ v4f dot_rows_bf16(const uint16_t* a, const uint16_t* b, int kb0, int kb1, int wave,
+                                             int lgrp) {
   v4f c = {0.f, 0.f, 0.f, 0.f};
-  const int kb_n = K / 128;
-  for (int kb = wave; kb < kb_n; kb += 2 * kPW) {
-    const bool two = kb + kPW < kb_n;
-    fv4i va[2][4], vb[2][4];
+  for (int kb = kb0 + wave; kb < kb1; kb += kW) {
+    fv4i va[4], vb[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (h == 1 && !two) break;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        va[h][i] = *reinterpret_cast<const fv4i*>(a + (kb + h * kPW) * 128 + i * 32 + lgrp * 8);
-        vb[h][i] = *reinterpret_cast<const fv4i*>(b + (kb + h * kPW) * 128 + i * 32 + lgrp * 8);
-      }
+    for (int i = 0; i < 4; ++i) {
+      va[i] = *reinterpret_cast<const fv4i*>(a + kb * 128 + i * 32 + lgrp * 8);
+      vb[i] = *reinterpret_cast<const fv4i*>(b + kb * 128 + i * 32 + lgrp * 8);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c = mfma_bf16_16x16x32(as_bf16x8(va[0][i]), as_bf16x8(vb[0][i]), c);
-    if (two) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c = mfma_bf16_16x16x32(as_bf16x8(va[1][i]), as_bf16x8(vb[1][i]), c);
-    }
+    for (int i = 0; i < 4; ++i) c = mfma_bf16_16x16x32(as_bf16x8(va[i]), as_bf16x8(vb[i]), c);
   }
   return c;
 }
 
-// 1x128 quantization of token rows: 64 tiles a workgroup, 16 lanes each.
+// Share s of S of kb_n K blocks.  The small dot products (router, shrink) are
+// cut along K over S workgroups, whose partial sums the reader adds in order:
+// one compute unit alone would take 8 - 17 us to read 16 rows of 7168 and
+// their tokens.
+__device__ __forceinline__ int share(int kb_n, int s, int S) { return (int)((int64_t)kb_n * s / S); }
+
+// 1x128 quantization of token rows: 32 tiles a workgroup, 16 lanes each.
 __device__ __forceinline__ void quant_tokens(const uint16_t* x, int64_t ldx, int T, int K, int block, uint8_t* xq,
                                              float* xs) {
   const int kb_n = K / 128;
-  const int tile = block * (kPB / 16) + (threadIdx.x >> 4);
+  const int tile = block * (kB / 16) + (threadIdx.x >> 4);
   if (tile >= T * kb_n) return;   // whole 16-lane groups
   const int t = tile / kb_n, kb = tile - t * kb_n, l16 = threadIdx.x & 15;
   const fv4i d = *reinterpret_cast<const fv4i*>(x + t * ldx + kb * 128 + l16 * 8);
@@ -125,7 +141,7 @@ __device__ __forceinline__ void quant_tokens(const uint16_t* x, int64_t ldx, int
   *reinterpret_cast<uint2*>(xq + (int64_t)t * K + kb * 128 + l16 * 8) = q;
   if (l16 == 0) xs[t * kb_n + kb] = s;
 }
-int quant_blocks(int64_t T, int64_t K) { return (int)((T * (K / 128) + kPB / 16 - 1) / (kPB / 16)); }
+int quant_blocks(int64_t T, int64_t K) { return (int)((T * (K / 128) + kB / 16 - 1) / (kB / 16)); }
 
 __device__ __forceinline__ void store_out(void* y, int64_t at, int fp32, float v) {
   if (fp32) static_cast<float*>(y)[at] = v;
@@ -133,99 +149,119 @@ __device__ __forceinline__ void store_out(void* y, int64_t at, int fp32, float v
 }
 
 // ===========================================================================
-// Mixture of experts for up to 64 tokens, four launches.
+// Mixture of experts for up to 64 tokens, four or five launches.
 // ===========================================================================
 
-// 1. Router logits and the values experts are chosen by (16 experts x 16 tokens
-//    a workgroup), and the 1x128 quantization of x.
-__global__ __launch_bounds__(kPB) void moe_prepare_kernel(MoeProblem p, int router_blocks) {
+// 1. Router logits (16 experts x 16 tokens x a share of K a workgroup), and the
+//    1x128 quantization of x.
+__global__ __launch_bounds__(kB) void moe_prepare_kernel(MoeProblem p, int router_blocks) {
   if ((int)blockIdx.x >= router_blocks) {
     quant_tokens(p.x, p.ldx, p.T, p.H, blockIdx.x - router_blocks, p.xq, p.xs);
     return;
   }
-  __shared__ v4f part[kPW][64];
+  __shared__ v4f part[kW][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lrow = lane & 15, lgrp = lane >> 4;
-  const int e_tiles = (p.E + 15) / 16;
-  const int e0 = (blockIdx.x % e_tiles) * 16, t0 = (blockIdx.x / e_tiles) * 16;
+  const int e_tiles = (p.E + 15) / 16, s = blockIdx.x % p.splits, et = blockIdx.x / p.splits;
+  const int e0 = (et % e_tiles) * 16, t0 = (et / e_tiles) * 16;
   const int e = e0 + lrow < p.E ? e0 + lrow : p.E - 1;
   const int t = t0 + lrow < p.T ? t0 + lrow : p.T - 1;
-  part[wave][lane] = dot_rows_bf16(p.router + e * p.ld_r, p.x + t * p.ldx, p.H, wave, lgrp);
+  const int kb_n = p.H / 128;
+  part[wave][lane] = dot_rows_bf16(p.router + e * p.ld_r, p.x + t * p.ldx, share(kb_n, s, p.splits),
+                                   share(kb_n, s + 1, p.splits), wave, lgrp);
   __syncthreads();
   if (wave == 0) {
     v4f c = part[0][lane];
 #pragma unroll
-    for (int w = 1; w < kPW; ++w) c += part[w][lane];
+    for (int w = 1; w < kW; ++w) c += part[w][lane];
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const int ee = e0 + lgrp * 4 + v;
-      if (ee < p.E && t0 + lrow < p.T) {
-        const int at = (t0 + lrow) * p.E + ee;
-        p.logits[at] = c[v];
-        if (p.bias) p.value[at] = sigmoid(c[v]) + p.bias[ee];   // otherwise value is logits
-      }
+      if (ee < p.E && t0 + lrow < p.T) p.logits[((int64_t)s * p.T + t0 + lrow) * p.E + ee] = c[v];
     }
   }
 }
 
+// The logit of expert e for token t; out of range (on: false): -infinity.
+__device__ __forceinline__ float logit(const MoeProblem& p, int t, int e, bool on) {
+  if (!on) return -INFINITY;
+  float v[kMoeSplits];
+#pragma unroll
+  for (int s = 0; s < kMoeSplits; ++s) v[s] = s < p.splits ? p.logits[((int64_t)s * p.T + t) * p.E + e] : 0.f;
+#pragma unroll
+  for (int s = 1; s < kMoeSplits; ++s) v[0] += v[s];
+  return v[0];
+}
+// what experts are chosen by
+__device__ __forceinline__ float choice_value(const MoeProblem& p, float l, int e) {
+  return p.bias ? sigmoid(l) + p.bias[e] : l;
+}
+
 // One wave: the chosen experts of token t, best first, with their gates.
-// Lane l holds experts l, l + 64, ...
+// Lane l holds experts l, l + 64, ..., at most kMost of them.
+template <int kMost>
 __device__ __forceinline__ void route_token(const MoeProblem& p, int t, int lane) {
-  constexpr int kMost = kMoeMaxExperts / 64;
   float l[kMost];
-  uint64_t key[kMost];
+  uint32_t key[kMost];   // order_bits; 0: no such expert, or taken
 #pragma unroll
   for (int c = 0; c < kMost; ++c) {
     const int e = c * 64 + lane;
-    const bool in = c * 64 < p.E && e < p.E;
-    l[c] = in ? p.logits[t * p.E + e] : -INFINITY;
-    key[c] = in ? order_key(p.value[t * p.E + e], e) : 0;
+    l[c] = -INFINITY;
+    key[c] = 0;
+    if (c * 64 < p.E) {
+      l[c] = logit(p, t, e, e < p.E);
+      if (e < p.E) key[c] = order_bits(choice_value(p, l[c], e));
+    }
   }
   float m = -INFINITY, sum = 1.0f;
   if (!p.sigmoid) {
 #pragma unroll
     for (int c = 0; c < kMost; ++c) m = fmaxf(m, l[c]);
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+    m = wave_max(m);
     sum = 0.f;
 #pragma unroll
     for (int c = 0; c < kMost; ++c)
       if (c * 64 < p.E) sum += c * 64 + lane < p.E ? expf(l[c] - m) : 0.f;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+    sum = wave_sum(sum);
   }
-  uint64_t below = ~0ull;         // keys at or above it are taken
   float my_score = 0.f, total = 0.f;
   int my_expert = 0;
   for (int j = 0; j < p.top_k; ++j) {
-    uint64_t best = 0;
+    // the lane's best that is left (bits 0: taken or absent), the lowest index first
+    uint32_t best = 0;
+    int at = 0;
     float lb = 0.f;
 #pragma unroll
     for (int c = 0; c < kMost; ++c)
-      if (c * 64 < p.E && key[c] < below && key[c] > best) {
+      if (c * 64 < p.E && key[c] > best) {
         best = key[c];
+        at = c;
         lb = l[c];
       }
+    const uint32_t top = wave_max_u32(best);
+    const uint32_t index = best == top ? (uint32_t)(at * 64 + lane) : 0xFFFFFFFFu;
+    const uint32_t e = ~wave_max_u32(~index);      // the smallest index among equals
+    const float le = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(lb), (int)(e & 63)));
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const uint64_t o = __shfl_xor(best, d);
-      const float ol = __shfl_xor(lb, d);
-      if (o > best) {
-        best = o;
-        lb = ol;
-      }
-    }
-    below = best;
-    const float score = p.sigmoid ? sigmoid(lb) : expf(lb - m) / sum;
+    for (int c = 0; c < kMost; ++c)
+      if (e == (uint32_t)(c * 64 + lane)) key[c] = 0;
+    const float score = p.sigmoid ? sigmoid(le) : expf(le - m) / sum;
     total += score;
     if (lane == j) {
       my_score = score;
-      my_expert = (int)(0xFFFFFFFFu - (uint32_t)best);
+      my_expert = (int)e;
     }
   }
   if (lane < p.top_k) {
     p.slot_expert[t * p.top_k + lane] = my_expert;
     p.slot_gate[t * p.top_k + lane] = (p.normalize ? my_score / total : my_score) * p.gate_scale;
   }
+}
+
+// 2. Routing, a wave per token.
+template <int kMost>
+__global__ __launch_bounds__(256) void moe_route_kernel(MoeProblem p) {
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t < p.T) route_token<kMost>(p, t, threadIdx.x & 63);
 }
 
 // One K block of the up kernel as loaded: the gate tile, the up tile, 16
@@ -265,20 +301,31 @@ __device__ __forceinline__ void up_sums(const MoeProblem& p, int el, int tile, c
     f.fg = sg[kb];
     f.fu = su[kb];
   };
-  auto products = [&](int kb, const UpLoads& f) {
+  // Loads return in the order of their issue: the token operands of the
+  // present block are asked for before the next block's weights.
+  Block x[NT];
+  float sx[NT];
+  auto tokens = [&](int kb, const UpLoads& f) {
+    if constexpr (NT == 1) {
+      x[0] = f.x;
+      sx[0] = f.sx;
+    } else {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        x[j] = load_row(p.xq + (int64_t)tok[j] * p.H + kb * 128, lgrp);
+        sx[j] = p.xs[tok[j] * kb_n + kb];
+      }
+      __asm__ volatile("" ::: "memory");
+    }
+  };
+  auto products = [&](const UpLoads& f) {
     const Bf16Block g16 = to_bf16(f.g), u16 = to_bf16(f.u);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       if (j * 16 < n) {
-        Block xb = f.x;
-        float sx = f.sx;
-        if constexpr (NT > 1) {
-          xb = load_row(p.xq + (int64_t)tok[j] * p.H + kb * 128, lgrp);
-          sx = p.xs[tok[j] * kb_n + kb];
-        }
-        const Bf16Block b = to_bf16(xb);
+        const Bf16Block b = to_bf16(x[j]);
         const v4f pg = block_product(g16, b), pu = block_product(u16, b);
-        const float cg = sx * f.fg, cu = sx * f.fu;
+        const float cg = sx[j] * f.fg, cu = sx[j] * f.fu;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           ag[j][v] = __builtin_fmaf(pg[v], cg, ag[j][v]);
@@ -287,72 +334,61 @@ __device__ __forceinline__ void up_sums(const MoeProblem& p, int el, int tile, c
       }
     }
   };
-  int kb = wave;
-  if (kb >= kb_n) return;
-  UpLoads f0{}, f1{};
-  fetch(kb, f0);
-  for (;;) {
-    const bool two = kb + kW < kb_n, three = kb + 2 * kW < kb_n;
-    if (two) fetch(kb + kW, f1);
-    products(kb, f0);
-    if (!two) break;
-    if (three) fetch(kb + 2 * kW, f0);
-    products(kb + kW, f1);
-    if (!three) break;
-    kb += 2 * kW;
+  if (wave >= kb_n) return;
+  const int last = kb_n - 1;
+  UpLoads f0, f1;
+  fetch(wave, f0);
+  for (int kb = wave;; kb += 2 * kW) {
+    tokens(kb, f0);
+    fetch(min(kb + kW, last), f1);     // past the wave's last block: one that is not used
+    products(f0);
+    if (kb + kW >= kb_n) break;
+    tokens(kb + kW, f1);
+    fetch(min(kb + 2 * kW, last), f0);
+    products(f1);
+    if (kb + 2 * kW >= kb_n) break;
   }
 }
 
-// 2. Routing (the first blocks, a wave per token), and h = silu(W1 x) (W3 x)
-//    for the tokens that chose a held expert: workgroup (expert, 16 channels)
-//    with the gate rows and the up rows of the same channels.  A workgroup
-//    finds its expert's tokens itself: a token chose expert e if fewer than
-//    top_k experts come before e, and that count is e's slot (one round trip
-//    for all tokens, with no launch between routing and products).  The
-//    products convert the codes to BF16: exact, with FP32 sums, because h is
-//    quantized again and the FP8 instruction's truncation would move codes.
-__global__ __launch_bounds__(kB, 4) void moe_up_kernel(MoeProblem p, int route_blocks) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lrow = lane & 15, lgrp = lane >> 4;
-  if ((int)blockIdx.x < route_blocks) {
-    const int t = blockIdx.x * kW + wave;
-    if (t < p.T) route_token(p, t, lane);
-    return;
-  }
+// 3. h = silu(W1 x) (W3 x) for the tokens that chose a held expert: workgroup
+//    (expert, 16 channels) with the gate rows and the up rows of the same
+//    channels.  The products convert the codes to BF16: exact, with FP32 sums,
+//    because h is quantized again and the FP8 instruction's truncation would
+//    move codes.
+//    A workgroup lists its expert's tokens itself.  kRouted: from the chosen
+//    slots (at most 1024 numbers).  Otherwise (a token per wave at most) it
+//    finds them from the logits, while the first blocks of the same launch do
+//    the routing for the kernels that follow: a token chose expert e if fewer
+//    than top_k experts come before e, and that count is e's slot.  That saves
+//    a launch (about 4 us); with more tokens every workgroup would repeat too
+//    many sums over the shares.
+template <int NT, bool kRouted>
+__global__ __launch_bounds__(kB, NT > 2 ? 2 : 4) void moe_up_kernel(MoeProblem p, int route_blocks) {
   __shared__ v4f part[kW][2][64];
   __shared__ int slot_of[kMoeMaxTokens];     // the expert's slot of each token, or -1
   __shared__ int list_t[kMoeMaxTokens], list_slot[kMoeMaxTokens], count;
-  const int tiles = p.I / 16;
-  const int el = (blockIdx.x - route_blocks) / tiles, tile = (blockIdx.x - route_blocks) % tiles;
-  const int e = p.first + el;
-  {
-    constexpr int kPer = kMoeMaxTokens / kW;   // tokens of a wave
-    uint64_t mine[kPer];
-    int before[kPer];
-    float own[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int t = wave + i * kW;
-      own[i] = t < p.T ? p.value[t * p.E + e] : 0.f;
-      before[i] = 0;
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) mine[i] = order_key(own[i], e);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lrow = lane & 15, lgrp = lane >> 4;
+  if (!kRouted && (int)blockIdx.x < route_blocks) {
+    if (wave < p.T) route_token<1>(p, wave, lane);
+    return;
+  }
+  const int tiles = p.I / 16, block = kRouted ? blockIdx.x : blockIdx.x - route_blocks;
+  const int el = block / tiles, tile = block % tiles;
+  if (threadIdx.x < kMoeMaxTokens) slot_of[threadIdx.x] = -1;
+  __syncthreads();
+  if constexpr (kRouted) {
+    for (int i = threadIdx.x; i < p.T * p.top_k; i += kB)
+      if (p.slot_expert[i] == p.first + el) slot_of[i / p.top_k] = i;
+  } else if (wave < p.T) {
+    const int e = p.first + el;
+    const uint32_t mine = order_bits(choice_value(p, logit(p, wave, e, true), e));
+    int before = 0;
     for (int c = 0; c < p.E; c += 64) {
-      float v[kPer];
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int t = wave + i * kW;
-        v[i] = t < p.T && c + lane < p.E ? p.value[t * p.E + c + lane] : 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        before[i] += __popcll(__ballot(c + lane < p.E && order_key(v[i], c + lane) > mine[i]));
+      const int ce = c + lane;
+      const uint32_t k = ce < p.E ? order_bits(choice_value(p, logit(p, wave, ce, true), ce)) : 0u;
+      before += __popcll(__ballot(k > mine || (k == mine && ce < e)));
     }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int t = wave + i * kW;
-      if (lane == 0) slot_of[t] = t < p.T && before[i] < p.top_k ? before[i] : -1;
-    }
+    if (lane == 0 && before < p.top_k) slot_of[wave] = wave * p.top_k + before;
   }
   __syncthreads();
   if (wave == 0) {
@@ -361,12 +397,12 @@ __global__ __launch_bounds__(kB, 4) void moe_up_kernel(MoeProblem p, int route_b
     const int at = __popcll(mask & ((1ull << lane) - 1));
     if (s >= 0) {
       list_t[at] = lane;
-      list_slot[at] = lane * p.top_k + s;
+      list_slot[at] = s;
     }
     if (lane == 0) count = __popcll(mask);
     if (tile == 0) {   // for the down kernel
       if (lane == 0) p.counts[el] = __popcll(mask);
-      if (s >= 0) p.lists[el * kMoeMaxTokens + at] = lane * p.top_k + s;
+      if (s >= 0) p.lists[el * kMoeMaxTokens + at] = s;
     }
   }
   __syncthreads();
@@ -375,7 +411,7 @@ __global__ __launch_bounds__(kB, 4) void moe_up_kernel(MoeProblem p, int route_b
 
   // column group j of the sums: a lane has 4 channels of one token
   auto finish = [&](int j, const v4f& ag, const v4f& au) {
-    if (j > 0) __syncthreads();
+    __syncthreads();
     part[wave][0][lane] = ag;
     part[wave][1][lane] = au;
     __syncthreads();
@@ -395,28 +431,87 @@ __global__ __launch_bounds__(kB, 4) void moe_up_kernel(MoeProblem p, int route_b
       *reinterpret_cast<float4*>(p.h + (int64_t)list_slot[j * 16 + lrow] * p.I + tile * 16 + lgrp * 4) = h;
     }
   };
-  if (n <= 16) {
-    v4f ag[1], au[1];
-    up_sums<1>(p, el, tile, list_t, n, wave, lane, ag, au);
-    finish(0, ag[0], au[0]);
-  } else if (n <= 32) {
-    v4f ag[2], au[2];
-    up_sums<2>(p, el, tile, list_t, n, wave, lane, ag, au);
+  // an expert with more than 16 NT tokens reads its weights again, from the
+  // last-level cache
+  for (int j0 = 0; j0 * 16 < n; j0 += NT) {
+    v4f ag[NT], au[NT];
+    up_sums<NT>(p, el, tile, list_t + j0 * 16, n - j0 * 16, wave, lane, ag, au);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) finish(j, ag[j], au[j]);
-  } else {
-    v4f ag[4], au[4];
-    up_sums<4>(p, el, tile, list_t, n, wave, lane, ag, au);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) finish(j, ag[j], au[j]);
+    for (int j = 0; j < NT; ++j)
+      if ((j0 + j) * 16 < n) finish(j0 + j, ag[j], au[j]);
   }
 }
 
-// 3. The 1x128 quantization of h (FP32 in): a tile spans eight workgroups of
-//    the up kernel, so it waits for the next launch.
-__global__ __launch_bounds__(kPB) void moe_quant_kernel(MoeProblem p) {
+// The plan of the down kernel: the chosen held experts' tokens in parts of at
+// most `span`.  plan[0] = parts, then [most] each part's expert, [most + 1] the
+// first of its slots, [T top_k] the slots and [T top_k] their gates (FP32).
+__host__ __device__ inline int plan_parts(const MoeProblem& p) {
+  const int slots = p.T * p.top_k;
+  return (p.local < slots ? p.local : slots) + slots / 16;
+}
+__device__ __forceinline__ void make_plan(const MoeProblem& p, int span) {
+  __shared__ int16_t active[kMoeMaxTokens * kMoeMaxTopK + kMoeMaxTokens * kMoeMaxTopK / 16];
+  __shared__ int16_t first[kMoeMaxTokens * kMoeMaxTopK + kMoeMaxTokens * kMoeMaxTopK / 16 + 1];
+  __shared__ int n_parts;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, most = plan_parts(p);
+  int32_t* plan_expert = p.plan + 1;
+  int32_t* plan_start = plan_expert + most;
+  int32_t* plan_slot = plan_start + most + 1;
+  float* plan_gate = reinterpret_cast<float*>(plan_slot + p.T * p.top_k);
+  if (wave == 0) {
+    int np = 0, ns = 0;
+    for (int c = 0; c < p.local; c += 64) {
+      const int cnt = c + lane < p.local ? p.counts[c + lane] : 0;
+      const int parts = (cnt + span - 1) / span;
+      int ic = cnt, ip = parts;     // inclusive sums over the lanes
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int oc = __shfl_up(ic, d), op = __shfl_up(ip, d);
+        if (lane >= d) {
+          ic += oc;
+          ip += op;
+        }
+      }
+      for (int q = 0; q < parts; ++q) {
+        const int at = np + ip - parts + q, s0 = ns + ic - cnt + q * span;
+        active[at] = (int16_t)(c + lane);
+        first[at] = (int16_t)s0;
+        plan_expert[at] = c + lane;
+        plan_start[at] = s0;
+      }
+      np += __shfl(ip, 63);
+      ns += __shfl(ic, 63);
+    }
+    if (lane == 0) {
+      n_parts = np;
+      first[np] = (int16_t)ns;
+      plan_start[np] = ns;
+      p.plan[0] = np;
+    }
+  }
+  __syncthreads();
+  for (int a = wave; a < n_parts; a += kW) {
+    int head = a;                   // the expert's first part
+    while (head > 0 && active[head - 1] == active[a]) --head;
+    const int n = first[a + 1] - first[a];
+    if (lane < n) {
+      const int s = p.lists[active[a] * kMoeMaxTokens + (a - head) * span + lane];
+      plan_slot[first[a] + lane] = s;
+      plan_gate[first[a] + lane] = p.slot_gate[s];
+    }
+  }
+}
+
+// 4. The 1x128 quantization of h (FP32 in): a tile spans eight workgroups of
+//    the up kernel, so it waits for the next launch.  The first block makes the
+//    down kernel's plan meanwhile.
+__global__ __launch_bounds__(kB) void moe_quant_kernel(MoeProblem p, int span) {
+  if (blockIdx.x == 0) {
+    make_plan(p, span);
+    return;
+  }
   const int kb_n = p.I / 128;
-  const int tile = blockIdx.x * (kPB / 16) + (threadIdx.x >> 4), l16 = threadIdx.x & 15;
+  const int tile = (blockIdx.x - 1) * (kB / 16) + (threadIdx.x >> 4), l16 = threadIdx.x & 15;
   if (tile >= p.T * p.top_k * kb_n) return;
   const int slot = tile / kb_n, kb = tile - slot * kb_n;
   const int el = p.slot_expert[slot] - p.first;
@@ -433,71 +528,51 @@ __global__ __launch_bounds__(kPB) void moe_quant_kernel(MoeProblem p) {
   if (l16 == 0) p.hs[slot * kb_n + kb] = s;
 }
 
-// 4. y: a workgroup has 16 output channels of every token.  The (expert, K
-//    block) units are dealt to the waves in equal runs; a wave adds gate x its
-//    sums into its own copy of the outputs in LDS when its expert ends, and
-//    the copies are summed in wave order at the end, so that the result does
-//    not depend on timing.  The next unit's weights are loaded before the
-//    present one's products, across experts too.
-template <int NT>
-__global__ __launch_bounds__(kPB) void moe_down_kernel(MoeProblem p) {
-  __shared__ float out[kPW][NT * 16][16 + 4];
-  __shared__ int slots[kMoeMaxTokens * kMoeMaxTopK];    // the chosen slots, expert by expert
-  __shared__ int16_t active[kMoeMaxExperts];            // chosen held experts
-  __shared__ int16_t start[kMoeMaxExperts + 1];         // the first of each one's slots
-  __shared__ int n_active;
+// A unit of the down kernel as loaded: the weights, and the codes and scales
+// of the expert's first 16 tokens.
+struct DownLoads {
+  Block w, x;
+  float sh, f;
+};
+
+// 5. y: a workgroup has 16 output channels of every token.  The plan's (part,
+//    K block) units are dealt to the waves in equal runs.  A wave adds gate x its
+//    sums into its own copy of the outputs in LDS when a part ends, and the
+//    copies are summed in wave order at the end, so that the result does not
+//    depend on timing.  The next unit is loaded before the present one's
+//    products, across parts too.
+template <int NT, int DW>
+__global__ __launch_bounds__(DW * 64) void moe_down_kernel(MoeProblem p) {
+  extern __shared__ float out[];      // [DW][T][20], 16 of 20 used, then the plan
+  constexpr int kDB = DW * 64;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lrow = lane & 15, lgrp = lane >> 4;
-  for (int i = threadIdx.x; i < kPW * NT * 16 * 20; i += kPB) (&out[0][0][0])[i] = 0.f;
-  if (wave == 0) {
-    int na = 0, ns = 0;
-    for (int c = 0; c < p.local; c += 64) {
-      const int cnt = c + lane < p.local ? p.counts[c + lane] : 0;
-      int incl = cnt;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(incl, d);
-        if (lane >= d) incl += o;
-      }
-      const uint64_t mask = __ballot(cnt > 0);
-      const int at = na + __popcll(mask & ((1ull << lane) - 1));
-      if (cnt > 0) {
-        active[at] = (int16_t)(c + lane);
-        start[at] = (int16_t)(ns + incl - cnt);
-      }
-      na += __popcll(mask);
-      ns += __shfl(incl, 63);
-    }
-    if (lane == 0) {
-      n_active = na;
-      start[na] = (int16_t)ns;
-    }
-  }
-  __syncthreads();
-  const int na = n_active;
-  for (int a = wave; a < na; a += kPW) {
-    const int n = start[a + 1] - start[a];
-    if (lane < n) slots[start[a] + lane] = p.lists[active[a] * kMoeMaxTokens + lane];
-  }
+  const int most = plan_parts(p), n_plan = 2 + 2 * most + 2 * p.T * p.top_k;
+  int32_t* plan = reinterpret_cast<int32_t*>(out + DW * p.T * 20);
+  for (int i = threadIdx.x; i < n_plan; i += kDB) plan[i] = p.plan[i];
+  for (int i = threadIdx.x; i < DW * p.T * 20; i += kDB) out[i] = 0.f;
+  const int32_t* active = plan + 1;
+  const int32_t* start = active + most;
+  const int32_t* slots = start + most + 1;
+  const float* gates = reinterpret_cast<const float*>(slots + p.T * p.top_k);
   __syncthreads();
 
   const int tile = blockIdx.x, kb_n = p.I / 128;
-  const int units = na * kb_n;
-  const int u0 = (int)((int64_t)units * wave / kPW), u1 = (int)((int64_t)units * (wave + 1) / kPW);
+  const int units = plan[0] * kb_n;
+  const int u0 = (int)((int64_t)units * wave / DW), u1 = (int)((int64_t)units * (wave + 1) / DW);
   if (u0 < u1) {
     int a = u0 / kb_n, kb = u0 - a * kb_n;      // the unit at hand
-    int na_ = a, nkb = kb;                      // the unit being fetched
-    auto advance = [&](int& ea, int& ek) {
-      if (++ek == kb_n) {
-        ek = 0;
-        ++ea;
+    int fa = a, fk = kb, left = u1 - u0;        // the unit to fetch next, and how many are left
+    auto fetch = [&](DownLoads& f) {
+      const int el = active[fa], s0 = start[fa];
+      const int s = slots[s0 + (lrow < start[fa + 1] - s0 ? lrow : 0)];
+      f.w = load_tile(p.w2 + ((int64_t)el * (p.H / 16) + tile) * kb_n * 2048 + (int64_t)fk * 2048, lane);
+      f.x = load_row(p.hq + (int64_t)s * p.I + fk * 128, lgrp);
+      f.sh = p.hs[s * kb_n + fk];
+      f.f = p.s2[((int64_t)el * (p.H / 128) + tile / 8) * kb_n + fk];
+      if (--left > 0 && ++fk == kb_n) {         // past the wave's last unit: that unit again, not used
+        fk = 0;
+        ++fa;
       }
-    };
-    Block w0, w1;
-    float f0, f1;
-    auto fetch = [&](Block& w, float& f) {
-      const int el = active[na_];
-      w = load_tile(p.w2 + ((int64_t)el * (p.H / 16) + tile) * kb_n * 2048 + (int64_t)nkb * 2048, lane);
-      f = p.s2[((int64_t)el * (p.H / 128) + tile / 8) * kb_n + nkb];
     };
     int n = 0, slot[NT];
     v4f acc[NT];
@@ -511,12 +586,12 @@ __global__ __launch_bounds__(kPB) void moe_down_kernel(MoeProblem p) {
         acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
       }
     };
-    auto flush = [&]() {
+    auto flush = [&](int fl) {
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         if (j * 16 + lrow < n) {
-          const float g = p.slot_gate[slot[j]];
-          float4* o = reinterpret_cast<float4*>(&out[wave][slot[j] / p.top_k][lgrp * 4]);
+          const float g = gates[start[fl] + j * 16 + lrow];
+          float4* o = reinterpret_cast<float4*>(&out[(wave * p.T + slot[j] / p.top_k) * 20 + lgrp * 4]);
           float4 v = *o;
           v.x = __builtin_fmaf(acc[j][0], g, v.x);
           v.y = __builtin_fmaf(acc[j][1], g, v.y);
@@ -526,51 +601,49 @@ __global__ __launch_bounds__(kPB) void moe_down_kernel(MoeProblem p) {
         }
       }
     };
-    auto unit = [&](const Block& w, float f) {
-      const v8i wa = as_operand(w);
+    int u = u0;
+    // the unit's products; false after the wave's last one
+    auto step = [&](const DownLoads& l) {
+      const v8i wa = as_operand(l.w);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         if (j * 16 < n) {
-          const v8i b = as_operand(load_row(p.hq + (int64_t)slot[j] * p.I + kb * 128, lgrp));
-          const float c = p.hs[slot[j] * kb_n + kb] * f;
+          const v8i b = as_operand(j == 0 ? l.x : load_row(p.hq + (int64_t)slot[j] * p.I + kb * 128, lgrp));
+          const float c = (j == 0 ? l.sh : p.hs[slot[j] * kb_n + kb]) * l.f;
           const v4f zero = {0.f, 0.f, 0.f, 0.f};
           const v4f q = mfma_e4m3_16x16x128(wa, b, zero);
 #pragma unroll
           for (int v = 0; v < 4; ++v) acc[j][v] = __builtin_fmaf(q[v], c, acc[j][v]);
         }
       }
-    };
-    auto step = [&](const Block& w, float f, bool last) {
-      unit(w, f);
-      advance(a, kb);
-      if (last || kb == 0) {
-        flush();
-        if (!last) begin();
+      const int part = a;
+      if (++kb == kb_n) {
+        kb = 0;
+        ++a;
       }
+      const bool more = ++u < u1;
+      if (!more || kb == 0) {
+        flush(part);
+        if (more) begin();
+      }
+      return more;
     };
+    DownLoads l0, l1;
     begin();
-    fetch(w0, f0);
-    for (int u = u0; u < u1; u += 2) {
-      const bool more = u + 1 < u1;
-      if (more) {
-        advance(na_, nkb);
-        fetch(w1, f1);
-      }
-      step(w0, f0, !more);
-      if (!more) break;
-      if (u + 2 < u1) {
-        advance(na_, nkb);
-        fetch(w0, f0);
-      }
-      step(w1, f1, u + 2 >= u1);
+    fetch(l0);
+    for (;;) {
+      fetch(l1);
+      if (!step(l0)) break;
+      fetch(l0);
+      if (!step(l1)) break;
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < p.T * 16; i += kPB) {
+  for (int i = threadIdx.x; i < p.T * 16; i += kDB) {
     const int t = i >> 4, c = i & 15;
-    float v = out[0][t][c];
+    float v = out[t * 20 + c];
 #pragma unroll
-    for (int w = 1; w < kPW; ++w) v += out[w][t][c];
+    for (int w = 1; w < DW; ++w) v += out[(w * p.T + t) * 20 + c];
     store_out(p.y, t * p.ldy + tile * 16 + c, p.y_fp32, v);
   }
 }
@@ -579,112 +652,129 @@ __global__ __launch_bounds__(kPB) void moe_down_kernel(MoeProblem p) {
 // Low-rank adapters beside a shared projection.
 // ===========================================================================
 
-// z[t] = scale_a (A_a x_t) goes to memory as the expand's products take it:
-// for every 8 ranks the 8 BF16 terms hi, then the 8 BF16 terms lo of z = hi +
-// lo (to 2^-17 of z), so it is split once here and not by every reader.
-__device__ __forceinline__ void store_z(uint16_t* zrow, int r0, const v4f& c, float s) {
-  typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
-  v4bf hi, lo;
+// The shrink z[t] = scale_a (A_a x_t) leaves FP32 partial sums zp[s][t][rank],
+// one per share of K; z8 adds 8 of them in order, scales them and gives the
+// expand's operands: z = hi + lo in BF16, to 2^-17 of z, so that the products
+// with both terms lose nothing that FP32 sums would keep.  A token without an
+// adapter has no sums (zeros here); an id past the last one gives NaN.
+__device__ __forceinline__ void z8(const AdapterProblem& p, int64_t t, int r, v8bf& hi, v8bf& lo) {
+  float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const int id = p.ids[t];
+  if (id >= 0) {
+    float4 u[kAdapterSplits][2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float z = c[i] * s;
-    hi[i] = (__bf16)z;
-    const float d = z - (float)hi[i];
+    for (int s = 0; s < kAdapterSplits; ++s) {
+      const float4* src = reinterpret_cast<const float4*>(p.zp + ((int64_t)s * p.T + t) * p.r + r);
+      u[s][0] = u[s][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s < p.splits && id < p.n) {
+        u[s][0] = src[0];
+        u[s][1] = src[1];
+      }
+    }
+    const float scale = id >= p.n ? NAN : p.scales != nullptr ? p.scales[id] : 1.0f;
+#pragma unroll
+    for (int s = 0; s < kAdapterSplits; ++s) {
+      z[0] += u[s][0].x; z[1] += u[s][0].y; z[2] += u[s][0].z; z[3] += u[s][0].w;
+      z[4] += u[s][1].x; z[5] += u[s][1].y; z[6] += u[s][1].z; z[7] += u[s][1].w;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] *= scale;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    hi[i] = (__bf16)z[i];
+    const float d = z[i] - (float)hi[i];
     lo[i] = (__bf16)(d == d ? d : 0.f);   // Inf and NaN sit in hi
   }
-  uint16_t* at = zrow + (r0 >> 3) * 16 + (r0 & 7);
-  *reinterpret_cast<v4bf*>(at) = hi;
-  *reinterpret_cast<v4bf*>(at + 8) = lo;
 }
 
 // The ids of a chunk of 16 tokens (in every 16-lane group; -1 past the last
-// token) and which of them have an adapter.
+// token) and which of them have an adapter that exists.
 __device__ __forceinline__ uint32_t chunk_ids(const AdapterProblem& p, int64_t t0, int lrow, int& id) {
   id = t0 + lrow < p.T ? p.ids[t0 + lrow] : -1;
+  if (id >= p.n) id = -1;
   return (uint32_t)(__ballot(id >= 0) & 0xFFFFull);
 }
 
-// z of the chunk's tokens with adapter a, 16 rows of A: every wave's partial
-// sums meet in LDS.  An id past the last adapter gives NaN.
-__device__ __forceinline__ void shrink_rows(const AdapterProblem& p, int64_t t0, int rt, int a, int id,
-                                            v4f (*part)[64]) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lrow = lane & 15, lgrp = lane >> 4;
-  const int row = rt * 16 + lrow < p.r ? rt * 16 + lrow : p.r - 1;
-  const uint16_t* xr = p.x + (t0 + lrow < p.T ? t0 + lrow : t0) * p.ldx;
-  v4f c = {NAN, NAN, NAN, NAN};
-  if (a < p.n) c = dot_rows_bf16(p.A + ((int64_t)a * p.r + row) * p.K, xr, (int)p.K, wave, lgrp);
-  __syncthreads();
-  part[wave][lane] = c;
-  __syncthreads();
-  const int r0 = rt * 16 + lgrp * 4;
-  if (wave == 0 && id == a && r0 < p.r) {
-    c = part[0][lane];
-#pragma unroll
-    for (int w = 1; w < kPW; ++w) c += part[w][lane];
-    store_z(p.z + (t0 + lrow) * 2 * p.r, r0, c, p.scales != nullptr && a < p.n ? p.scales[a] : 1.0f);
-  }
-}
-
 // 1. Few tokens: the quantization of x, and the shrink: workgroup (chunk of 16
-//    tokens, 16 rows of A, one of `step` shares of the chunk's adapters, which
-//    are taken in the order of their first token).
-__global__ __launch_bounds__(kPB) void adapter_prepare_kernel(AdapterProblem p, int shrink_blocks, int step) {
-  __shared__ v4f part[kPW][64];
-  const int b = blockIdx.x;
+//    tokens, 16 rows of A, share of K, one of `step` shares of the chunk's
+//    adapters, which are taken in the order of their first token).
+__global__ __launch_bounds__(kB) void adapter_prepare_kernel(AdapterProblem p, int shrink_blocks, int step) {
+  __shared__ v4f part[kW][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lrow = lane & 15, lgrp = lane >> 4;
+  int b = blockIdx.x;
   if (b >= shrink_blocks) {
     quant_tokens(p.x, p.ldx, (int)p.T, (int)p.K, b - shrink_blocks, p.xq, p.xs);
     return;
   }
-  const int rts = (p.r + 15) / 16;
-  const int first = b % step, rt = (b / step) % rts;
-  const int64_t t0 = (int64_t)(b / (step * rts)) * 16;
+  const int rts = (p.r + 15) / 16, kb_n = (int)(p.K / 128);
+  const int first = b % step;
+  b /= step;
+  const int s = b % p.splits;
+  b /= p.splits;
+  const int rt = b % rts;
+  const int64_t t0 = (int64_t)(b / rts) * 16;
+  const int row = rt * 16 + lrow < p.r ? rt * 16 + lrow : p.r - 1, r0 = rt * 16 + lgrp * 4;
+  const uint16_t* xr = p.x + (t0 + lrow < p.T ? t0 + lrow : t0) * p.ldx;
   int id;
-  uint32_t left = chunk_ids(p, t0, threadIdx.x & 15, id);
+  uint32_t left = chunk_ids(p, t0, lrow, id);
   for (int turn = 0; left != 0; ++turn) {
     const int a = __shfl(id, __builtin_ctz(left));
     left &= ~(uint32_t)__ballot(id == a);
-    if (turn % step == first) shrink_rows(p, t0, rt, a, id, part);
+    if (turn % step != first) continue;
+    __syncthreads();
+    part[wave][lane] = dot_rows_bf16(p.A + ((int64_t)a * p.r + row) * p.K, xr, share(kb_n, s, p.splits),
+                                     share(kb_n, s + 1, p.splits), wave, lgrp);
+    __syncthreads();
+    if (wave == 0 && id == a && r0 < p.r) {
+      v4f c = part[0][lane];
+#pragma unroll
+      for (int w = 1; w < kW; ++w) c += part[w][lane];
+      *reinterpret_cast<v4f*>(p.zp + ((int64_t)s * p.T + t0 + lrow) * p.r + r0) = c;
+    }
   }
 }
 
 // Prompts: the quantization of x (codes and MN-major scales as the row
-// quantizer writes them) and the shrink in one pass over x: a workgroup has 16
-// tokens, its waves deal the K blocks.  A lane holds 32 values of one token's
-// 1x128 tile, which are both the quantizer's input and the products' operand.
-// The tokens of the chunk's first adapter get their products in that pass;
-// further adapters in the chunk take another over x (from L2).
+// quantizer writes them) and the shrink in one pass over x: workgroup (chunk
+// of 16 tokens, share of K), its waves dealing the K blocks.  A lane holds 32
+// values of one token's 1x128 tile, which are both the quantizer's input and
+// the products' operand.  The adapters of the chunk take turns on the same
+// accumulators: a column belongs to one token, and its sums are kept only in
+// its own adapter's turn (a select, not a product with zero, so that an
+// adapter with infinite weights stays among its own tokens).
 template <int RT>
-__global__ __launch_bounds__(kPB) void adapter_prompt_kernel(AdapterProblem p, int64_t ld_s) {
-  __shared__ v4f part[RT][kPW][64];
+__global__ __launch_bounds__(kB) void adapter_prompt_kernel(AdapterProblem p, int64_t ld_s) {
+  __shared__ v4f part[kW][RT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lrow = lane & 15, lgrp = lane >> 4;
-  const int64_t t0 = (int64_t)blockIdx.x * 16, t = t0 + lrow;
+  const int s = blockIdx.x % p.splits, kb_n = (int)(p.K / 128);
+  const int64_t t0 = (int64_t)(blockIdx.x / p.splits) * 16, t = t0 + lrow;
   const bool in = t < p.T;
   int id;
-  uint32_t left = chunk_ids(p, t0, lrow, id);
-  const int lead = left != 0 ? __shfl(id, __builtin_ctz(left)) : -1;
-  const bool dot = lead >= 0 && lead < p.n;
+  const uint32_t any = chunk_ids(p, t0, lrow, id);
   const uint16_t* xr = p.x + (in ? t : t0) * p.ldx + lgrp * 8;
-  const uint16_t* ar[RT];
   v4f acc[RT];
+  int64_t arow[RT];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
-    const int row = rt * 16 + lrow < p.r ? rt * 16 + lrow : p.r - 1;
-    ar[rt] = p.A + ((int64_t)(dot ? lead : 0) * p.r + row) * p.K + lgrp * 8;
+    arow[rt] = (rt * 16 + lrow < p.r ? rt * 16 + lrow : p.r - 1) * p.K + lgrp * 8;
     acc[rt] = v4f{0.f, 0.f, 0.f, 0.f};
   }
-  const int kb_n = (int)(p.K / 128);
-  for (int kb = wave; kb < kb_n; kb += kPW) {
+  for (int kb = share(kb_n, s, p.splits) + wave; kb < share(kb_n, s + 1, p.splits); kb += kW) {
     fv4i x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const fv4i*>(xr + kb * 128 + i * 32);
-    if (dot) {
+    for (uint32_t left = any; left != 0;) {
+      const int a = __shfl(id, __builtin_ctz(left));
+      left &= ~(uint32_t)__ballot(id == a);
+      const uint16_t* A = p.A + (int64_t)a * p.r * p.K + kb * 128;
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        fv4i a[4];
+        v4f c = acc[rt];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const fv4i*>(ar[rt] + kb * 128 + i * 32);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[rt] = mfma_bf16_16x16x32(as_bf16x8(a[i]), as_bf16x8(x[i]), acc[rt]);
+        for (int i = 0; i < 4; ++i)
+          c = mfma_bf16_16x16x32(as_bf16x8(*reinterpret_cast<const fv4i*>(A + arow[rt] + i * 32)), as_bf16x8(x[i]), c);
+        if (id == a) acc[rt] = c;
       }
     }
     uint32_t m = 0;
@@ -698,43 +788,51 @@ __global__ __launch_bounds__(kPB) void adapter_prompt_kernel(AdapterProblem p, i
     m = max(h[0], h[1]);
     const auto f = __builtin_amdgcn_permlane32_swap(m, m, false, false);
     m = max(f[0], f[1]);
-    float s = 0.f;
+    float sc = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint2 q = quant8_bf16_tile(d[i], m, s);
+      const uint2 q = quant8_bf16_tile(d[i], m, sc);
       if (in) *reinterpret_cast<uint2*>(p.xq + t * p.K + kb * 128 + i * 32 + lgrp * 8) = q;
     }
-    if (in && lgrp == 0) p.xs[kb * ld_s + t] = s;
+    if (in && lgrp == 0) p.xs[kb * ld_s + t] = sc;
   }
-  if (left == 0) return;
+  if (any == 0) return;
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) part[rt][wave][lane] = acc[rt];
+  for (int rt = 0; rt < RT; ++rt) part[wave][rt][lane] = acc[rt];
   __syncthreads();
-  for (int rt = wave; rt < RT; rt += kPW) {
+  for (int rt = wave; rt < RT; rt += kW) {
     const int r0 = rt * 16 + lgrp * 4;
-    if (id == lead && r0 < p.r) {
-      v4f c = part[rt][0][lane];
+    if (id >= 0 && r0 < p.r) {
+      v4f c = part[0][rt][lane];
 #pragma unroll
-      for (int w = 1; w < kPW; ++w) c += part[rt][w][lane];
-      if (!dot) c = v4f{NAN, NAN, NAN, NAN};
-      store_z(p.z + t * 2 * p.r, r0, c, p.scales != nullptr && dot ? p.scales[lead] : 1.0f);
+      for (int w = 1; w < kW; ++w) c += part[w][rt][lane];
+      *reinterpret_cast<v4f*>(p.zp + ((int64_t)s * p.T + t) * p.r + r0) = c;
     }
-  }
-  left &= ~(uint32_t)__ballot(id == lead);
-  while (left != 0) {
-    const int a = __shfl(id, __builtin_ctz(left));
-    left &= ~(uint32_t)__ballot(id == a);
-    for (int rt = 0; rt < (p.r + 15) / 16; ++rt) shrink_rows(p, t0, rt, a, id, part[0]);
   }
 }
 
-// 2. Few tokens: projection and expand, 16 RT output columns a workgroup; the
-//    next K block's weights are loaded before the present one's products.
+// Prompts: the sums over the shares of K, as the GEMM's epilogue reads them
+// (for every 8 ranks the 8 terms hi, then the 8 terms lo).
+__global__ __launch_bounds__(256) void adapter_z_kernel(AdapterProblem p) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int r8 = p.r / 8;
+  if (i >= p.T * r8) return;
+  v8bf hi, lo;
+  z8(p, i / r8, (int)(i % r8) * 8, hi, lo);
+  reinterpret_cast<v8bf*>(p.z)[2 * i] = hi;
+  reinterpret_cast<v8bf*>(p.z)[2 * i + 1] = lo;
+}
+
+// 2. Few tokens: projection and expand, 16 RT output columns a workgroup (with
+//    two tiles every token operand is used twice, and half as many are read
+//    from L2); the next K block's weights are loaded before the present one's
+//    products.
 template <int NT, int RT>
-__global__ __launch_bounds__(kB, (NT > 2 && RT > 1) ? 2 : 4) void adapter_project_kernel(AdapterProblem p) {
+__global__ __launch_bounds__(kB, 4) void adapter_project_kernel(AdapterProblem p) {
   __shared__ v4f part[kW][RT][NT][64];
+  extern __shared__ v8bf zs[];            // [T][r / 8][hi, lo]
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lrow = lane & 15, lgrp = lane >> 4;
-  const int tile = blockIdx.x * RT, kb_n = (int)(p.K / 128), T = (int)p.T;
+  const int tile = blockIdx.x * RT, kb_n = (int)(p.K / 128), T = (int)p.T, r8 = p.r / 8;
   const uint8_t* w = p.W + (int64_t)tile * kb_n * 2048;
   const float* sw = p.sW + (tile / 8) * p.ld_sw;      // RT divides 8: one block row
   int tok[NT];
@@ -749,69 +847,101 @@ __global__ __launch_bounds__(kB, (NT > 2 && RT > 1) ? 2 : 4) void adapter_projec
 #pragma unroll
     for (int i = 0; i < RT; ++i) a[i] = load_tile(w + ((int64_t)i * kb_n + kb) * 2048, lane);
   };
-  auto products = [&](int kb, const Block (&a)[RT]) {
-    const float f = sw[kb];
+  // the batch's adapters, in the order of their first token, and the tokens of each
+  __shared__ int adapter[kAdapterFewTokens];
+  __shared__ uint64_t member[kAdapterFewTokens];
+  __shared__ int n_adapters;
+  const int last = kb_n - 1;
+  Block a0[RT], a1[RT];
+  fetch(min(wave, last), a0);
+  if (wave == kW - 1) {
+    const int id = lane < T ? p.ids[lane] : -1;
+    uint64_t left = __ballot(id >= 0);
+    int n = 0;
+    while (left != 0) {
+      const int a = __shfl(id, __builtin_ctzll(left));
+      const uint64_t m = __ballot(id == a);
+      left &= ~m;
+      if (lane == 0) {
+        adapter[n] = a < p.n ? a : 0;      // its tokens' z is NaN
+        member[n] = m;
+      }
+      ++n;
+    }
+    if (lane == 0) n_adapters = n;
+  }
+  for (int i = threadIdx.x; i < T * r8; i += kB) z8(p, i / r8, (i % r8) * 8, zs[2 * i], zs[2 * i + 1]);
+  __syncthreads();
+
+  const v8bf none = __builtin_bit_cast(v8bf, fv4i{0, 0, 0, 0});
+  const int n_ad = n_adapters;
+  auto fetch_b = [&](int turn, int r0, v8bf (&bw)[RT]) {
+    const uint16_t* brow = p.B + ((int64_t)adapter[turn] * p.N + tile * 16 + lrow) * p.r;
+    const int r = r0 + lgrp * 8;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+      bw[i] = r < p.r ? *reinterpret_cast<const v8bf*>(brow + (int64_t)i * 16 * p.r + r) : none;
+  };
+  // a column's sums are kept in its own adapter's turn
+  auto expand = [&](int turn, int r0, const v8bf (&bw)[RT]) {
+    const uint64_t members = member[turn];
+    const int r = r0 + lgrp * 8;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const uint32_t m = (uint32_t)(members >> (16 * j)) & 0xFFFFu;
+      if (m == 0) continue;
+      const int at = 2 * (tok[j] * r8 + r / 8);
+      const v8bf hi = r < p.r ? zs[at] : none, lo = r < p.r ? zs[at + 1] : none;
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const v4f c = mfma_bf16_16x16x32(bw[i], lo, mfma_bf16_16x16x32(bw[i], hi, acc[i][j]));
+        if ((m >> lrow) & 1) acc[i][j] = c;
+      }
+    }
+  };
+  // One K block and one of the wave's adapters a step.  Loads return in the
+  // order of their issue: the token operands of the present block are asked
+  // for first, then the next block's weights and the adapter's.
+  auto step = [&](int kb, int turn, const Block (&a)[RT], Block (&next)[RT]) {
+    const int kc = min(kb, last);        // past the wave's last block: one that is not used
     Block b[NT];
     float c[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      b[j] = load_row(p.xq + tok[j] * p.K + kb * 128, lgrp);
-      c[j] = p.xs[tok[j] * kb_n + kb] * f;
+      b[j] = load_row(p.xq + tok[j] * p.K + kc * 128, lgrp);
+      c[j] = p.xs[tok[j] * kb_n + kc];
     }
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const v8i bj = as_operand(b[j]);
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const v4f zero = {0.f, 0.f, 0.f, 0.f};
-        const v4f q = mfma_e4m3_16x16x128(as_operand(a[i]), bj, zero);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(q[v], c[j], acc[i][j][v]);
-      }
-    }
-  };
-  Block a0[RT], a1[RT];
-  if (wave < kb_n) fetch(wave, a0);
-  // the adapters of the batch, dealt to the waves in the order of their first
-  // token; the rows of other adapters enter as zero columns
-  const int id = lane < T ? p.ids[lane] : -1;
-  uint64_t left = __ballot(id >= 0);
-  for (int turn = 0; left != 0; ++turn) {
-    const int a = __shfl(id, __builtin_ctzll(left));
-    const uint64_t members = __ballot(id == a);
-    left &= ~members;
-    if (turn % kW != wave) continue;
-    const uint16_t* brow = p.B + ((int64_t)(a < p.n ? a : 0) * p.N + tile * 16 + lrow) * p.r;
-    for (int r0 = 0; r0 < p.r; r0 += 32) {
-      const int r = r0 + lgrp * 8;
-      const fv4i none = {0, 0, 0, 0};
-      fv4i bw[RT];
-#pragma unroll
-      for (int i = 0; i < RT; ++i)
-        bw[i] = r < p.r ? *reinterpret_cast<const fv4i*>(brow + (int64_t)i * 16 * p.r + r) : none;
+    __asm__ volatile("" ::: "memory");
+    v8bf bw[RT];
+    const bool ad = turn < n_ad;
+    fetch(min(kb + kW, last), next);
+    if (ad) fetch_b(turn, 0, bw);
+    if (kb < kb_n) {
+      const float f = sw[kb];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const uint32_t m = (uint32_t)(members >> (16 * j)) & 0xFFFFu;
-        if (m == 0) continue;
-        const bool on = ((m >> lrow) & 1) && r < p.r;
-        const uint16_t* z = p.z + (int64_t)tok[j] * 2 * p.r + 2 * r;
-        const fv4i hi = on ? *reinterpret_cast<const fv4i*>(z) : none;
-        const fv4i lo = on ? *reinterpret_cast<const fv4i*>(z + 8) : none;
+        const v8i bj = as_operand(b[j]);
+        const float cj = c[j] * f;
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-          acc[i][j] = mfma_bf16_16x16x32(as_bf16x8(bw[i]), as_bf16x8(hi), acc[i][j]);
-          acc[i][j] = mfma_bf16_16x16x32(as_bf16x8(bw[i]), as_bf16x8(lo), acc[i][j]);
+          const v4f zero = {0.f, 0.f, 0.f, 0.f};
+          const v4f q = mfma_e4m3_16x16x128(as_operand(a[i]), bj, zero);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(q[v], cj, acc[i][j][v]);
         }
       }
     }
-  }
-  for (int kb = wave; kb < kb_n; kb += 2 * kW) {
-    const bool two = kb + kW < kb_n;
-    if (two) fetch(kb + kW, a1);
-    products(kb, a0);
-    if (!two) break;
-    if (kb + 2 * kW < kb_n) fetch(kb + 2 * kW, a0);
-    products(kb + kW, a1);
+    if (ad) {
+      expand(turn, 0, bw);
+      for (int r0 = 32; r0 < p.r; r0 += 32) {
+        fetch_b(turn, r0, bw);
+        expand(turn, r0, bw);
+      }
+    }
+  };
+  for (int kb = wave, turn = wave; kb < kb_n || turn < n_ad; kb += 2 * kW, turn += 2 * kW) {
+    step(kb, turn, a0, a1);
+    step(kb + kW, turn + kW, a1, a0);
   }
 #pragma unroll
   for (int i = 0; i < RT; ++i)
@@ -838,36 +968,61 @@ __global__ __launch_bounds__(kB, (NT > 2 && RT > 1) ? 2 : 4) void adapter_projec
 template <int RT>
 void project(const AdapterProblem& p, hipStream_t stream) {
   const dim3 grid((unsigned)(p.N / 16 / RT));
+  const size_t lds = (size_t)p.T * p.r * 4;
   switch ((p.T + 15) / 16) {
-    case 1: hipLaunchKernelGGL((adapter_project_kernel<1, RT>), grid, dim3(kB), 0, stream, p); break;
-    case 2: hipLaunchKernelGGL((adapter_project_kernel<2, RT>), grid, dim3(kB), 0, stream, p); break;
-    case 3: hipLaunchKernelGGL((adapter_project_kernel<3, RT>), grid, dim3(kB), 0, stream, p); break;
-    default: hipLaunchKernelGGL((adapter_project_kernel<4, RT>), grid, dim3(kB), 0, stream, p); break;
+    case 1: hipLaunchKernelGGL((adapter_project_kernel<1, RT>), grid, dim3(kB), lds, stream, p); break;
+    case 2: hipLaunchKernelGGL((adapter_project_kernel<2, RT>), grid, dim3(kB), lds, stream, p); break;
+    case 3: hipLaunchKernelGGL((adapter_project_kernel<3, RT>), grid, dim3(kB), lds, stream, p); break;
+    default: hipLaunchKernelGGL((adapter_project_kernel<4, RT>), grid, dim3(kB), lds, stream, p); break;
   }
 }
 
 }  // namespace
 
+template <int NT, int DW>
+static void down_waves(const MoeProblem& p, hipStream_t stream) {
+  const size_t lds = ((size_t)DW * p.T * 20 + 2 + 2 * plan_parts(p) + 2 * p.T * p.top_k) * 4;
+  hipLaunchKernelGGL((moe_down_kernel<NT, DW>), dim3(p.H / 16), dim3(DW * 64), lds, stream, p);
+}
+// more waves a workgroup where there are too few workgroups for the card
+template <int NT>
+static void down(const MoeProblem& p, hipStream_t stream) {
+  if (p.H / 16 <= 256) down_waves<NT, 16>(p, stream);
+  else down_waves<NT, 8>(p, stream);
+}
+
 hipError_t launch_moe_few_tokens(const MoeProblem& p, hipStream_t stream) {
   const int t_tiles = (p.T + 15) / 16;
-  const int router_blocks = (p.E + 15) / 16 * t_tiles;
-  hipLaunchKernelGGL(moe_prepare_kernel, dim3(router_blocks + quant_blocks(p.T, p.H)), dim3(kPB), 0, stream, p,
+  const int router_blocks = (p.E + 15) / 16 * t_tiles * p.splits;
+  hipLaunchKernelGGL(moe_prepare_kernel, dim3(router_blocks + quant_blocks(p.T, p.H)), dim3(kB), 0, stream, p,
                      router_blocks);
-  const int route_blocks = (p.T + kW - 1) / kW;
-  hipLaunchKernelGGL(moe_up_kernel, dim3(route_blocks + p.local * (p.I / 16)), dim3(kB), 0, stream, p, route_blocks);
-  hipLaunchKernelGGL(moe_quant_kernel, dim3(quant_blocks((int64_t)p.T * p.top_k, p.I)), dim3(kPB), 0, stream, p);
-  const dim3 down(p.H / 16);
-  if (t_tiles == 1) hipLaunchKernelGGL(moe_down_kernel<1>, down, dim3(kPB), 0, stream, p);
-  else if (t_tiles == 2) hipLaunchKernelGGL(moe_down_kernel<2>, down, dim3(kPB), 0, stream, p);
-  else hipLaunchKernelGGL(moe_down_kernel<4>, down, dim3(kPB), 0, stream, p);
+  const int up = p.local * (p.I / 16);
+  const int per = p.T * p.top_k / p.E;   // tokens that an expert gets on average
+  if (p.T <= kW && p.E <= 64) {
+    hipLaunchKernelGGL((moe_up_kernel<1, false>), dim3(1 + up), dim3(kB), 0, stream, p, 1);
+  } else {
+    const dim3 route((p.T + 3) / 4);
+    if (p.E <= 64) hipLaunchKernelGGL(moe_route_kernel<1>, route, dim3(256), 0, stream, p);
+    else if (p.E <= 256) hipLaunchKernelGGL(moe_route_kernel<4>, route, dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL(moe_route_kernel<kMoeMaxExperts / 64>, route, dim3(256), 0, stream, p);
+    if (per <= 8) hipLaunchKernelGGL((moe_up_kernel<1, true>), dim3(up), dim3(kB), 0, stream, p, 0);
+    else if (per <= 24) hipLaunchKernelGGL((moe_up_kernel<2, true>), dim3(up), dim3(kB), 0, stream, p, 0);
+    else hipLaunchKernelGGL((moe_up_kernel<4, true>), dim3(up), dim3(kB), 0, stream, p, 0);
+  }
+  const int span = per <= 8 ? 16 : per <= 24 ? 32 : 64;
+  hipLaunchKernelGGL(moe_quant_kernel, dim3(1 + quant_blocks((int64_t)p.T * p.top_k, p.I)), dim3(kB), 0, stream, p,
+                     span);
+  if (span == 16) down<1>(p, stream);
+  else if (span == 32) down<2>(p, stream);
+  else down<4>(p, stream);
   return hipGetLastError();
 }
 
 hipError_t launch_adapter_few(const AdapterProblem& p, hipStream_t stream) {
   const int chunks = (int)((p.T + 15) / 16), rts = (p.r + 15) / 16;
   const int step = p.T < 16 ? (int)p.T : 16;
-  const int shrink_blocks = chunks * rts * step;
-  hipLaunchKernelGGL(adapter_prepare_kernel, dim3(shrink_blocks + quant_blocks(p.T, p.K)), dim3(kPB), 0, stream, p,
+  const int shrink_blocks = chunks * rts * step * p.splits;
+  hipLaunchKernelGGL(adapter_prepare_kernel, dim3(shrink_blocks + quant_blocks(p.T, p.K)), dim3(kB), 0, stream, p,
                      shrink_blocks, step);
   if (p.N / 16 >= kWideTiles) project<2>(p, stream);
   else project<1>(p, stream);
@@ -875,11 +1030,12 @@ hipError_t launch_adapter_few(const AdapterProblem& p, hipStream_t stream) {
 }
 
 hipError_t launch_adapter_prompt(const AdapterProblem& p, int64_t ld_s, hipStream_t stream) {
-  const dim3 grid((unsigned)((p.T + 15) / 16));
-  if (p.r <= 16) hipLaunchKernelGGL(adapter_prompt_kernel<1>, grid, dim3(kPB), 0, stream, p, ld_s);
-  else if (p.r <= 32) hipLaunchKernelGGL(adapter_prompt_kernel<2>, grid, dim3(kPB), 0, stream, p, ld_s);
-  else if (p.r <= 64) hipLaunchKernelGGL(adapter_prompt_kernel<4>, grid, dim3(kPB), 0, stream, p, ld_s);
-  else hipLaunchKernelGGL(adapter_prompt_kernel<8>, grid, dim3(kPB), 0, stream, p, ld_s);
+  const dim3 grid((unsigned)((p.T + 15) / 16 * p.splits));
+  if (p.r <= 16) hipLaunchKernelGGL(adapter_prompt_kernel<1>, grid, dim3(kB), 0, stream, p, ld_s);
+  else if (p.r <= 32) hipLaunchKernelGGL(adapter_prompt_kernel<2>, grid, dim3(kB), 0, stream, p, ld_s);
+  else if (p.r <= 64) hipLaunchKernelGGL(adapter_prompt_kernel<4>, grid, dim3(kB), 0, stream, p, ld_s);
+  else hipLaunchKernelGGL(adapter_prompt_kernel<8>, grid, dim3(kB), 0, stream, p, ld_s);
+  hipLaunchKernelGGL(adapter_z_kernel, dim3((unsigned)((p.T * (p.r / 8) + 255) / 256)), dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 

@@ -1216,7 +1216,9 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
               const int m = j * 16 + lrow, ch = i * 4 + lgrp;
               v4f* at = reinterpret_cast<v4f*>(ob + m * 256 + ((ch ^ (m & 15)) << 4));
               const v8bf b = __builtin_bit_cast(v8bf, bw[i]);
-              *at = mfma_bf16_16x16x32(b, lo, mfma_bf16_16x16x32(b, hi, *at));
+              const v4f c = mfma_bf16_16x16x32(b, lo, mfma_bf16_16x16x32(b, hi, *at));
+              // the sums of other adapters' rows stay (0 x an infinite weight is not 0)
+              if ((in >> m) & 1) *at = c;
             }
           }
         }

@@ -52,6 +52,13 @@ constexpr int64_t kNormMaxCols = 16384;
 
 // ---- the few-token expert layer ----
 constexpr int kMoeMaxTokens = 64, kMoeMaxTopK = 16, kMoeMaxExperts = 1024;
+constexpr int kMoeSplits = 8;
+// shares of a row of K that small dot products are cut into: eight waves with
+// about a 128-wide block each
+inline int dot_splits(int64_t K, int most) {
+  const int64_t s = (K / 128 + 7) / 8;
+  return (int)(s < most ? s : most);
+}
 struct MoeProblem {
   int T, H, I, E, first, local, top_k;
   const uint16_t* x;          // BF16 [T][ldx]
@@ -69,8 +76,8 @@ struct MoeProblem {
   int64_t ldy;
   int y_fp32;
   // workspace
-  float* logits;              // [T][E]
-  float* value;               // [T][E]: what experts are chosen by (logits, if there is no bias)
+  int splits;                 // shares of H that the logits are summed over
+  float* logits;              // [splits][T][E]: partial sums
   uint8_t* xq;                // [T][H]
   float* xs;                  // [T][H / 128]
   int32_t* slot_expert;       // [T][top_k]: chosen experts, best first
@@ -80,12 +87,19 @@ struct MoeProblem {
   float* hs;                  // [T top_k][I / 128]
   int32_t* counts;            // [local]: slots that chose each held expert
   int32_t* lists;             // [local][kMoeMaxTokens]: those slots (token top_k + place), in token order
+  int32_t* plan;              // [2 + 2 parts + 2 T top_k]: see make_plan; parts <= T top_k (1 + 1/16)
 };
 hipError_t launch_moe_few_tokens(const MoeProblem& p, hipStream_t stream);
 
 // ---- adapters beside a shared projection ----
 constexpr int kAdapterFewTokens = 64;   // the most tokens of the few-token form
 constexpr int kAdapterMaxRank = 128;
+constexpr int kAdapterSplits = 8;
+// shares of K of the shrink: for prompts no more than fill the card
+inline int adapter_splits(int64_t T, int64_t K) {
+  const int64_t fill = (1024 + (T + 15) / 16 - 1) / ((T + 15) / 16);
+  return dot_splits(K, (int)(fill < kAdapterSplits ? fill : kAdapterSplits));
+}
 struct AdapterProblem {
   int64_t T, N, K;
   int r, n;
@@ -104,7 +118,9 @@ struct AdapterProblem {
   // workspace
   uint8_t* xq;                // [T][K]
   float* xs;                  // few: [T][K / 128]; otherwise [K / 128][round_up(T, 4)]
-  uint16_t* z;                // [T][r / 8][16]: A x as BF16 terms hi[8], lo[8] for every 8 ranks
+  int splits;                 // adapter_splits(T, K)
+  float* zp;                  // [splits][T][r]: partial sums of A x
+  uint16_t* z;                // prompts: [T][r / 8][16]: A x as BF16 terms hi[8], lo[8] for every 8 ranks
 };
 // the few-token form (T <= kAdapterFewTokens): quantization, shrink, projection and expand
 hipError_t launch_adapter_few(const AdapterProblem& p, hipStream_t stream);
