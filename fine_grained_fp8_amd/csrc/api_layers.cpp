@@ -28,7 +28,7 @@ T* at(void* ws, int64_t off) {
 }
 
 struct MoeLayout {
-  int64_t logits, xq, xs, expert, gate, h, hq, hs, counts, lists, plan, bytes;
+  int64_t logits, xq, xs, expert, gate, h, hq, hs, counts, lists, plan, parts, bytes;
 };
 MoeLayout moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t local, int64_t k) {
   Carver c;
@@ -43,6 +43,7 @@ MoeLayout moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int64_t local, 
   l.hs = c.take(T * k * (I / 128) * 4);
   l.counts = c.take(local * 4);
   l.lists = c.take(local * fp8bs::kMoeMaxTokens * 4);
+  l.parts = c.take(fp8bs::moe_cuts(H) > 1 ? H / 16 * fp8bs::moe_cuts(H) * T * 64 : 0);
   l.plan = c.take((2 + 2 * (T * k + T * k / 16) + 2 * T * k) * 4);
   l.bytes = c.used;
   return l;
@@ -55,7 +56,7 @@ AdapterLayout adapter_layout(int64_t T, int64_t K, int64_t r) {
   Carver c;
   AdapterLayout l{};
   if (T == 0) return l;
-  l.xq = c.take(T * K);
+  l.xq = c.take((T + 15) / 16 * 16 * K);
   l.xs = c.take((K / 128) * ((T + 3) / 4 * 4) * 4);
   l.zp = c.take(fp8bs::adapter_splits(T, K) * T * r * 4);
   l.z = c.take(T * r * 4);
@@ -240,6 +241,7 @@ fp8_status fp8_moe_few_tokens(int64_t T, int64_t H, int64_t I, int32_t E, int32_
   p.counts = at<int32_t>(workspace, l.counts);
   p.lists = at<int32_t>(workspace, l.lists);
   p.plan = at<int32_t>(workspace, l.plan);
+  p.parts = at<float>(workspace, l.parts);
   return launched(fp8bs::launch_moe_few_tokens(p, reinterpret_cast<hipStream_t>(stream)));
 }
 

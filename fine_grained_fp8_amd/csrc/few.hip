@@ -22,8 +22,6 @@ typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
 constexpr int kB = 512;         // threads of a workgroup
 constexpr int kW = kB / 64;     // and its waves
-// 16-row tiles from which on a workgroup of the projection takes two of them
-constexpr int64_t kWideTiles = 1024;
 
 __device__ __forceinline__ v8bf as_bf16x8(const fv4i& v) { return __builtin_bit_cast(v8bf, v); }
 
@@ -45,9 +43,10 @@ struct Block {
 __device__ __forceinline__ Block load_tile(const uint8_t* tile, int lane) {
   return Block{*reinterpret_cast<const fv4i*>(tile + lane * 16), *reinterpret_cast<const fv4i*>(tile + 1024 + lane * 16)};
 }
-// the same of a token's row-major codes
-__device__ __forceinline__ Block load_row(const uint8_t* row, int lgrp) {
-  return Block{*reinterpret_cast<const fv4i*>(row + lgrp * 16), *reinterpret_cast<const fv4i*>(row + 64 + lgrp * 16)};
+// the same of a token's row-major codes: `block` (one for the wave) + the lane's
+// 32-bit offset, row start + 16 g (the code arrays here stay below 2^31 bytes)
+__device__ __forceinline__ Block load_row(const uint8_t* block, uint32_t lane_off) {
+  return Block{*reinterpret_cast<const fv4i*>(block + lane_off), *reinterpret_cast<const fv4i*>(block + 64 + lane_off)};
 }
 __device__ __forceinline__ v8i as_operand(const Block& b) {
   return v8i{b.lo[0], b.lo[1], b.lo[2], b.lo[3], b.hi[0], b.hi[1], b.hi[2], b.hi[3]};
@@ -128,7 +127,10 @@ __device__ __forceinline__ v4f dot_rows_bf16(const uint16_t* a, const uint16_t* 
 // their tokens.
 __device__ __forceinline__ int share(int kb_n, int s, int S) { return (int)((int64_t)kb_n * s / S); }
 
-// 1x128 quantization of token rows: 32 tiles a workgroup, 16 lanes each.
+// 1x128 quantization of token rows: 32 tiles a workgroup, 16 lanes each.  The
+// codes row-major [T][K], or (kTiled) as operand tiles of 16 tokens x 128, whose
+// loads are whole lines (16 rows of 64 bytes a load cost twice as much).
+template <bool kTiled>
 __device__ __forceinline__ void quant_tokens(const uint16_t* x, int64_t ldx, int T, int K, int block, uint8_t* xq,
                                              float* xs) {
   const int kb_n = K / 128;
@@ -138,7 +140,10 @@ __device__ __forceinline__ void quant_tokens(const uint16_t* x, int64_t ldx, int
   const fv4i d = *reinterpret_cast<const fv4i*>(x + t * ldx + kb * 128 + l16 * 8);
   float s;
   const uint2 q = quant8_bf16(make_uint4((uint32_t)d[0], (uint32_t)d[1], (uint32_t)d[2], (uint32_t)d[3]), s);
-  *reinterpret_cast<uint2*>(xq + (int64_t)t * K + kb * 128 + l16 * 8) = q;
+  const int64_t at = kTiled ? ((int64_t)(t >> 4) * kb_n + kb) * 2048 + (l16 >> 3) * 1024 +
+                                  ((l16 & 7) >> 1) * 256 + (t & 15) * 16 + (l16 & 1) * 8
+                            : (int64_t)t * K + kb * 128 + l16 * 8;
+  *reinterpret_cast<uint2*>(xq + at) = q;
   if (l16 == 0) xs[t * kb_n + kb] = s;
 }
 int quant_blocks(int64_t T, int64_t K) { return (int)((T * (K / 128) + kB / 16 - 1) / (kB / 16)); }
@@ -149,18 +154,19 @@ __device__ __forceinline__ void store_out(void* y, int64_t at, int fp32, float v
 }
 
 // ===========================================================================
-// Mixture of experts for up to 64 tokens, four or five launches.
+// Mixture of experts for up to 64 tokens, four to six launches.
 // ===========================================================================
 
 // 1. Router logits (16 experts x 16 tokens x a share of K a workgroup), and the
 //    1x128 quantization of x.
 __global__ __launch_bounds__(kB) void moe_prepare_kernel(MoeProblem p, int router_blocks) {
   if ((int)blockIdx.x >= router_blocks) {
-    quant_tokens(p.x, p.ldx, p.T, p.H, blockIdx.x - router_blocks, p.xq, p.xs);
+    quant_tokens<false>(p.x, p.ldx, p.T, p.H, blockIdx.x - router_blocks, p.xq, p.xs);
     return;
   }
   __shared__ v4f part[kW][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lrow = lane & 15, lgrp = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lrow = lane & 15, lgrp = lane >> 4;
   const int e_tiles = (p.E + 15) / 16, s = blockIdx.x % p.splits, et = blockIdx.x / p.splits;
   const int e0 = (et % e_tiles) * 16, t0 = (et / e_tiles) * 16;
   const int e = e0 + lrow < p.E ? e0 + lrow : p.E - 1;
@@ -284,19 +290,21 @@ __device__ __forceinline__ void up_sums(const MoeProblem& p, int el, int tile, c
   const uint8_t* wu = wg + (int64_t)p.I * p.H;
   const float* sg = p.s13 + ((int64_t)el * 2 * (p.I / 128) + tile / 8) * kb_n;
   const float* su = sg + (int64_t)(p.I / 128) * kb_n;
-  int tok[NT];
+  uint32_t xoff[NT], soff[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int c = j * 16 + lrow;
-    tok[j] = list_t[c < n ? c : 0];
+    const uint32_t t = (uint32_t)list_t[c < n ? c : 0];
+    xoff[j] = t * (uint32_t)p.H + lgrp * 16;
+    soff[j] = t * (uint32_t)kb_n;
     ag[j] = au[j] = v4f{0.f, 0.f, 0.f, 0.f};
   }
   auto fetch = [&](int kb, UpLoads& f) {
     f.g = load_tile(wg + (int64_t)kb * 2048, lane);
     f.u = load_tile(wu + (int64_t)kb * 2048, lane);
     if constexpr (NT == 1) {
-      f.x = load_row(p.xq + (int64_t)tok[0] * p.H + kb * 128, lgrp);
-      f.sx = p.xs[tok[0] * kb_n + kb];
+      f.x = load_row(p.xq + kb * 128, xoff[0]);
+      f.sx = (p.xs + kb)[soff[0]];
     }
     f.fg = sg[kb];
     f.fu = su[kb];
@@ -312,8 +320,8 @@ __device__ __forceinline__ void up_sums(const MoeProblem& p, int el, int tile, c
     } else {
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        x[j] = load_row(p.xq + (int64_t)tok[j] * p.H + kb * 128, lgrp);
-        sx[j] = p.xs[tok[j] * kb_n + kb];
+        x[j] = load_row(p.xq + kb * 128, xoff[j]);
+        sx[j] = (p.xs + kb)[soff[j]];
       }
       __asm__ volatile("" ::: "memory");
     }
@@ -367,7 +375,8 @@ __global__ __launch_bounds__(kB, NT > 2 ? 2 : 4) void moe_up_kernel(MoeProblem p
   __shared__ v4f part[kW][2][64];
   __shared__ int slot_of[kMoeMaxTokens];     // the expert's slot of each token, or -1
   __shared__ int list_t[kMoeMaxTokens], list_slot[kMoeMaxTokens], count;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lrow = lane & 15, lgrp = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lrow = lane & 15, lgrp = lane >> 4;
   if (!kRouted && (int)blockIdx.x < route_blocks) {
     if (wave < p.T) route_token<1>(p, wave, lane);
     return;
@@ -541,11 +550,18 @@ struct DownLoads {
 //    copies are summed in wave order at the end, so that the result does not
 //    depend on timing.  The next unit is loaded before the present one's
 //    products, across parts too.
+//    Where the channels give fewer workgroups than the card has compute units,
+//    `cuts` workgroups share a tile's units: one compute unit loads about 25
+//    GB/s here, so that 128 of them would take twice as long as 256.  Each
+//    leaves its FP32 sums in the workspace for one more small launch, about 4
+//    us; a count of arrivals in this one cost 40 us, because every workgroup
+//    has to write back its XCD's L2 before it counts.
 template <int NT, int DW>
-__global__ __launch_bounds__(DW * 64) void moe_down_kernel(MoeProblem p) {
+__global__ __launch_bounds__(DW * 64) void moe_down_kernel(MoeProblem p, int cuts) {
   extern __shared__ float out[];      // [DW][T][20], 16 of 20 used, then the plan
   constexpr int kDB = DW * 64;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lrow = lane & 15, lgrp = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lrow = lane & 15, lgrp = lane >> 4;
   const int most = plan_parts(p), n_plan = 2 + 2 * most + 2 * p.T * p.top_k;
   int32_t* plan = reinterpret_cast<int32_t*>(out + DW * p.T * 20);
   for (int i = threadIdx.x; i < n_plan; i += kDB) plan[i] = p.plan[i];
@@ -556,42 +572,55 @@ __global__ __launch_bounds__(DW * 64) void moe_down_kernel(MoeProblem p) {
   const float* gates = reinterpret_cast<const float*>(slots + p.T * p.top_k);
   __syncthreads();
 
-  const int tile = blockIdx.x, kb_n = p.I / 128;
-  const int units = plan[0] * kb_n;
-  const int u0 = (int)((int64_t)units * wave / DW), u1 = (int)((int64_t)units * (wave + 1) / DW);
+  const int tile = blockIdx.x / cuts, cut = blockIdx.x % cuts, kb_n = p.I / 128;
+  const int units = plan[0] * kb_n, run = cut * DW + wave;
+  const int u0 = __builtin_amdgcn_readfirstlane((int)((int64_t)units * run / (DW * cuts)));
+  const int u1 = __builtin_amdgcn_readfirstlane((int)((int64_t)units * (run + 1) / (DW * cuts)));
   if (u0 < u1) {
-    int a = u0 / kb_n, kb = u0 - a * kb_n;      // the unit at hand
+    int a = __builtin_amdgcn_readfirstlane(u0 / kb_n), kb = u0 - a * kb_n;   // the unit at hand
     int fa = a, fk = kb, left = u1 - u0;        // the unit to fetch next, and how many are left
+    // addresses of the unit to fetch: a part's are set when it begins
+    const uint8_t* fw = nullptr;
+    const float* fs = nullptr;
+    uint32_t fx = 0, fh = 0;
+    auto aim = [&]() {
+      const int el = __builtin_amdgcn_readfirstlane(active[fa]), s0 = start[fa];
+      const uint32_t s = (uint32_t)slots[s0 + (lrow < start[fa + 1] - s0 ? lrow : 0)];
+      fw = p.w2 + ((int64_t)el * (p.H / 16) + tile) * kb_n * 2048;
+      fs = p.s2 + ((int64_t)el * (p.H / 128) + tile / 8) * kb_n;
+      fx = s * (uint32_t)p.I + lgrp * 16;
+      fh = s * (uint32_t)kb_n;
+    };
     auto fetch = [&](DownLoads& f) {
-      const int el = active[fa], s0 = start[fa];
-      const int s = slots[s0 + (lrow < start[fa + 1] - s0 ? lrow : 0)];
-      f.w = load_tile(p.w2 + ((int64_t)el * (p.H / 16) + tile) * kb_n * 2048 + (int64_t)fk * 2048, lane);
-      f.x = load_row(p.hq + (int64_t)s * p.I + fk * 128, lgrp);
-      f.sh = p.hs[s * kb_n + fk];
-      f.f = p.s2[((int64_t)el * (p.H / 128) + tile / 8) * kb_n + fk];
+      f.w = load_tile(fw + fk * 2048, lane);
+      f.x = load_row(p.hq + fk * 128, fx);
+      f.sh = (p.hs + fk)[fh];
+      f.f = fs[fk];
       if (--left > 0 && ++fk == kb_n) {         // past the wave's last unit: that unit again, not used
         fk = 0;
         ++fa;
+        aim();
       }
     };
-    int n = 0, slot[NT];
+    int n = 0;
+    uint32_t slot[NT];
     v4f acc[NT];
     auto begin = [&]() {
       const int s0 = start[a];
-      n = start[a + 1] - s0;
+      n = __builtin_amdgcn_readfirstlane(start[a + 1] - s0);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const int c = j * 16 + lrow;
-        slot[j] = slots[s0 + (c < n ? c : 0)];
+        slot[j] = (uint32_t)slots[s0 + (c < n ? c : 0)];
         acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
       }
     };
-    auto flush = [&](int fl) {
+    auto flush = [&](int part) {
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         if (j * 16 + lrow < n) {
-          const float g = gates[start[fl] + j * 16 + lrow];
-          float4* o = reinterpret_cast<float4*>(&out[(wave * p.T + slot[j] / p.top_k) * 20 + lgrp * 4]);
+          const float g = gates[start[part] + j * 16 + lrow];
+          float4* o = reinterpret_cast<float4*>(&out[(wave * p.T + (int)slot[j] / p.top_k) * 20 + lgrp * 4]);
           float4 v = *o;
           v.x = __builtin_fmaf(acc[j][0], g, v.x);
           v.y = __builtin_fmaf(acc[j][1], g, v.y);
@@ -608,8 +637,8 @@ __global__ __launch_bounds__(DW * 64) void moe_down_kernel(MoeProblem p) {
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         if (j * 16 < n) {
-          const v8i b = as_operand(j == 0 ? l.x : load_row(p.hq + (int64_t)slot[j] * p.I + kb * 128, lgrp));
-          const float c = (j == 0 ? l.sh : p.hs[slot[j] * kb_n + kb]) * l.f;
+          const v8i b = as_operand(j == 0 ? l.x : load_row(p.hq + kb * 128, slot[j] * (uint32_t)p.I + lgrp * 16));
+          const float c = (j == 0 ? l.sh : (p.hs + kb)[slot[j] * (uint32_t)kb_n]) * l.f;
           const v4f zero = {0.f, 0.f, 0.f, 0.f};
           const v4f q = mfma_e4m3_16x16x128(wa, b, zero);
 #pragma unroll
@@ -630,6 +659,7 @@ __global__ __launch_bounds__(DW * 64) void moe_down_kernel(MoeProblem p) {
     };
     DownLoads l0, l1;
     begin();
+    aim();
     fetch(l0);
     for (;;) {
       fetch(l1);
@@ -644,8 +674,20 @@ __global__ __launch_bounds__(DW * 64) void moe_down_kernel(MoeProblem p) {
     float v = out[t * 20 + c];
 #pragma unroll
     for (int w = 1; w < DW; ++w) v += out[(w * p.T + t) * 20 + c];
-    store_out(p.y, t * p.ldy + tile * 16 + c, p.y_fp32, v);
+    if (cuts == 1) store_out(p.y, t * p.ldy + tile * 16 + c, p.y_fp32, v);
+    else p.parts[((int64_t)blockIdx.x * p.T + t) * 16 + c] = v;
   }
+}
+
+// 6. Where tiles were cut: the sums of a tile's workgroups, in order.
+__global__ __launch_bounds__(256) void moe_combine_kernel(MoeProblem p, int cuts) {
+  const int i = blockIdx.x * 256 + threadIdx.x;     // (tile, token, channel)
+  if (i >= p.T * p.H) return;
+  const int per = p.T * 16, tile = i / per, t = i % per >> 4, c = i & 15;
+  const float* src = p.parts + (int64_t)tile * cuts * per + t * 16 + c;
+  float v = src[0];
+  for (int q = 1; q < cuts; ++q) v += src[q * per];
+  store_out(p.y, t * p.ldy + tile * 16 + c, p.y_fp32, v);
 }
 
 // ===========================================================================
@@ -701,10 +743,11 @@ __device__ __forceinline__ uint32_t chunk_ids(const AdapterProblem& p, int64_t t
 //    adapters, which are taken in the order of their first token).
 __global__ __launch_bounds__(kB) void adapter_prepare_kernel(AdapterProblem p, int shrink_blocks, int step) {
   __shared__ v4f part[kW][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lrow = lane & 15, lgrp = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lrow = lane & 15, lgrp = lane >> 4;
   int b = blockIdx.x;
   if (b >= shrink_blocks) {
-    quant_tokens(p.x, p.ldx, (int)p.T, (int)p.K, b - shrink_blocks, p.xq, p.xs);
+    quant_tokens<true>(p.x, p.ldx, (int)p.T, (int)p.K, b - shrink_blocks, p.xq, p.xs);
     return;
   }
   const int rts = (p.r + 15) / 16, kb_n = (int)(p.K / 128);
@@ -746,7 +789,8 @@ __global__ __launch_bounds__(kB) void adapter_prepare_kernel(AdapterProblem p, i
 template <int RT>
 __global__ __launch_bounds__(kB) void adapter_prompt_kernel(AdapterProblem p, int64_t ld_s) {
   __shared__ v4f part[kW][RT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lrow = lane & 15, lgrp = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lrow = lane & 15, lgrp = lane >> 4;
   const int s = blockIdx.x % p.splits, kb_n = (int)(p.K / 128);
   const int64_t t0 = (int64_t)(blockIdx.x / p.splits) * 16, t = t0 + lrow;
   const bool in = t < p.T;
@@ -827,19 +871,22 @@ __global__ __launch_bounds__(256) void adapter_z_kernel(AdapterProblem p) {
 //    two tiles every token operand is used twice, and half as many are read
 //    from L2); the next K block's weights are loaded before the present one's
 //    products.
-template <int NT, int RT>
-__global__ __launch_bounds__(kB, 4) void adapter_project_kernel(AdapterProblem p) {
-  __shared__ v4f part[kW][RT][NT][64];
+template <int NT, int RT, int PW>
+__global__ __launch_bounds__(PW * 64, RT == 4 ? 2 : 4) void adapter_project_kernel(AdapterProblem p) {
+  __shared__ v4f part[PW][RT][NT][64];
   extern __shared__ v8bf zs[];            // [T][r / 8][hi, lo]
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lrow = lane & 15, lgrp = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lrow = lane & 15, lgrp = lane >> 4;
   const int tile = blockIdx.x * RT, kb_n = (int)(p.K / 128), T = (int)p.T, r8 = p.r / 8;
   const uint8_t* w = p.W + (int64_t)tile * kb_n * 2048;
   const float* sw = p.sW + (tile / 8) * p.ld_sw;      // RT divides 8: one block row
   int tok[NT];
+  uint32_t soff[NT];
   v4f acc[RT][NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     tok[j] = j * 16 + lrow < T ? j * 16 + lrow : T - 1;
+    soff[j] = (uint32_t)tok[j] * (uint32_t)kb_n;
 #pragma unroll
     for (int i = 0; i < RT; ++i) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
   }
@@ -854,7 +901,7 @@ __global__ __launch_bounds__(kB, 4) void adapter_project_kernel(AdapterProblem p
   const int last = kb_n - 1;
   Block a0[RT], a1[RT];
   fetch(min(wave, last), a0);
-  if (wave == kW - 1) {
+  if (wave == PW - 1) {
     const int id = lane < T ? p.ids[lane] : -1;
     uint64_t left = __ballot(id >= 0);
     int n = 0;
@@ -870,7 +917,7 @@ __global__ __launch_bounds__(kB, 4) void adapter_project_kernel(AdapterProblem p
     }
     if (lane == 0) n_adapters = n;
   }
-  for (int i = threadIdx.x; i < T * r8; i += kB) z8(p, i / r8, (i % r8) * 8, zs[2 * i], zs[2 * i + 1]);
+  for (int i = threadIdx.x; i < T * r8; i += PW * 64) z8(p, i / r8, (i % r8) * 8, zs[2 * i], zs[2 * i + 1]);
   __syncthreads();
 
   const v8bf none = __builtin_bit_cast(v8bf, fv4i{0, 0, 0, 0});
@@ -908,13 +955,13 @@ __global__ __launch_bounds__(kB, 4) void adapter_project_kernel(AdapterProblem p
     float c[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      b[j] = load_row(p.xq + tok[j] * p.K + kc * 128, lgrp);
-      c[j] = p.xs[tok[j] * kb_n + kc];
+      b[j] = load_tile(p.xq + ((int64_t)j * kb_n + kc) * 2048, lane);
+      c[j] = (p.xs + kc)[soff[j]];
     }
     __asm__ volatile("" ::: "memory");
     v8bf bw[RT];
     const bool ad = turn < n_ad;
-    fetch(min(kb + kW, last), next);
+    fetch(min(kb + PW, last), next);
     if (ad) fetch_b(turn, 0, bw);
     if (kb < kb_n) {
       const float f = sw[kb];
@@ -939,20 +986,20 @@ __global__ __launch_bounds__(kB, 4) void adapter_project_kernel(AdapterProblem p
       }
     }
   };
-  for (int kb = wave, turn = wave; kb < kb_n || turn < n_ad; kb += 2 * kW, turn += 2 * kW) {
+  for (int kb = wave, turn = wave; kb < kb_n || turn < n_ad; kb += 2 * PW, turn += 2 * PW) {
     step(kb, turn, a0, a1);
-    step(kb + kW, turn + kW, a1, a0);
+    step(kb + PW, turn + PW, a1, a0);
   }
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) part[wave][i][j][lane] = acc[i][j];
   __syncthreads();
-  for (int ij = wave; ij < RT * NT; ij += kW) {
+  for (int ij = wave; ij < RT * NT; ij += PW) {
     const int i = ij / NT, j = ij % NT;
     v4f c = part[0][i][j][lane];
 #pragma unroll
-    for (int q = 1; q < kW; ++q) c += part[q][i][j][lane];
+    for (int q = 1; q < PW; ++q) c += part[q][i][j][lane];
     if (j * 16 + lrow < T) {
       const int64_t at = (j * 16 + lrow) * p.ldc + (tile + i) * 16 + lgrp * 4;
       if (p.out_fp32) {
@@ -965,30 +1012,35 @@ __global__ __launch_bounds__(kB, 4) void adapter_project_kernel(AdapterProblem p
   }
 }
 
-template <int RT>
+template <int NT>
 void project(const AdapterProblem& p, hipStream_t stream) {
-  const dim3 grid((unsigned)(p.N / 16 / RT));
   const size_t lds = (size_t)p.T * p.r * 4;
-  switch ((p.T + 15) / 16) {
-    case 1: hipLaunchKernelGGL((adapter_project_kernel<1, RT>), grid, dim3(kB), lds, stream, p); break;
-    case 2: hipLaunchKernelGGL((adapter_project_kernel<2, RT>), grid, dim3(kB), lds, stream, p); break;
-    case 3: hipLaunchKernelGGL((adapter_project_kernel<3, RT>), grid, dim3(kB), lds, stream, p); break;
-    default: hipLaunchKernelGGL((adapter_project_kernel<4, RT>), grid, dim3(kB), lds, stream, p); break;
+  const int64_t tiles = p.N / 16;
+  // Tiles and waves of a workgroup: more tiles read fewer token operands from
+  // L2 (which count like weights against a CU's load rate), but leave fewer
+  // workgroups.  Measured at 7168 x 18432 (K x N) without adapters, us:
+  //   48 tokens: 2 tiles 4 waves 50, 4 tiles 4 waves 48, 2 tiles 8 waves 51;
+  //   16 tokens: 33, 35, 34;  64 tokens: 68, 54, 76.
+  // At 18432 x 7168, 48 tokens: 2 tiles 8 waves 48, 1 tile 8 waves 65.
+  if (tiles >= 1024) {
+    constexpr int RT = NT == 4 ? 4 : 2;
+    hipLaunchKernelGGL((adapter_project_kernel<NT, RT, 4>), dim3((unsigned)(tiles / RT)), dim3(256), lds, stream, p);
+  } else if (tiles >= 256) {
+    hipLaunchKernelGGL((adapter_project_kernel<NT, 2, 8>), dim3((unsigned)(tiles / 2)), dim3(512), lds, stream, p);
+  } else {
+    hipLaunchKernelGGL((adapter_project_kernel<NT, 1, 8>), dim3((unsigned)tiles), dim3(512), lds, stream, p);
   }
 }
 
 }  // namespace
 
-template <int NT, int DW>
-static void down_waves(const MoeProblem& p, hipStream_t stream) {
-  const size_t lds = ((size_t)DW * p.T * 20 + 2 + 2 * plan_parts(p) + 2 * p.T * p.top_k) * 4;
-  hipLaunchKernelGGL((moe_down_kernel<NT, DW>), dim3(p.H / 16), dim3(DW * 64), lds, stream, p);
-}
-// more waves a workgroup where there are too few workgroups for the card
 template <int NT>
 static void down(const MoeProblem& p, hipStream_t stream) {
-  if (p.H / 16 <= 256) down_waves<NT, 16>(p, stream);
-  else down_waves<NT, 8>(p, stream);
+  const int tiles = p.H / 16, cuts = moe_cuts(p.H);
+  const size_t lds = ((size_t)8 * p.T * 20 + 2 + 2 * plan_parts(p) + 2 * p.T * p.top_k) * 4;
+  hipLaunchKernelGGL((moe_down_kernel<NT, 8>), dim3(tiles * cuts), dim3(512), lds, stream, p, cuts);
+  if (cuts > 1)
+    hipLaunchKernelGGL(moe_combine_kernel, dim3((p.T * p.H + 255) / 256), dim3(256), 0, stream, p, cuts);
 }
 
 hipError_t launch_moe_few_tokens(const MoeProblem& p, hipStream_t stream) {
@@ -1024,8 +1076,12 @@ hipError_t launch_adapter_few(const AdapterProblem& p, hipStream_t stream) {
   const int shrink_blocks = chunks * rts * step * p.splits;
   hipLaunchKernelGGL(adapter_prepare_kernel, dim3(shrink_blocks + quant_blocks(p.T, p.K)), dim3(kB), 0, stream, p,
                      shrink_blocks, step);
-  if (p.N / 16 >= kWideTiles) project<2>(p, stream);
-  else project<1>(p, stream);
+  switch (chunks) {
+    case 1: project<1>(p, stream); break;
+    case 2: project<2>(p, stream); break;
+    case 3: project<3>(p, stream); break;
+    default: project<4>(p, stream); break;
+  }
   return hipGetLastError();
 }
 

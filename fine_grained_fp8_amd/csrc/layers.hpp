@@ -53,6 +53,12 @@ constexpr int64_t kNormMaxCols = 16384;
 // ---- the few-token expert layer ----
 constexpr int kMoeMaxTokens = 64, kMoeMaxTopK = 16, kMoeMaxExperts = 1024;
 constexpr int kMoeSplits = 8;
+// workgroups that share a 16-channel tile of the down product, so that there
+// are about two for every compute unit
+inline int moe_cuts(int64_t H) {
+  const int64_t c = (512 + H / 16 - 1) / (H / 16);
+  return H / 16 >= 256 ? 1 : (int)(c < 8 ? c : 8);
+}
 // shares of a row of K that small dot products are cut into: eight waves with
 // about a 128-wide block each
 inline int dot_splits(int64_t K, int most) {
@@ -87,6 +93,7 @@ struct MoeProblem {
   float* hs;                  // [T top_k][I / 128]
   int32_t* counts;            // [local]: slots that chose each held expert
   int32_t* lists;             // [local][kMoeMaxTokens]: those slots (token top_k + place), in token order
+  float* parts;               // [H / 16][moe_cuts(H)][T][16]: the down kernel's sums, if a tile is cut
   int32_t* plan;              // [2 + 2 parts + 2 T top_k]: see make_plan; parts <= T top_k (1 + 1/16)
 };
 hipError_t launch_moe_few_tokens(const MoeProblem& p, hipStream_t stream);
@@ -116,7 +123,7 @@ struct AdapterProblem {
   int64_t ldc;
   int out_fp32;
   // workspace
-  uint8_t* xq;                // [T][K]
+  uint8_t* xq;                // few: operand tiles of 16 tokens; otherwise [T][K]
   float* xs;                  // few: [T][K / 128]; otherwise [K / 128][round_up(T, 4)]
   int splits;                 // adapter_splits(T, K)
   float* zp;                  // [splits][T][r]: partial sums of A x
