@@ -1171,9 +1171,80 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
     const uint16_t* bcol = ad.B + (n0w + lrow) * ad.r;
     const int id0 = em0 + lane < em_end ? ad.ids[em0 + lane] : -1;
     const int id1 = em0 + 64 + lane < em_end ? ad.ids[em0 + 64 + lane] : -1;
+    // A step is 32 ranks of one adapter in one half; the next step is asked for
+    // before the present one's products.  (a, rows, r0): the last one asked for;
+    // left: the half's rows whose adapters are still to come.
+    struct Step {
+      uint64_t in;                       // the half's rows with the adapter
+      v4i bw[DNI], zh[DNJ / 2], zl[DNJ / 2];
+    };
+    uint64_t left = 0, rows = 0;
+    int a = 0, r0 = 0;
+    auto load_step = [&](Step& s, int64_t mh) {
+      s.in = rows;
+      const uint16_t* ba = bcol + (int64_t)(a < ad.n ? a : 0) * p.N * ad.r;
+      const int r = r0 + lgrp * 8;
+      const v4i none = {0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < DNI; ++i)
+        s.bw[i] = r < ad.r ? *reinterpret_cast<const v4i*>(ba + (int64_t)i * 16 * ad.r + r) : none;
+#pragma unroll
+      for (int j = 0; j < DNJ / 2; ++j) {
+        const bool on = ((rows >> (16 * j + lrow)) & 1) && r < ad.r;
+        const uint16_t* zp = ad.z + (mh + j * 16 + lrow) * 2 * ad.r + 2 * r;
+        s.zh[j] = on ? *reinterpret_cast<const v4i*>(zp) : none;
+        s.zl[j] = on ? *reinterpret_cast<const v4i*>(zp + 8) : none;
+      }
+    };
+    auto next_adapter = [&](int id) {
+      a = __builtin_amdgcn_readlane(id, (int)__builtin_ctzll(left));
+      rows = __ballot(id == a);
+      left &= ~rows;
+      r0 = 0;
+    };
+    // asks for the half's next step; in == 0: there is none
+    auto advance = [&](Step& s, int id, int64_t mh) {
+      r0 += 32;
+      if (rows == 0 || r0 >= ad.r) {
+        rows = 0;
+        if (left != 0) next_adapter(id);
+      }
+      s.in = 0;
+      if (rows != 0) load_step(s, mh);
+    };
+    auto open_half = [&](Step& s, int id, int64_t mh) {
+      rows = 0;
+      left = __ballot(id >= 0);
+      advance(s, id, mh);
+    };
+    auto apply = [&](const Step& s) {
+#pragma unroll
+      for (int j = 0; j < DNJ / 2; ++j) {
+        if (((s.in >> (16 * j)) & 0xFFFFu) == 0) continue;
+        const v8bf hi = __builtin_bit_cast(v8bf, s.zh[j]), lo = __builtin_bit_cast(v8bf, s.zl[j]);
+        const int m = j * 16 + lrow;
+        v4f c[DNI];
+#pragma unroll
+        for (int i = 0; i < DNI; ++i)
+          c[i] = *reinterpret_cast<const v4f*>(ob + m * 256 + (((i * 4 + lgrp) ^ (m & 15)) << 4));
+#pragma unroll
+        for (int i = 0; i < DNI; ++i) c[i] = mfma_bf16_16x16x32(__builtin_bit_cast(v8bf, s.bw[i]), hi, c[i]);
+#pragma unroll
+        for (int i = 0; i < DNI; ++i) c[i] = mfma_bf16_16x16x32(__builtin_bit_cast(v8bf, s.bw[i]), lo, c[i]);
+        // the sums of other adapters' rows stay (0 x an infinite weight is not 0)
+        if ((s.in >> m) & 1) {
+#pragma unroll
+          for (int i = 0; i < DNI; ++i)
+            *reinterpret_cast<v4f*>(ob + m * 256 + (((i * 4 + lgrp) ^ (m & 15)) << 4)) = c[i];
+        }
+      }
+    };
+    Step s0, s1;
+    open_half(s0, id0, em0);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int64_t mh = em0 + half * 64;
+      const int id = half == 0 ? id0 : id1;
 #pragma unroll
       for (int j = 0; j < DNJ / 2; ++j) {
 #pragma unroll
@@ -1183,46 +1254,15 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
           *reinterpret_cast<float4*>(ob + m * 256 + ((ch ^ (m & 15)) << 4)) = make_float4(r[0], r[1], r[2], r[3]);
         }
       }
-      const int id = half == 0 ? id0 : id1;
-      uint64_t left = __ballot(id >= 0);
 #pragma unroll 1
-      while (left != 0) {
-        const int a = __builtin_amdgcn_readlane(id, (int)__builtin_ctzll(left));
-        const uint64_t in = __ballot(id == a);
-        left &= ~in;
-        const uint16_t* ba = bcol + (int64_t)(a < ad.n ? a : 0) * p.N * ad.r;
-#pragma unroll 1
-        for (int r0 = 0; r0 < ad.r; r0 += 32) {
-          // all loads of the step first: one round trip
-          const int r = r0 + lgrp * 8;
-          const v4i none = {0, 0, 0, 0};
-          v4i bw[DNI], zh[DNJ / 2], zl[DNJ / 2];
-#pragma unroll
-          for (int i = 0; i < DNI; ++i)
-            bw[i] = r < ad.r ? *reinterpret_cast<const v4i*>(ba + (int64_t)i * 16 * ad.r + r) : none;
-#pragma unroll
-          for (int j = 0; j < DNJ / 2; ++j) {
-            const bool on = ((in >> (16 * j + lrow)) & 1) && r < ad.r;
-            const uint16_t* zp = ad.z + (mh + j * 16 + lrow) * 2 * ad.r + 2 * r;
-            zh[j] = on ? *reinterpret_cast<const v4i*>(zp) : none;
-            zl[j] = on ? *reinterpret_cast<const v4i*>(zp + 8) : none;
-          }
-#pragma unroll
-          for (int j = 0; j < DNJ / 2; ++j) {
-            if (((in >> (16 * j)) & 0xFFFFu) == 0) continue;
-            const v8bf hi = __builtin_bit_cast(v8bf, zh[j]), lo = __builtin_bit_cast(v8bf, zl[j]);
-#pragma unroll
-            for (int i = 0; i < DNI; ++i) {
-              const int m = j * 16 + lrow, ch = i * 4 + lgrp;
-              v4f* at = reinterpret_cast<v4f*>(ob + m * 256 + ((ch ^ (m & 15)) << 4));
-              const v8bf b = __builtin_bit_cast(v8bf, bw[i]);
-              const v4f c = mfma_bf16_16x16x32(b, lo, mfma_bf16_16x16x32(b, hi, *at));
-              // the sums of other adapters' rows stay (0 x an infinite weight is not 0)
-              if ((in >> m) & 1) *at = c;
-            }
-          }
-        }
+      while (s0.in != 0) {
+        advance(s1, id, mh);
+        apply(s0);
+        if (s1.in == 0) break;
+        advance(s0, id, mh);
+        apply(s1);
       }
+      if (half == 0) open_half(s0, id1, em0 + 64);
       if constexpr (kOutF32) {
 #pragma unroll 4
         for (int t = 0; t < 16; ++t) {

@@ -462,6 +462,88 @@ def test_adapter_linear_strided_rows_and_another_stream(gpu_lib, T):
     assert torch.equal(out[:, :N], want) and (out[:, N:] == 3).all()
 
 
+@pytest.mark.parametrize("T", [24, 150])
+def test_adapters_with_infinite_weights_stay_among_their_tokens(gpu_lib, T):
+    N, K, n, r = 256, 256, 4, 24
+    wq, ws, A, B, _ = make_adapters(N, K, n, r, 120)
+    x, ids = bf16_dev(syn.gaussian((T, K), seed=121)), np.arange(T, dtype=np.int32) % n
+    args = lambda A_, B_: (x, dev(tile_codes(wq)), dev(ws), bf16_dev(A_), bf16_dev(B_), dev(ids))
+    clean = gpu_lib.adapter_linear(*args(A, B))
+    A2, B2 = A.copy(), B.copy()
+    A2[1, 3, 7], A2[1, 4, 7], B2[2, :, 5], B2[2, 9, 6] = 0x7F80, 0x7FC0, 0xFF80, 0x7FC0
+    y = gpu_lib.adapter_linear(*args(A2, B2))
+    other = torch.from_numpy((ids != 1) & (ids != 2)).cuda()
+    assert torch.equal(y[other], clean[other])
+    assert not torch.isfinite(y[ids == 1]).any() and not torch.isfinite(y[ids == 2]).any()
+
+
+@pytest.mark.parametrize("T,N,K,r", [(1, 4096, 128, 8), (33, 4096, 256, 40), (64, 4224, 128, 128), (5, 16384, 128, 16),
+                                     (47, 16512, 128, 64), (64, 16384, 256, 32)])
+def test_adapter_linear_wide_outputs(gpu_lib, T, N, K, r):
+    """The widths at which a workgroup takes two and four tiles of columns."""
+    n = 5
+    wq, ws, A, B, sc = make_adapters(N, K, n, r, 130)
+    xb = syn.gaussian((T, K), seed=131)
+    ids = np.random.default_rng(132).integers(-1, n, T).astype(np.int32)
+    f64 = lambda bits: quant.bf16_to_f32(bits).astype(np.float64)
+    y = gpu_lib.adapter_linear(bf16_dev(xb), dev(tile_codes(wq)), dev(ws), bf16_dev(A), bf16_dev(B), dev(ids), scales=dev(sc))
+    check_adapters(y, *layers.adapters(xb, wq, ws, f64(A), f64(B), ids, sc))
+
+
+def test_adapter_linear_on_a_split_tail(gpu_lib):
+    """More output tiles than the persistent grid, with a tail that is cut
+    along K: the adapters are added once per tile, by the piece that ends it."""
+    T, N, K, n, r = 2100, 3968, 1024, 6, 16
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    if cus == 256:
+        gpu_lib.block_gemm("fprop_tiled", *gpu_lib.quant_act_1x128(rand((T, K), 1, torch.bfloat16))[:2],
+                           torch.zeros(N, K, dtype=torch.uint8, device="cuda"), torch.ones(N // 128, K // 128, device="cuda"))
+        assert gpu_lib.probe_gemm_split(((T + 127) // 128) * ((N + 255) // 256), K)[1] > 1
+    wq, ws, A, B, sc = make_adapters(N, K, n, r, 140)
+    xb = syn.gaussian((T, K), seed=141)
+    ids = np.repeat(np.random.default_rng(142).integers(-1, n, 60), 35).astype(np.int32)
+    f64 = lambda bits: quant.bf16_to_f32(bits).astype(np.float64)
+    y = gpu_lib.adapter_linear(bf16_dev(xb), dev(tile_codes(wq)), dev(ws), bf16_dev(A), bf16_dev(B), dev(ids), scales=dev(sc))
+    check_adapters(y, *layers.adapters(xb, wq, ws, f64(A), f64(B), ids, sc))
+
+
+@pytest.mark.parametrize("T,E,local,k,H,I", [(64, 300, 20, 3, 256, 128), (40, 700, 9, 2, 128, 256), (64, 40, 40, 2, 4096, 128),
+                                             (8, 64, 64, 16, 128, 128), (9, 64, 64, 16, 128, 128), (50, 2, 2, 1, 256, 256)])
+def test_moe_uneven_choices(gpu_lib, T, E, local, k, H, I):
+    """Most tokens choose the same few experts, whatever the average is."""
+    x0 = quant.bf16_to_f32(syn.gaussian((T, H), seed=150))
+    common = quant.bf16_to_f32(syn.gaussian((1, H), seed=151))
+    xb = syn.f32_to_bf16_bits(0.3 * x0 + common)
+    rb = syn.gaussian((E, H), seed=152, std=H ** -0.5)
+    w13, w2, d = make_experts(local, H, I, 153)
+    R, X = quant.bf16_to_f32(rb).astype(np.float64), quant.bf16_to_f32(xb).astype(np.float64)
+    order = np.argsort(-(X @ R.T).mean(axis=0))
+    rb = rb[np.concatenate([order, order])[:E]] if E <= order.size else rb      # the liked experts first: held ones
+    R = quant.bf16_to_f32(rb).astype(np.float64)
+    y, ids, _ = gpu_lib.moe_few_tokens(bf16_dev(xb), bf16_dev(rb), **d, top_k=k, return_routing=True)
+    ids = ids.cpu().numpy()
+    counts = np.bincount(ids.ravel(), minlength=E)
+    assert counts.max() > min(T, 16) - 1
+    Y, _, _, mag, slack = layers.moe(xb, R, w13, w2, k, 0, ids=ids)
+    check_moe(y, Y, mag * 1.01, slack)
+
+
+def test_layer_norm_past_32_bit_offsets(gpu_lib):
+    """Rows beyond 2^31 elements and 2^32 bytes from the first."""
+    rows, cols = 300_000, 8192
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    tail = rand((5, cols), 160, torch.bfloat16)
+    x[-5:] = tail
+    y, mean, rstd = gpu_lib.layer_norm(x, return_stats=True)
+    want = gpu_lib.layer_norm(tail)
+    assert torch.equal(y[-5:], want) and (y[:-5:4999] == 0).all()
+    dx, dw, db = gpu_lib.layer_norm_backward(x, x, mean, rstd)
+    want, wdw, wdb = gpu_lib.layer_norm_backward(tail, tail, mean[-5:].clone(), rstd[-5:].clone())
+    assert torch.equal(dx[-5:], want)
+    # zero rows add zeros; the five rows meet in another order
+    assert torch.allclose(dw, wdw, rtol=1e-5, atol=1e-5) and torch.allclose(db, wdb, rtol=1e-5, atol=1e-5)
+
+
 # ------------------------------------------------------------- graphs, refusals
 
 def test_operators_replay_from_a_graph(gpu_lib):
