@@ -3,13 +3,18 @@
 // up to 64 tokens (plus the adapters' two small products for any number).
 //
 // With so few rows every weight byte is used for a handful of products: the
-// kernels are bound by reading the weights once from HBM, so they are laid
-// out for that.  A workgroup owns 16 output rows (one operand tile row) and
-// all its columns' tokens; its eight waves split the K blocks, each wave
-// loading whole 2 KB operand tiles (16 bytes a lane) straight into MFMA
-// operand registers; the partial sums meet in LDS.  The weight rows are the
-// MFMA's "A" rows, the tokens its 16 columns: a lane ends with 4 consecutive
-// outputs of one token.
+// kernels are bound by reading the weights once, so they are laid out for
+// that.  A workgroup owns 16 output rows (one operand tile row), or two or four
+// such; its waves split the K blocks, each loading whole 2 KB operand tiles (16
+// bytes a lane) straight into MFMA operand registers, one block ahead of the
+// products; the partial sums meet in LDS.  The weight rows are the MFMA's "A"
+// rows, the tokens its 16 columns: a lane ends with 4 consecutive outputs of
+// one token.
+//
+// What bounds them, measured: a CU takes in about 25 GB/s here, weights and
+// token operands alike, and all of them 5.2 - 6.4 TB/s; so work goes to all 256
+// CUs, and operands that are read again from L2 cost like weights.  A small
+// dependent launch costs 4 - 5 us.
 #include "device.hpp"
 #include "layers.hpp"
 
@@ -370,6 +375,10 @@ __device__ __forceinline__ void up_sums(const MoeProblem& p, int el, int tile, c
 //    than top_k experts come before e, and that count is e's slot.  That saves
 //    a launch (about 4 us); with more tokens every workgroup would repeat too
 //    many sums over the shares.
+//    64 tokens on 64 experts of 2048 x 1408: 63 us for 369 MB (5.8 TB/s); 8 of 64
+//    experts of 7168 x 2048, 32 tokens: 40 us for 229 MB (5.7 TB/s); one token on
+//    two experts: 13 - 16 us for 59 MB.  Without the block loaded ahead 97 us in
+//    the first case, with three blocks a wave in flight (spilled) 400.
 template <int NT, bool kRouted>
 __global__ __launch_bounds__(kB, NT > 2 ? 2 : 4) void moe_up_kernel(MoeProblem p, int route_blocks) {
   __shared__ v4f part[kW][2][64];
@@ -556,6 +565,8 @@ struct DownLoads {
 //    leaves its FP32 sums in the workspace for one more small launch, about 4
 //    us; a count of arrivals in this one cost 40 us, because every workgroup
 //    has to write back its XCD's L2 before it counts.
+//    64 tokens on 64 experts of 2048 x 1408: 39 us for 185 MB, uncut 61; 8 experts
+//    of 7168 x 2048, 32 tokens: 24 us for 117 MB (4.9 TB/s).
 template <int NT, int DW>
 __global__ __launch_bounds__(DW * 64) void moe_down_kernel(MoeProblem p, int cuts) {
   extern __shared__ float out[];      // [DW][T][20], 16 of 20 used, then the plan

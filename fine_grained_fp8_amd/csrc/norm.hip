@@ -171,6 +171,15 @@ __device__ __forceinline__ float rsqrt_refined(float v) {
   return __builtin_fmaf(0.5f * e, r, r);
 }
 
+// Forward.  Each lane keeps one run of 8 values (two for rows over 8192), so a
+// row of 7168 takes a workgroup of 1024 lanes and two of them fill a CU: with
+// more runs a lane, fewer rows are in flight per CU and the registers of w and b
+// double.  Bound by memory for plain output (8192 x 7168 BF16: 44.4 us, 5.3
+// TB/s; a copy of the same bytes reaches 4.9 - 5.2) and about evenly by memory
+// and the vector unit with codes (43.8 us, 178 MB; of which the scales' 4-byte
+// stores 3.5 us).  Measured against it at that size, us plain / with codes: two
+// runs and 512 lanes 45.6 / 42.8, four and 256 lanes 59 / 77, a wave a row with
+// w and b in LDS 61 / 52.
 template <typename T, bool kVec, int G, int B, int NV, bool kQuant>
 __global__ __launch_bounds__(B) void layer_norm_kernel(LayerNormProblem p) {
   constexpr int kRows = B / G;
@@ -271,6 +280,12 @@ struct Run<float> {
   __device__ __forceinline__ float get(int k) const { return __int_as_float(k < 4 ? d[k] : e[k - 4]); }
 };
 
+// Backward.  A workgroup walks rows and keeps the column sums of its lanes' 8
+// columns in registers; one per CU of 1024 lanes, so that the shares it leaves
+// (256 x 2 x C floats) stay small beside dy, x and dx.  8192 x 7168 BF16: 84 us for
+// both launches, 352 MB (4.2 TB/s).  With two runs a lane (512 lanes) 125 us,
+// with four (256 lanes) 192: the sums, w and the rows in flight no longer fit
+// the registers that two rows a CU need.
 template <typename T, bool kVec, int G, int B, int NV>
 __global__ __launch_bounds__(B) void layer_norm_backward_kernel(LayerNormGradProblem p) {
   constexpr int kRows = B / G;

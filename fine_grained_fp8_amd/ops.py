@@ -441,7 +441,7 @@ def _is_fp32(t: torch.Tensor) -> int:
 def _check_vec(name, t, n, dtypes):
     if t is None:
         return
-    if t.dim() != 1 or t.numel() != n or not t.is_contiguous() or not t.is_cuda or t.dtype not in dtypes:
+    if t.dtype not in dtypes or t.shape != (n,) or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name}: a contiguous device vector of {n} elements of {dtypes} is required, got "
                          f"{t.dtype} {tuple(t.shape)}")
 
@@ -449,10 +449,17 @@ def _check_vec(name, t, n, dtypes):
 def _norm_affine(weight, bias, cols):
     _check_vec("weight", weight, cols, _FLOATS)
     _check_vec("bias", bias, cols, _FLOATS)
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise TypeError(f"weight is {weight.dtype} and bias {bias.dtype}: one type is required")
     t = weight if weight is not None else bias
-    return _lib.OUT_BF16 if t is None else _is_fp32(t)
+    if t is None:
+        return _lib.OUT_BF16
+    if bias is not None and bias.dtype != t.dtype:
+        raise TypeError(f"weight is {weight.dtype} and bias {bias.dtype}: one type is required")
+    return _is_fp32(t)
+
+
+def _empty_as(x):
+    """A contiguous tensor of x's shape and type (the short call where x is one)."""
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
 def _same_device(dev, **tensors):
@@ -485,7 +492,7 @@ def layer_norm(x: torch.Tensor, weight=None, bias=None, *, eps: float = 1e-5, re
     wt = _norm_affine(weight, bias, cols)
     _same_device(x.device, weight=weight, bias=bias, out=out)
     if out is None:
-        out = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+        out = _empty_as(x)
     else:
         _check_2d("out", out, (x.dtype,))
         if out.shape != x.shape:
@@ -543,7 +550,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
     _check_vec("mean", mean, rows, (torch.float32,))
     _check_vec("rstd", rstd, rows, (torch.float32,))
     _same_device(x.device, dy=dy, mean=mean, rstd=rstd, weight=weight)
-    dx = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+    dx = _empty_as(x)
     dweight = torch.empty(cols, dtype=torch.float32, device=x.device)
     dbias = torch.empty_like(dweight)
     nbytes = lib.fp8_layer_norm_backward_workspace(rows, cols)

@@ -622,3 +622,36 @@ def test_refusals(gpu_lib):
         fp8.adapter_linear(x, rest[0], rest[1], bf16_dev(A[:, :12]), bf16_dev(B[:, :, :12]), rest[4])
     with pytest.raises(ValueError):
         fp8.adapter_linear(x, rest[0], rest[1], rest[2], rest[3][:, :128].contiguous(), rest[4])
+
+
+# ------------------------------------------------------------- the operators together
+
+def test_example_block(gpu_lib):
+    """The example's block: the prompt form of a batch against the same tokens
+    served a few at a time, and its training step against FP32 autograd."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import decoder_block as ex
+    torch.manual_seed(3)
+    block = ex.Block(512, 256)
+    x = torch.randn(150, 512, device="cuda").bfloat16()
+    ids = (torch.arange(150, device="cuda") % 5 - 1).to(torch.int32)
+    whole = block.serve(x, ids).double()
+    few = torch.cat([block.serve(p, i) for p, i in zip(x.split(9), ids.split(9))]).double()
+    # the same sums in another order: a BF16 rounding here and there, codes that
+    # move with it, and a token whose two experts lie that near may change one
+    d = (whole - few).norm(dim=1) / whole.norm(dim=1)
+    assert d.median() < 2e-3 and (d > 2e-2).sum() <= 3
+
+    w = (0.05 * torch.randn(256, 512, device="cuda")).bfloat16()
+    xt, dy = torch.randn(256, 512, device="cuda").bfloat16(), (1e-2 * torch.randn(256, 256, device="cuda")).bfloat16()
+    norm = 1 + 0.1 * torch.randn(512, device="cuda"), 0.1 * torch.randn(512, device="cuda")
+    y, dx, dw, dnw, dnb = ex.train_step(xt, norm, w, dy)
+    X, W = xt.float().requires_grad_(), w.float().requires_grad_()
+    NW, NB = (n.clone().requires_grad_() for n in norm)
+    Y = torch.nn.functional.layer_norm(X, (512,), NW, NB, 1e-5) @ W.t()
+    Y.backward(dy.float())
+    for got, want in ((y, Y), (dx, X.grad), (dw, W.grad), (dnw, NW.grad), (dnb, NB.grad)):
+        # both operands of every product rounded to E4M3: 2^-4 / sqrt(3) each at most, over many terms
+        assert (got.float() - want).norm() <= 0.06 * want.norm()
