@@ -769,13 +769,14 @@ __global__ __launch_bounds__(kB) void adapter_prepare_kernel(AdapterProblem p, i
   const int rt = b % rts;
   const int64_t t0 = (int64_t)(b / rts) * 16;
   const int row = rt * 16 + lrow < p.r ? rt * 16 + lrow : p.r - 1, r0 = rt * 16 + lgrp * 4;
-  const uint16_t* xr = p.x + (t0 + lrow < p.T ? t0 + lrow : t0) * p.ldx;
   int id;
   uint32_t left = chunk_ids(p, t0, lrow, id);
   for (int turn = 0; left != 0; ++turn) {
-    const int a = __shfl(id, __builtin_ctz(left));
+    const int one = __builtin_ctz(left), a = __shfl(id, one);
     left &= ~(uint32_t)__ballot(id == a);
     if (turn % step != first) continue;
+    // other adapters' tokens: the column is not used, and reads a line that is
+    const uint16_t* xr = p.x + (t0 + (id == a ? lrow : one)) * p.ldx;
     __syncthreads();
     part[wave][lane] = dot_rows_bf16(p.A + ((int64_t)a * p.r + row) * p.K, xr, share(kb_n, s, p.splits),
                                      share(kb_n, s + 1, p.splits), wave, lgrp);
@@ -878,19 +879,19 @@ __global__ __launch_bounds__(256) void adapter_z_kernel(AdapterProblem p) {
   reinterpret_cast<v8bf*>(p.z)[2 * i + 1] = lo;
 }
 
-// 2. Few tokens: projection and expand, 16 RT output columns a workgroup (with
-//    two tiles every token operand is used twice, and half as many are read
-//    from L2); the next K block's weights are loaded before the present one's
-//    products.
+// 2. Few tokens: projection and expand, RT tiles of 16 output columns a
+//    workgroup (every token operand is read once for them); the next K block's
+//    weights are loaded before the present one's products.
 template <int NT, int RT, int PW>
-__global__ __launch_bounds__(PW * 64, RT == 4 ? 2 : 4) void adapter_project_kernel(AdapterProblem p) {
-  __shared__ v4f part[PW][RT][NT][64];
+__global__ __launch_bounds__(PW * 64, 2) void adapter_project_kernel(AdapterProblem p) {
+  __shared__ v4f part[PW][RT][64];
   extern __shared__ v8bf zs[];            // [T][r / 8][hi, lo]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lrow = lane & 15, lgrp = lane >> 4;
-  const int tile = blockIdx.x * RT, kb_n = (int)(p.K / 128), T = (int)p.T, r8 = p.r / 8;
-  const uint8_t* w = p.W + (int64_t)tile * kb_n * 2048;
-  const float* sw = p.sW + (tile / 8) * p.ld_sw;      // RT divides 8: one block row
+  const int kb_n = (int)(p.K / 128), T = (int)p.T, r8 = p.r / 8;
+  int tile[RT];                           // past the last one: the last one again, not stored
+#pragma unroll
+  for (int i = 0; i < RT; ++i) tile[i] = min((int)blockIdx.x * RT + i, (int)(p.N / 16) - 1);
   int tok[NT];
   uint32_t soff[NT];
   v4f acc[RT][NT];
@@ -903,7 +904,7 @@ __global__ __launch_bounds__(PW * 64, RT == 4 ? 2 : 4) void adapter_project_kern
   }
   auto fetch = [&](int kb, Block (&a)[RT]) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i) a[i] = load_tile(w + ((int64_t)i * kb_n + kb) * 2048, lane);
+    for (int i = 0; i < RT; ++i) a[i] = load_tile(p.W + ((int64_t)tile[i] * kb_n + kb) * 2048, lane);
   };
   // the batch's adapters, in the order of their first token, and the tokens of each
   __shared__ int adapter[kAdapterFewTokens];
@@ -934,11 +935,11 @@ __global__ __launch_bounds__(PW * 64, RT == 4 ? 2 : 4) void adapter_project_kern
   const v8bf none = __builtin_bit_cast(v8bf, fv4i{0, 0, 0, 0});
   const int n_ad = n_adapters;
   auto fetch_b = [&](int turn, int r0, v8bf (&bw)[RT]) {
-    const uint16_t* brow = p.B + ((int64_t)adapter[turn] * p.N + tile * 16 + lrow) * p.r;
+    const uint16_t* brow = p.B + ((int64_t)adapter[turn] * p.N + lrow) * p.r;
     const int r = r0 + lgrp * 8;
 #pragma unroll
     for (int i = 0; i < RT; ++i)
-      bw[i] = r < p.r ? *reinterpret_cast<const v8bf*>(brow + (int64_t)i * 16 * p.r + r) : none;
+      bw[i] = r < p.r ? *reinterpret_cast<const v8bf*>(brow + (int64_t)tile[i] * 16 * p.r + r) : none;
   };
   // a column's sums are kept in its own adapter's turn
   auto expand = [&](int turn, int r0, const v8bf (&bw)[RT]) {
@@ -975,14 +976,16 @@ __global__ __launch_bounds__(PW * 64, RT == 4 ? 2 : 4) void adapter_project_kern
     fetch(min(kb + PW, last), next);
     if (ad) fetch_b(turn, 0, bw);
     if (kb < kb_n) {
-      const float f = sw[kb];
+      float f[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) f[i] = p.sW[(tile[i] / 8) * p.ld_sw + kb];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const v8i bj = as_operand(b[j]);
-        const float cj = c[j] * f;
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
           const v4f zero = {0.f, 0.f, 0.f, 0.f};
+          const float cj = c[j] * f[i];
           const v4f q = mfma_e4m3_16x16x128(as_operand(a[i]), bj, zero);
 #pragma unroll
           for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(q[v], cj, acc[i][j][v]);
@@ -1001,45 +1004,60 @@ __global__ __launch_bounds__(PW * 64, RT == 4 ? 2 : 4) void adapter_project_kern
     step(kb, turn, a0, a1);
     step(kb + PW, turn + PW, a1, a0);
   }
+  for (int j = 0; j < NT; ++j) {
+    if (j != 0) __syncthreads();
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
+    for (int i = 0; i < RT; ++i) {
+      v4f v = acc[i][0];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) part[wave][i][j][lane] = acc[i][j];
-  __syncthreads();
-  for (int ij = wave; ij < RT * NT; ij += PW) {
-    const int i = ij / NT, j = ij % NT;
-    v4f c = part[0][i][j][lane];
+      for (int q = 1; q < NT; ++q) v = j == q ? acc[i][q] : v;
+      part[wave][i][lane] = v;
+    }
+    __syncthreads();
+    for (int i = wave; i < RT; i += PW) {
+      v4f c = part[0][i][lane];
 #pragma unroll
-    for (int q = 1; q < PW; ++q) c += part[q][i][j][lane];
-    if (j * 16 + lrow < T) {
-      const int64_t at = (j * 16 + lrow) * p.ldc + (tile + i) * 16 + lgrp * 4;
-      if (p.out_fp32) {
-        *reinterpret_cast<float4*>(static_cast<float*>(p.C) + at) = make_float4(c[0], c[1], c[2], c[3]);
-      } else {
-        typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
-        *reinterpret_cast<v4bf*>(static_cast<uint16_t*>(p.C) + at) = __builtin_convertvector(c, v4bf);
+      for (int q = 1; q < PW; ++q) c += part[q][i][lane];
+      const int n = (blockIdx.x * RT + i) * 16;
+      if (j * 16 + lrow < T && n < p.N) {
+        const int64_t at = (j * 16 + lrow) * p.ldc + n + lgrp * 4;
+        if (p.out_fp32) {
+          *reinterpret_cast<float4*>(static_cast<float*>(p.C) + at) = make_float4(c[0], c[1], c[2], c[3]);
+        } else {
+          typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+          *reinterpret_cast<v4bf*>(static_cast<uint16_t*>(p.C) + at) = __builtin_convertvector(c, v4bf);
+        }
       }
     }
   }
 }
 
-template <int NT>
+template <int NT, int RT, int PW>
 void project(const AdapterProblem& p, hipStream_t stream) {
   const size_t lds = (size_t)p.T * p.r * 4;
-  const int64_t tiles = p.N / 16;
-  // Tiles and waves of a workgroup: more tiles read fewer token operands from
-  // L2 (which count like weights against a CU's load rate), but leave fewer
-  // workgroups.  Measured at 7168 x 18432 (K x N) without adapters, us:
-  //   48 tokens: 2 tiles 4 waves 50, 4 tiles 4 waves 48, 2 tiles 8 waves 51;
-  //   16 tokens: 33, 35, 34;  64 tokens: 68, 54, 76.
-  // At 18432 x 7168, 48 tokens: 2 tiles 8 waves 48, 1 tile 8 waves 65.
-  if (tiles >= 1024) {
-    constexpr int RT = NT == 4 ? 4 : 2;
-    hipLaunchKernelGGL((adapter_project_kernel<NT, RT, 4>), dim3((unsigned)(tiles / RT)), dim3(256), lds, stream, p);
-  } else if (tiles >= 256) {
-    hipLaunchKernelGGL((adapter_project_kernel<NT, 2, 8>), dim3((unsigned)(tiles / 2)), dim3(512), lds, stream, p);
-  } else {
-    hipLaunchKernelGGL((adapter_project_kernel<NT, 1, 8>), dim3((unsigned)tiles), dim3(512), lds, stream, p);
+  hipLaunchKernelGGL((adapter_project_kernel<NT, RT, PW>), dim3((unsigned)((p.N / 16 + RT - 1) / RT)),
+                     dim3(PW * 64), lds, stream, p);
+}
+
+// Tiles of a workgroup: one workgroup of eight waves for each of the 256 CUs
+// where up to 5 tiles suffice for that (more would not fit the registers), as
+// a workgroup reads all token operands, which count like weights against its
+// CU's load rate; wider outputs take several smaller workgroups a CU.
+// Measured at K x N with rank 32, every token its own adapter, us:
+//   7168 x 18432 (1152 tiles), 48 tokens: 1 tile 82, 2 68, 3 68, 4 78, 5 55;
+//     2 and 3 tiles with 4 waves 65 and 60; 64 tokens: 5 tiles 65, 2 x 4 waves 83;
+//   18432 x 7168 (448 tiles), 48 tokens: 81, 63, 68, 75, 81;
+//   4096 x 4096 (256 tiles), 64 tokens: 31, 32, 35, 38, 43;
+//   1536 x 24576 (1536 tiles), 64 tokens: 80, 67, 54, 58, 67; 3 x 4 waves 46.
+template <int NT>
+void project_few(const AdapterProblem& p, hipStream_t stream) {
+  switch ((p.N / 16 + 255) / 256) {
+    case 1: return project<NT, 1, 8>(p, stream);
+    case 2: return project<NT, 2, 8>(p, stream);
+    case 3: return project<NT, 3, 8>(p, stream);
+    case 4: return project<NT, 4, 8>(p, stream);
+    case 5: return project<NT, 5, 8>(p, stream);
+    default: return project<NT, 3, 4>(p, stream);
   }
 }
 
@@ -1088,10 +1106,10 @@ hipError_t launch_adapter_few(const AdapterProblem& p, hipStream_t stream) {
   hipLaunchKernelGGL(adapter_prepare_kernel, dim3(shrink_blocks + quant_blocks(p.T, p.K)), dim3(kB), 0, stream, p,
                      shrink_blocks, step);
   switch (chunks) {
-    case 1: project<1>(p, stream); break;
-    case 2: project<2>(p, stream); break;
-    case 3: project<3>(p, stream); break;
-    default: project<4>(p, stream); break;
+    case 1: project_few<1>(p, stream); break;
+    case 2: project_few<2>(p, stream); break;
+    case 3: project_few<3>(p, stream); break;
+    default: project_few<4>(p, stream); break;
   }
   return hipGetLastError();
 }

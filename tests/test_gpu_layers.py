@@ -480,11 +480,26 @@ def test_adapters_with_infinite_weights_stay_among_their_tokens(gpu_lib, T):
 @pytest.mark.parametrize("T,N,K,r", [(1, 4096, 128, 8), (33, 4096, 256, 40), (64, 4224, 128, 128), (5, 16384, 128, 16),
                                      (47, 16512, 128, 64), (64, 16384, 256, 32)])
 def test_adapter_linear_wide_outputs(gpu_lib, T, N, K, r):
-    """The widths at which a workgroup takes two and four tiles of columns."""
+    """Widths at which a workgroup takes one, two and four tiles of columns."""
     n = 5
     wq, ws, A, B, sc = make_adapters(N, K, n, r, 130)
     xb = syn.gaussian((T, K), seed=131)
     ids = np.random.default_rng(132).integers(-1, n, T).astype(np.int32)
+    f64 = lambda bits: quant.bf16_to_f32(bits).astype(np.float64)
+    y = gpu_lib.adapter_linear(bf16_dev(xb), dev(tile_codes(wq)), dev(ws), bf16_dev(A), bf16_dev(B), dev(ids), scales=dev(sc))
+    check_adapters(y, *layers.adapters(xb, wq, ws, f64(A), f64(B), ids, sc))
+
+
+@pytest.mark.parametrize("T,N,K,r", [(64, 8320, 128, 16), (17, 12288, 256, 8), (64, 12416, 128, 32), (48, 16512, 384, 24),
+                                     (64, 20480, 128, 128), (1, 18432, 128, 16), (64, 20608, 256, 16), (33, 24576, 128, 64)])
+def test_adapter_linear_columns_of_a_workgroup(gpu_lib, T, N, K, r):
+    """Widths at which a workgroup takes three, four and five tiles of columns,
+    the last workgroup fewer, and those that take several workgroups a CU."""
+    n = 70
+    wq, ws, A, B, sc = make_adapters(N, K, n, r, 133)
+    xb = syn.activation_with_outliers(T, K, seed=134)
+    ids = np.random.default_rng(135).permutation(n)[:T].astype(np.int32)
+    ids[T // 2] = -1
     f64 = lambda bits: quant.bf16_to_f32(bits).astype(np.float64)
     y = gpu_lib.adapter_linear(bf16_dev(xb), dev(tile_codes(wq)), dev(ws), bf16_dev(A), bf16_dev(B), dev(ids), scales=dev(sc))
     check_adapters(y, *layers.adapters(xb, wq, ws, f64(A), f64(B), ids, sc))
