@@ -468,8 +468,10 @@ __host__ __device__ inline int plan_parts(const MoeProblem& p) {
   return (p.local < slots ? p.local : slots) + slots / 16;
 }
 __device__ __forceinline__ void make_plan(const MoeProblem& p, int span) {
-  __shared__ int16_t active[kMoeMaxTokens * kMoeMaxTopK + kMoeMaxTokens * kMoeMaxTopK / 16];
-  __shared__ int16_t first[kMoeMaxTokens * kMoeMaxTopK + kMoeMaxTokens * kMoeMaxTopK / 16 + 1];
+  constexpr int kSlots = kMoeMaxTokens * kMoeMaxTopK, kParts = kSlots + kSlots / 16;
+  __shared__ int from[kParts];          // a part's first entry in p.lists
+  __shared__ int16_t first[kParts + 1];
+  __shared__ int entry[kSlots];         // where in p.lists the plan's slots come from
   __shared__ int n_parts;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, most = plan_parts(p);
   int32_t* plan_expert = p.plan + 1;
@@ -492,7 +494,7 @@ __device__ __forceinline__ void make_plan(const MoeProblem& p, int span) {
       }
       for (int q = 0; q < parts; ++q) {
         const int at = np + ip - parts + q, s0 = ns + ic - cnt + q * span;
-        active[at] = (int16_t)(c + lane);
+        from[at] = (c + lane) * kMoeMaxTokens + q * span;
         first[at] = (int16_t)s0;
         plan_expert[at] = c + lane;
         plan_start[at] = s0;
@@ -508,15 +510,14 @@ __device__ __forceinline__ void make_plan(const MoeProblem& p, int span) {
     }
   }
   __syncthreads();
-  for (int a = wave; a < n_parts; a += kW) {
-    int head = a;                   // the expert's first part
-    while (head > 0 && active[head - 1] == active[a]) --head;
-    const int n = first[a + 1] - first[a];
-    if (lane < n) {
-      const int s = p.lists[active[a] * kMoeMaxTokens + (a - head) * span + lane];
-      plan_slot[first[a] + lane] = s;
-      plan_gate[first[a] + lane] = p.slot_gate[s];
-    }
+  for (int a = wave; a < n_parts; a += kW)
+    if (lane < first[a + 1] - first[a]) entry[first[a] + lane] = from[a] + lane;
+  __syncthreads();
+  // all slots at once: two round trips to memory
+  for (int i = threadIdx.x; i < first[n_parts]; i += kB) {
+    const int s = p.lists[entry[i]];
+    plan_slot[i] = s;
+    plan_gate[i] = p.slot_gate[s];
   }
 }
 
