@@ -102,10 +102,16 @@ hipError_t launch_moe_few_tokens(const MoeProblem& p, hipStream_t stream);
 constexpr int kAdapterFewTokens = 64;   // the most tokens of the few-token form
 constexpr int kAdapterMaxRank = 128;
 constexpr int kAdapterSplits = 8;
-// shares of K of the shrink: for prompts no more than fill the card
+// Shares of K of the shrink.  Prompts: about four 128-wide blocks each, so that
+// a wave has one or two blocks' loads to wait for.  Measured at rank 64 with 1 /
+// 2 / 4 / 8 shares, us of a call with 1024 outputs: K = 2048, 1333 tokens 47 / 41
+// / 40 / 41; K = 7168, 4096 tokens 114 / 113 / 110 / 103; K = 18432, 8192 tokens
+// 484 / 450 / 407 / 396.  (One share that writes z itself and saves the launch
+// that adds the shares: the first of each.)
 inline int adapter_splits(int64_t T, int64_t K) {
-  const int64_t fill = (1024 + (T + 15) / 16 - 1) / ((T + 15) / 16);
-  return dot_splits(K, (int)(fill < kAdapterSplits ? fill : kAdapterSplits));
+  if (T <= kAdapterFewTokens) return dot_splits(K, kAdapterSplits);
+  const int64_t s = (K / 128 + 3) / 4;
+  return (int)(s < kAdapterSplits ? s : kAdapterSplits);
 }
 struct AdapterProblem {
   int64_t T, N, K;
