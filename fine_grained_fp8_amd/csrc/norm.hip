@@ -176,8 +176,8 @@ __device__ __forceinline__ float rsqrt_refined(float v) {
 // more runs a lane, fewer rows are in flight per CU and the registers of w and b
 // double.  Bound by memory for plain output (8192 x 7168 BF16: 44.4 us, 5.3
 // TB/s; a copy of the same bytes reaches 4.9 - 5.2) and about evenly by memory
-// and the vector unit with codes (43.8 us, 178 MB; of which the scales' 4-byte
-// stores 3.5 us).  Measured against it at that size, us plain / with codes: two
+// and the vector unit with codes (43.4 us, 178 MB; loading the next row ahead 44.6).
+// Measured against it at that size, us plain / with codes: two
 // runs and 512 lanes 45.6 / 42.8, four and 256 lanes 59 / 77, a wave a row with
 // w and b in LDS 61 / 52.
 // The codes are those of the FP32 result: a value within a few FP32 ulp of the
@@ -198,7 +198,11 @@ __global__ __launch_bounds__(B) void layer_norm_kernel(LayerNormProblem p) {
     load_affine<kVec, G>(p.b, p.w_fp32, 0.f, i, l, cols, b[i]);
   }
   const float fc = (float)cols, inv_c = 1.0f / fc;
-  for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < p.rows; r0 += (int64_t)gridDim.x * kRows) {
+  // workgroups are dealt to the 8 XCDs in turn: each XCD's take neighbouring
+  // rows, whose scales then meet in its L2 and leave as whole lines (at 8192 x
+  // 7168 60.6 MB are written; in the plain order 73.4, and 0.5 us more)
+  const int64_t first = kQuant && gridDim.x % 8 == 0 ? blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8 : blockIdx.x;
+  for (int64_t r0 = first * kRows; r0 < p.rows; r0 += (int64_t)gridDim.x * kRows) {
     const int64_t row = r0 + grp;
     const bool on = row < p.rows;
     float x[NV][8];
@@ -244,10 +248,10 @@ __global__ __launch_bounds__(B) void layer_norm_kernel(LayerNormProblem p) {
       if (!kQuant || p.y != nullptr) store8<kVec, G>(static_cast<T*>(p.y) + row * p.ldy, i, l, cols, y);
       if constexpr (kQuant) {
         // the run of 16 lanes is one 1x128 tile
-        uint32_t t = 0;
+        float a = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) t = max(t, __float_as_uint(y[k]) & 0x7FFFFFFFu);
-        t = row16_max_u32(t);
+        for (int k = 0; k < 8; ++k) a = __builtin_elementwise_maximum(a, fabsf(y[k]));   // NaN stays
+        const uint32_t t = row16_max_u32(__float_as_uint(a) & 0x7FFFFFFFu);
         const int c = column<true, G>(i, 0, l);
         float sc;
         const uint2 q = quant8_f32(y, t, sc);
