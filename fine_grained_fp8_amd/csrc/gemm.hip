@@ -1163,14 +1163,17 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
   // hold one of its rows are read back, and B_a z is added by the BF16 matrix
   // unit (z comes as two BF16 terms), the rows of other adapters as zero
   // columns.  Then whole row segments are rounded and stored, as above.
-  auto store_tile_adapters = [&](int64_t em0, int64_t em_end, int64_t en0) {
+  // 4096 x 18432 x 7168, rank 16, segments of 512 rows: 477 us (no adapters
+  // 428 - 437; the ids asked for at the tile's end 491 - 509), rank 64, one
+  // adapter: 494 (518); 1333 x 7168 x 2048, rank 64, segments of 97: 59 (42
+  // without).  What it adds is mostly latency: a step's loads, L2 hits, for
+  // eight matrix products a subtile; a third step in flight would spill.
+  auto store_tile_adapters = [&](int64_t em0, int64_t em_end, int64_t en0, int id0, int id1) {
     const AdapterEpilogue& ad = p.adapters;
     const int64_t n0w = en0 + wave * 64;
     uint8_t* ob = wave == 0 ? lds_z0 : wave == 1 ? lds_z1 : wave == 2 ? lds_z2 : lds_z3;
     if (n0w >= p.N) return;   // N is a multiple of 128: the wave's 64 columns are all in or all out
     const uint16_t* bcol = ad.B + (n0w + lrow) * ad.r;
-    const int id0 = em0 + lane < em_end ? ad.ids[em0 + lane] : -1;
-    const int id1 = em0 + 64 + lane < em_end ? ad.ids[em0 + 64 + lane] : -1;
     // A step is 32 ranks of one adapter in one half; the next step is asked for
     // before the present one's products.  (a, rows, r0): the last one asked for;
     // left: the half's rows whose adapters are still to come.
@@ -1310,6 +1313,13 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
     while (next < work_ids && !setup_tile(next)) next += gridDim.x;
     more = next < work_ids;
   }
+  int id0 = -1, id1 = -1;
+  if constexpr (kAdapters) {
+    // the tile's ids, asked for here: at its end they would return after the next
+    // item's first blocks
+    if (m0 + lane < m_end) id0 = p.adapters.ids[m0 + lane];
+    if (m0 + 64 + lane < m_end) id1 = p.adapters.ids[m0 + 64 + lane];
+  }
   if (!more) {
     // no next item: its "first blocks" are this tile's last block
     nx_kb_lo = kb_hi - 1;
@@ -1419,11 +1429,11 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
     if (tid == 0) p.ws_count[et] = 0u;
     // the split path ends here and never reaches the K loop again (the
     // compiler's wait analysis would otherwise carry its loads into the loop)
-    if constexpr (kAdapters) store_tile_adapters(em0, em_end, en0);
+    if constexpr (kAdapters) store_tile_adapters(em0, em_end, en0, id0, id1);
     else store_tile(em0, em_end, en0, erows_m, erows_n);
     return;
   }
-  if constexpr (kAdapters) store_tile_adapters(em0, em_end, en0);
+  if constexpr (kAdapters) store_tile_adapters(em0, em_end, en0, id0, id1);
   else store_tile(em0, em_end, en0, erows_m, erows_n);
   if (!more) {
     wait_vm<0>();   // the reloads streamed by the last round land before the workgroup ends
