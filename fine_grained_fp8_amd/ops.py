@@ -24,6 +24,38 @@ def _stream(stream=None) -> int:
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
+def _empty(shape, dtype, device, stream, scratch=False):
+    """Uninitialized memory for a call on `stream` (None: the current one).
+
+    It comes from the pool of the stream that the kernels run on: a block of
+    the current stream's pool may still be in use by work pending there (a
+    former call's scratch goes back to the pool when that call returns), which
+    a kernel on another stream would not wait for.  What the call returns is
+    the caller's to read on the current stream, so that stream's work holds
+    the memory back when the tensor is dropped; scratch is seen by `stream`
+    alone."""
+    if stream is None or stream.cuda_stream == _stream():
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if not scratch:
+        t.record_stream(current)
+    return t
+
+
+def _empty_as(x, stream):
+    """A contiguous tensor of x's shape and type (the short call where x is one)."""
+    if stream is None and x.is_contiguous():
+        return torch.empty_like(x)
+    return _empty(x.shape, x.dtype, x.device, stream)
+
+
+def _workspace(nbytes: int, device, stream):
+    """Scratch memory of one call (nbytes -1: the call itself refuses)."""
+    return _empty(max(nbytes, 0), torch.uint8, device, stream, scratch=True)
+
+
 def _ptr(t):
     return None if t is None else ctypes_ptr(t)
 
@@ -457,25 +489,10 @@ def _norm_affine(weight, bias, cols):
     return _is_fp32(t)
 
 
-def _empty_as(x):
-    """A contiguous tensor of x's shape and type (the short call where x is one)."""
-    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-
-
 def _same_device(dev, **tensors):
     for name, t in tensors.items():
         if t is not None and t.device != dev:
             raise ValueError(f"{name}: on {t.device}, the input is on {dev}")
-
-
-def _workspace(nbytes: int, device, stream):
-    """Scratch memory of one call.  It comes from the current stream's memory
-    pool; a call on another stream tells the pool, so that the memory is not
-    handed out again before that stream is done with it."""
-    ws = torch.empty(max(nbytes, 0), dtype=torch.uint8, device=device)   # -1: the call itself refuses
-    if stream is not None and stream.cuda_stream != _stream():
-        ws.record_stream(stream)
-    return ws
 
 
 def layer_norm(x: torch.Tensor, weight=None, bias=None, *, eps: float = 1e-5, return_stats: bool = False,
@@ -492,15 +509,15 @@ def layer_norm(x: torch.Tensor, weight=None, bias=None, *, eps: float = 1e-5, re
     wt = _norm_affine(weight, bias, cols)
     _same_device(x.device, weight=weight, bias=bias, out=out)
     if out is None:
-        out = _empty_as(x)
+        out = _empty_as(x, stream)
     else:
         _check_2d("out", out, (x.dtype,))
         if out.shape != x.shape:
             raise ValueError(f"out: expected {tuple(x.shape)}, got {tuple(out.shape)}")
     mean = rstd = None
     if return_stats:
-        mean = torch.empty(rows, dtype=torch.float32, device=x.device)
-        rstd = torch.empty_like(mean)
+        mean = _empty(rows, torch.float32, x.device, stream)
+        rstd = _empty_as(mean, stream)
     st = lib.fp8_layer_norm(_ptr(x), rows, cols, x.stride(0), _is_fp32(x), _ptr(weight), _ptr(bias), wt, eps,
                             _ptr(out), out.stride(0), _ptr(mean), _ptr(rstd), None, 0, None, 0, _stream(stream))
     _lib.check("fp8_layer_norm", st)
@@ -519,13 +536,13 @@ def layer_norm_quant(x: torch.Tensor, weight=None, bias=None, *, eps: float = 1e
     rows, cols = x.shape
     wt = _norm_affine(weight, bias, cols)
     _same_device(x.device, weight=weight, bias=bias)
-    q = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
-    s = torch.empty((cols // 128, round_up(rows, 4)), dtype=torch.float32, device=x.device)
-    y = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if return_y else None
+    q = _empty((rows, cols), torch.uint8, x.device, stream)
+    s = _empty((cols // 128, round_up(rows, 4)), torch.float32, x.device, stream)
+    y = _empty((rows, cols), x.dtype, x.device, stream) if return_y else None
     mean = rstd = None
     if return_stats:
-        mean = torch.empty(rows, dtype=torch.float32, device=x.device)
-        rstd = torch.empty_like(mean)
+        mean = _empty(rows, torch.float32, x.device, stream)
+        rstd = _empty_as(mean, stream)
     st = lib.fp8_layer_norm(_ptr(x), rows, cols, x.stride(0), _is_fp32(x), _ptr(weight), _ptr(bias), wt, eps,
                             _ptr(y), cols, _ptr(mean), _ptr(rstd), _ptr(q), cols, _ptr(s), s.stride(0),
                             _stream(stream))
@@ -550,9 +567,9 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
     _check_vec("mean", mean, rows, (torch.float32,))
     _check_vec("rstd", rstd, rows, (torch.float32,))
     _same_device(x.device, dy=dy, mean=mean, rstd=rstd, weight=weight)
-    dx = _empty_as(x)
-    dweight = torch.empty(cols, dtype=torch.float32, device=x.device)
-    dbias = torch.empty_like(dweight)
+    dx = _empty_as(x, stream)
+    dweight = _empty(cols, torch.float32, x.device, stream)
+    dbias = _empty_as(dweight, stream)
     nbytes = lib.fp8_layer_norm_backward_workspace(rows, cols)
     ws = _workspace(nbytes, x.device, stream)
     st = lib.fp8_layer_norm_backward(_ptr(dy), dy.stride(0), _ptr(x), x.stride(0), rows, cols, _is_fp32(x),
@@ -604,15 +621,15 @@ def moe_few_tokens(x: torch.Tensor, router: torch.Tensor, w13: torch.Tensor, s13
     _check_vec("bias", bias, E, (torch.float32,))
     _same_device(x.device, router=router, w13=w13, s13=s13, w2=w2, s2=s2, bias=bias, out=out)
     if out is None:
-        out = torch.empty((T, H), dtype=out_dtype, device=x.device)
+        out = _empty((T, H), out_dtype, x.device, stream)
     else:
         _check_2d("out", out, _FLOATS)
         if out.shape != x.shape:
             raise ValueError(f"out: expected {tuple(x.shape)}, got {tuple(out.shape)}")
     ids = gates = None
     if return_routing:
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=x.device)
-        gates = torch.empty((T, top_k), dtype=torch.float32, device=x.device)
+        ids = _empty((T, top_k), torch.int32, x.device, stream)
+        gates = _empty((T, top_k), torch.float32, x.device, stream)
     nbytes = lib.fp8_moe_few_tokens_workspace(T, H, I, E, local, top_k)
     ws = _workspace(nbytes, x.device, stream)
     st = lib.fp8_moe_few_tokens(T, H, I, E, first_expert, local, top_k, _ptr(x), x.stride(0), _ptr(router),
@@ -652,7 +669,7 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, sw: torch.Tensor, lora_a: t
     _check_vec("scales", scales, n, (torch.float32,))
     _same_device(x.device, w=w, sw=sw, lora_a=lora_a, lora_b=lora_b, ids=ids, scales=scales, out=out)
     if out is None:
-        out = torch.empty((T, N), dtype=out_dtype, device=x.device)
+        out = _empty((T, N), out_dtype, x.device, stream)
     else:
         _check_2d("out", out, _FLOATS)
         if tuple(out.shape) != (T, N):

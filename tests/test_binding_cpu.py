@@ -1,0 +1,118 @@
+"""The binding's own work (ops.py), on the CPU: a stand-in library records the
+calls, and streams and the memory pool are recorded instead of used."""
+import contextlib
+import types
+
+import pytest
+import torch
+
+from fine_grained_fp8_amd import ops
+
+
+class Recorder:
+    """Which stream was current at each allocation, and which streams each
+    tensor was reported to."""
+
+    def __init__(self, monkeypatch):
+        self.current = types.SimpleNamespace(cuda_stream=1)
+        self.side = types.SimpleNamespace(cuda_stream=2)
+        self.born, self.told, self.calls = {}, {}, []
+        self.keep = []          # no address comes back within a test
+        for name in ("empty", "full"):
+            monkeypatch.setattr(torch, name, self.tracked(getattr(torch, name)))
+        monkeypatch.setattr(torch, "empty_like", self.tracked(torch.empty_like))
+        monkeypatch.setattr(torch.Tensor, "record_stream",
+                            lambda t, s: self.told.setdefault(t.data_ptr(), []).append(s.cuda_stream), raising=False)
+        monkeypatch.setattr(torch.cuda, "stream", self.use)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: self.current)
+        monkeypatch.setattr(ops, "_stream", lambda s=None: (self.current if s is None else s).cuda_stream)
+        for check in ("_check_2d", "_check_vec"):
+            monkeypatch.setattr(ops, check, lambda *a, **k: None)
+        monkeypatch.setattr(ops._lib, "load_library", lambda path=None: self)
+
+    def tracked(self, make):
+        def made(*args, **kwargs):
+            t = make(*args, **kwargs)
+            self.born[t.data_ptr()] = self.current.cuda_stream
+            self.keep.append(t)
+            return t
+        return made
+
+    @contextlib.contextmanager
+    def use(self, stream):
+        before, self.current = self.current, stream
+        yield
+        self.current = before
+
+    def __getattr__(self, name):
+        if not name.startswith("fp8_"):
+            raise AttributeError(name)
+
+        def entry(*args):
+            if name.endswith("_workspace"):
+                return 4096
+            self.calls.append((name, args))
+            return 0
+        return entry
+
+
+@pytest.fixture
+def rec(monkeypatch):
+    return Recorder(monkeypatch)
+
+
+def bf16(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def codes(*shape):
+    return torch.zeros(shape, dtype=torch.uint8)
+
+
+def scales(*shape):
+    return torch.ones(shape)
+
+
+LAYER_CALLS = {
+    "layer_norm": lambda **k: ops.layer_norm(bf16(4, 256), return_stats=True, **k),
+    "layer_norm_quant": lambda **k: ops.layer_norm_quant(bf16(4, 256), return_y=True, return_stats=True, **k),
+    "layer_norm_backward": lambda **k: ops.layer_norm_backward(bf16(4, 256), bf16(4, 256), scales(4), scales(4), **k),
+    "moe_few_tokens": lambda **k: ops.moe_few_tokens(bf16(4, 256), bf16(8, 256), codes(2, 256, 256), scales(2, 2, 2),
+                                                     codes(2, 256, 128), scales(2, 2, 1), top_k=2, return_routing=True, **k),
+    "adapter_linear": lambda **k: ops.adapter_linear(bf16(4, 256), codes(384, 256), scales(3, 2), bf16(3, 16, 256),
+                                                     bf16(3, 384, 16), torch.zeros(4, dtype=torch.int32), **k),
+}
+SCRATCH = {"layer_norm_backward", "moe_few_tokens", "adapter_linear"}
+
+
+def check_memory_of_a_call(rec, call, scratch):
+    """On a stream that is not the current one a call's memory comes from that
+    stream's pool: memory of the current stream's pool may still be in use by
+    work that the current stream has pending (a former call's scratch is free
+    to the pool as soon as that call returned)."""
+    before = set(rec.born)
+    out = call(stream=rec.side)
+    out = [t for t in (out if isinstance(out, tuple) else (out,)) if t is not None]
+    new = set(rec.born) - before
+    (_, args), = rec.calls
+    assert args[-1] == 2
+    used = {a for a in args if a in new}
+    assert {t.data_ptr() for t in out} <= used
+    assert all(rec.born[a] == 2 for a in used), {a: rec.born[a] for a in used}
+    # the caller's later work on the current stream holds an output's memory back
+    assert all(1 in rec.told.get(t.data_ptr(), []) for t in out)
+    assert len(used) == len(out) + scratch
+    assert rec.current.cuda_stream == 1
+
+
+@pytest.mark.parametrize("name", LAYER_CALLS)
+def test_memory_of_a_call_on_another_stream(rec, name):
+    check_memory_of_a_call(rec, LAYER_CALLS[name], int(name in SCRATCH))
+
+
+@pytest.mark.parametrize("name", LAYER_CALLS)
+def test_memory_of_a_call_on_the_current_stream(rec, name):
+    for kwargs in ({}, {"stream": rec.current}):
+        LAYER_CALLS[name](**kwargs)
+    assert all(args[-1] == 1 for _, args in rec.calls)
+    assert set(rec.born.values()) == {1} and not rec.told

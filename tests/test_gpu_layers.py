@@ -559,6 +559,40 @@ def test_layer_norm_past_32_bit_offsets(gpu_lib):
     assert torch.allclose(dw, wdw, rtol=1e-5, atol=1e-5) and torch.allclose(db, wdb, rtol=1e-5, atol=1e-5)
 
 
+# ------------------------------------------------------------- streams
+
+def test_calls_on_two_streams_at_once(gpu_lib):
+    """Calls queued on another stream while the current stream still runs
+    calls whose scratch memory has gone back to the pool: neither waits for
+    the other, and each has its own results."""
+    N, K, n, r = 384, 512, 3, 16
+    wq, ws, A, B, _ = make_adapters(N, K, n, r, 170)
+    rest = (dev(tile_codes(wq)), dev(ws), bf16_dev(A), bf16_dev(B))
+    _, _, d = make_experts(4, K, 128, 171)
+    router = bf16_dev(syn.gaussian((4, K), seed=172, std=0.1))
+    side = torch.cuda.Stream()
+    for T in (8, 200):
+        xs = [bf16_dev(syn.gaussian((T, K), seed=173 + i)) for i in range(2)]
+        ids = dev(np.arange(T, dtype=np.int32) % n)
+        stats = [gpu_lib.layer_norm(x, return_stats=True) for x in xs]
+
+        def calls(i, stream=None):
+            _, mean, rstd = stats[i]
+            out = list(gpu_lib.layer_norm_backward(xs[i], xs[i], mean, rstd, stream=stream))
+            out.append(gpu_lib.adapter_linear(xs[i], *rest, ids, stream=stream))
+            out.append(gpu_lib.moe_few_tokens(xs[i][:64], router, **d, top_k=2, stream=stream))
+            return out
+
+        want = [calls(0), calls(1)]
+        torch.cuda.synchronize()
+        for _ in range(20):
+            here = calls(0)
+            there = calls(1, side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(here, want[0]))
+        assert all(torch.equal(a, b) for a, b in zip(there, want[1]))
+
+
 # ------------------------------------------------------------- graphs, refusals
 
 def test_operators_replay_from_a_graph(gpu_lib):
