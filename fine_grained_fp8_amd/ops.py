@@ -114,7 +114,7 @@ def quant_act_1x128(x: torch.Tensor, direction: str = "row", *, scales_in=None,
     else:
         raise ValueError(direction)
     if out is None:
-        q = torch.empty(q_shape, dtype=torch.uint8, device=dev)
+        q = _empty(q_shape, torch.uint8, dev, stream)
     else:
         _check_2d("out", out, (torch.uint8, torch.float8_e4m3fn))
         if tuple(out.shape) != q_shape or not out.is_contiguous():
@@ -131,10 +131,9 @@ def quant_act_1x128(x: torch.Tensor, direction: str = "row", *, scales_in=None,
         scales = scales_out
         ld_s = scales_out.stride(0)
     else:
-        scales = torch.empty(s_shape, dtype=torch.float32, device=dev)
+        scales = _empty(s_shape, torch.float32, dev, stream)
         ld_s = s_shape[1]
-    amax = torch.empty(s_shape if scales_in is None else tuple(scales_in.shape),
-                       dtype=torch.float32, device=dev) if return_amax else None
+    amax = _empty(s_shape if scales_in is None else tuple(scales_in.shape), torch.float32, dev, stream) if return_amax else None
     st = lib.fp8_quant_act_1x128(
         _ptr(x), rows, cols, x.stride(0), tile_dir, _ptr(q), q.stride(0),
         _ptr(scales), ld_s, _ptr(scales_in), _ptr(amax), _ptr(sat_count), _stream(stream))
@@ -152,10 +151,10 @@ def quant_act_dual(x: torch.Tensor, *, tiled: bool = False, stream=None):
     lib = _lib.load_library()
     _check_2d("x", x, _BF16)
     rows, cols = x.shape
-    q_row = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
-    s_row = torch.empty((cols // 128, round_up(rows, 4)), dtype=torch.float32, device=x.device)
-    q_col = torch.empty((cols, rows), dtype=torch.uint8, device=x.device)
-    s_col = torch.empty((rows // 128, round_up(cols, 4)), dtype=torch.float32, device=x.device)
+    q_row = _empty((rows, cols), torch.uint8, x.device, stream)
+    s_row = _empty((cols // 128, round_up(rows, 4)), torch.float32, x.device, stream)
+    q_col = _empty((cols, rows), torch.uint8, x.device, stream)
+    s_col = _empty((rows // 128, round_up(cols, 4)), torch.float32, x.device, stream)
     if tiled:
         st = lib.fp8_quant_act_dual_tiled(_ptr(x), rows, cols, x.stride(0), _ptr(q_row), q_row.stride(0),
                                           _ptr(s_row), s_row.stride(0), _ptr(q_col), _ptr(s_col),
@@ -180,9 +179,9 @@ def quant_weight_128x128(w: torch.Tensor, *, transposed: bool = False, tiled: bo
     lib = _lib.load_library()
     _check_2d("w", w, _BF16)
     rows, cols = w.shape
-    q = torch.empty((rows, cols), dtype=torch.uint8, device=w.device)
-    q_t = torch.empty((cols, rows), dtype=torch.uint8, device=w.device) if transposed else None
-    scales = torch.empty((rows // 128, cols // 128), dtype=torch.float32, device=w.device)
+    q = _empty((rows, cols), torch.uint8, w.device, stream)
+    q_t = _empty((cols, rows), torch.uint8, w.device, stream) if transposed else None
+    scales = _empty((rows // 128, cols // 128), torch.float32, w.device, stream)
     if tiled:
         st = lib.fp8_quant_weight_128x128_tiled(_ptr(w), rows, cols, w.stride(0), _ptr(q), _ptr(q_t),
                                                 _ptr(scales), scales.stride(0), _stream(stream))
@@ -227,7 +226,7 @@ def block_gemm(layout: str, A: torch.Tensor, sA: torch.Tensor, B: torch.Tensor, 
     M, K = A.shape
     N = B.shape[1] if layout == "dgrad" else B.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=A.device)
+        out = _empty((M, N), out_dtype, A.device, stream)
     code = _lib.OUT_FP32 if out.dtype == torch.float32 else _lib.OUT_BF16
     st = getattr(lib, _entry)(
         _lib.LAYOUT[layout], M, N, K, _ptr(A), A.stride(0), _ptr(sA), sA.stride(0),
@@ -254,12 +253,12 @@ def block_gemm_fused_quant(x: torch.Tensor, W: torch.Tensor, sW: torch.Tensor, *
     M, K = x.shape
     N = W.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        out = _empty((M, N), out_dtype, x.device, stream)
     code = _lib.OUT_FP32 if out.dtype == torch.float32 else _lib.OUT_BF16
     q = s = None
     if with_codes:
-        q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
-        s = torch.empty((K // 128, round_up(M, 4)), dtype=torch.float32, device=x.device)
+        q = _empty((M, K), torch.uint8, x.device, stream)
+        s = _empty((K // 128, round_up(M, 4)), torch.float32, x.device, stream)
     st = lib.fp8_block_gemm_fused_quant(
         M, N, K, _ptr(x), x.stride(0), _ptr(W), W.stride(0), _ptr(sW), sW.stride(0), _ptr(out), code,
         out.stride(0), _ptr(q) if q is not None else None, q.stride(0) if q is not None else 0,
@@ -287,7 +286,7 @@ def block_gemm_grouped(offsets: torch.Tensor, A: torch.Tensor, sA: torch.Tensor,
     G, N, K = B.shape
     total_M = A.shape[0]
     if out is None:
-        out = torch.empty((total_M, N), dtype=out_dtype, device=A.device)
+        out = _empty((total_M, N), out_dtype, A.device, stream)
     code = _lib.OUT_FP32 if out.dtype == torch.float32 else _lib.OUT_BF16
     if tiled:
         st = lib.fp8_block_gemm_grouped_tiled(
@@ -321,7 +320,7 @@ def cast_e4m3(x: torch.Tensor, *, out=None, stream=None):
     if x.dtype != torch.float32 or not x.is_contiguous() or not x.is_cuda:
         raise ValueError("x: contiguous float32 device tensor required")
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        out = _empty(x.shape, torch.uint8, x.device, stream)
     st = lib.fp8_cast_e4m3(_ptr(x), x.numel(), _ptr(out), _stream(stream))
     _lib.check("fp8_cast_e4m3", st)
     return out
@@ -350,7 +349,7 @@ def pack_tokens(x: torch.Tensor, src_rows=None, *, T=None, stride=None, out=None
         T = rows
     stride = round_up(message_bytes(H), 16) if stride is None else stride
     if out is None:
-        out = torch.empty((T, stride), dtype=torch.uint8, device=x.device)
+        out = _empty((T, stride), torch.uint8, x.device, stream)
     st = lib.fp8_pack_tokens(_ptr(x), rows, H, x.stride(0), _ptr(src_rows), T, _ptr(out),
                              out.stride(0), _stream(stream))
     _lib.check("fp8_pack_tokens", st)
@@ -363,8 +362,8 @@ def unpack_tokens(msg: torch.Tensor, H: int, *, stream=None):
     lib = _lib.load_library()
     _check_2d("msg", msg, (torch.uint8,))
     T = msg.shape[0]
-    q = torch.empty((T, H), dtype=torch.uint8, device=msg.device)
-    s = torch.empty((H // 128, round_up(T, 4)), dtype=torch.float32, device=msg.device)
+    q = _empty((T, H), torch.uint8, msg.device, stream)
+    s = _empty((H // 128, round_up(T, 4)), torch.float32, msg.device, stream)
     st = lib.fp8_unpack_tokens(_ptr(msg), T, H, msg.stride(0), _ptr(q), q.stride(0), _ptr(s),
                                s.stride(0), _stream(stream))
     _lib.check("fp8_unpack_tokens", st)
@@ -376,7 +375,7 @@ def dequant_tokens(msg: torch.Tensor, H: int, *, stream=None):
     lib = _lib.load_library()
     _check_2d("msg", msg, (torch.uint8,))
     T = msg.shape[0]
-    y = torch.empty((T, H), dtype=torch.bfloat16, device=msg.device)
+    y = _empty((T, H), torch.bfloat16, msg.device, stream)
     st = lib.fp8_dequant_tokens(_ptr(msg), T, H, msg.stride(0), _ptr(y), y.stride(0), _stream(stream))
     _lib.check("fp8_dequant_tokens", st)
     return y
@@ -393,7 +392,7 @@ def gemm_promotion(A: torch.Tensor, B: torch.Tensor, promote_k: int, *, stream=N
     N = B.shape[0]
     if B.shape[1] != K:
         raise ValueError(f"A {tuple(A.shape)} and B {tuple(B.shape)}: K differs")
-    C = torch.empty((M, N), dtype=torch.float32, device=A.device)
+    C = _empty((M, N), torch.float32, A.device, stream)
     st = lib.fp8_gemm_promotion(_ptr(A), M, K, A.stride(0), _ptr(B), N, B.stride(0), promote_k,
                                 _ptr(C), C.stride(0), _stream(stream))
     _lib.check("fp8_gemm_promotion", st)
@@ -416,7 +415,7 @@ def probe_mfma(codes: torch.Tensor, workgroups: int, iters: int, mode: str = "pl
         raise ValueError("codes: a contiguous uint8 tensor of at least 4096 elements")
     if mode not in PROBE_MFMA_MODES:
         raise ValueError(f"mode: one of {sorted(PROBE_MFMA_MODES)}")
-    out = torch.empty(workgroups * 256, dtype=torch.float32, device=codes.device)
+    out = _empty(workgroups * 256, torch.float32, codes.device, stream)
     st = lib.fp8_probe_mfma(workgroups, iters, PROBE_MFMA_MODES[mode], _ptr(codes), _ptr(out), _stream(stream))
     _lib.check("fp8_probe_mfma", st)
     return out
@@ -428,7 +427,7 @@ def probe_recip_online(s: torch.Tensor, *, stream=None):
     lib = _lib.load_library()
     if s.dtype != torch.float32 or not s.is_contiguous():
         raise ValueError("s: a contiguous float32 tensor")
-    r = torch.empty_like(s)
+    r = _empty_as(s, stream)
     st = lib.fp8_probe_recip_online(_ptr(s), _ptr(r), s.numel(), _stream(stream))
     _lib.check("fp8_probe_recip_online", st)
     return r
@@ -455,8 +454,8 @@ def quant_act_tiles(x: torch.Tensor, tile: int = 128, rank: int = 1, *, sat_coun
     lib = _lib.load_library()
     _check_2d("x", x, _BF16)
     rows, cols = x.shape
-    q = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
-    s = torch.empty((cols // tile, round_up(rows, 4)), dtype=torch.float32, device=x.device)
+    q = _empty((rows, cols), torch.uint8, x.device, stream)
+    s = _empty((cols // tile, round_up(rows, 4)), torch.float32, x.device, stream)
     st = lib.fp8_quant_act_tiles(_ptr(x), rows, cols, x.stride(0), tile, rank, _ptr(q), q.stride(0),
                                  _ptr(s), s.stride(0), _ptr(sat_count), _stream(stream))
     _lib.check("fp8_quant_act_tiles", st)

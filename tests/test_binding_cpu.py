@@ -116,3 +116,31 @@ def test_memory_of_a_call_on_the_current_stream(rec, name):
         LAYER_CALLS[name](**kwargs)
     assert all(args[-1] == 1 for _, args in rec.calls)
     assert set(rec.born.values()) == {1} and not rec.told
+
+
+BASE_CALLS = {
+    "quant_act_1x128": lambda **k: ops.quant_act_1x128(bf16(4, 256), return_amax=True, **k),
+    "quant_act_dual": lambda **k: ops.quant_act_dual(bf16(128, 256), **k),
+    "quant_act_dual_tiled": lambda **k: ops.quant_act_dual(bf16(128, 256), tiled=True, **k),
+    "quant_weight_128x128": lambda **k: ops.quant_weight_128x128(bf16(128, 256), transposed=True, **k),
+    "quant_weight_128x128_tiled": lambda **k: ops.quant_weight_128x128(bf16(128, 256), tiled=True, transposed=True, **k),
+    "block_gemm": lambda **k: ops.block_gemm("fprop", codes(4, 256), scales(2, 4), codes(128, 256), scales(1, 2), **k),
+    "block_gemm_fused_quant": lambda **k: ops.block_gemm_fused_quant(bf16(4, 256), codes(128, 256), scales(1, 2),
+                                                                     with_codes=True, **k),
+    "block_gemm_grouped": lambda **k: ops.block_gemm_grouped(torch.zeros(3, dtype=torch.int32), codes(4, 256), scales(2, 4),
+                                                             codes(2, 128, 256), scales(2, 1, 2), **k),
+    "cast_e4m3": lambda **k: ops.cast_e4m3(scales(64), **k),
+    "pack_tokens": lambda **k: ops.pack_tokens(bf16(4, 256), **k),
+    "unpack_tokens": lambda **k: ops.unpack_tokens(codes(4, 272), 256, **k),
+    "dequant_tokens": lambda **k: ops.dequant_tokens(codes(4, 272), 256, **k),
+    "gemm_promotion": lambda **k: ops.gemm_promotion(codes(4, 256), codes(128, 256), 128, **k),
+    "probe_mfma": lambda **k: ops.probe_mfma(codes(4096), 2, 1, **k),
+    "probe_recip_online": lambda **k: ops.probe_recip_online(scales(64), **k),
+    "quant_act_tiles": lambda **k: ops.quant_act_tiles(bf16(4, 256), **k),
+}
+
+
+@pytest.mark.parametrize("name", BASE_CALLS)
+def test_outputs_of_the_other_calls_on_another_stream(rec, name, monkeypatch):
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True, raising=False)
+    check_memory_of_a_call(rec, BASE_CALLS[name], 0)
