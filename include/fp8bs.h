@@ -531,7 +531,9 @@ int64_t fp8_moe_few_tokens_workspace(int64_t T, int64_t H, int64_t I, int32_t E,
  *  ids     int32 [T]; a negative id has no adapter, an id >= adapters gives a
  *          row of NaN
  *  scales  optional FP32 [adapters] (NULL: ones)
- *  C       [T][ldc >= N], BF16 or FP32, rounded once from FP32 sums
+ *  C       [T][ldc >= N], BF16 or FP32, rounded once from FP32 sums; A_a x enters
+ *          the second product with 16 bits (2^-16).  Infinities and NaN in A, B
+ *          and x act as in the formula, on the rows of their own tokens
  *  N % 128 == 0, K % 128 == 0, rank % 8 == 0, rank <= 128.  Rows 16-byte
  *  aligned.  Limits as for fp8_block_gemm.  Above 64 tokens the projection
  *  runs on fp8_block_gemm's persistent kernel (and its per-stream workspace).

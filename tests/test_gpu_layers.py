@@ -704,3 +704,52 @@ def test_example_block(gpu_lib):
     for got, want in ((y, Y), (dx, X.grad), (dw, W.grad), (dnw, NW.grad), (dnb, NB.grad)):
         # both operands of every product rounded to E4M3: 2^-4 / sqrt(3) each at most, over many terms
         assert (got.float() - want).norm() <= 0.06 * want.norm()
+
+
+# ------------------------------------------------------------- infinities through an adapter's up product
+
+@pytest.mark.parametrize("T", [3, 24, 150])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_infinite_up_weights_give_the_formulas_values(gpu_lib, T, out_dtype):
+    """B_a z with infinite weights in B is an infinity of the sign of weight x z,
+    or NaN where two meet: also where z is a BF16 value itself (adapter 0 picks
+    values of x), and with ranks past the first matrix product's 32."""
+    N, K, n, r = 384, 256, 4, 40
+    wq, ws, A, B, sc = make_adapters(N, K, n, r, 180)
+    A[0] = 0
+    A[0, np.arange(r), np.arange(r)] = 0x3F80               # z_k = x_k
+    sc[0] = 1.0
+    B0 = B.copy()                                           # with 0 in place of the infinities
+    for a in range(n):
+        for row, k, bits in ((3, 5, 0x7F80), (70, 37, 0xFF80), (200, 0, 0x7F80), (200, 39, 0x7F80), (383, 8, 0xFF80)):
+            B[a, row, k], B0[a, row, k] = bits, 0
+    xb = syn.gaussian((T, K), seed=181)
+    ids = (np.arange(T) % (n + 1) - 1).astype(np.int32)
+    f64 = lambda bits: quant.bf16_to_f32(bits).astype(np.float64)
+    with np.errstate(invalid="ignore"):
+        Y = layers.adapters(xb, wq, ws, f64(A), f64(B), ids, sc)[0]
+    F, mag, low = layers.adapters(xb, wq, ws, f64(A), f64(B0), ids, sc)
+    bad = ~np.isfinite(Y)
+    assert np.isinf(Y).any() and bad.sum() == 4 * (ids >= 0).sum()
+    # every z that meets an infinity is far from 0, as FP32 sums see it
+    for a in range(n):
+        z = f64(xb)[ids == a] @ f64(A[a]).T[:, [0, 5, 8, 37, 39]]
+        assert (np.abs(z) > 1e-4).all()
+    y = host(gpu_lib.adapter_linear(bf16_dev(xb), dev(tile_codes(wq)), dev(ws), bf16_dev(A), bf16_dev(B), dev(ids),
+                                    scales=dev(sc), out_dtype=out_dtype))
+    assert np.array_equal(y[bad], Y[bad], equal_nan=True)
+    tol = out_ulp(out_dtype) * np.abs(F) + 2.0 ** -9 * mag + 2.0 ** -16 * low
+    assert (np.abs(y - F) <= tol)[~bad].all()
+
+
+@pytest.mark.parametrize("T", [2, 70])
+def test_adapter_sums_past_the_largest_bf16_value(gpu_lib, T):
+    """A x = 1.99609375 x 2^127 is an FP32 value that rounds to infinity in BF16."""
+    N, K, r = 128, 128, 8
+    x, A = torch.zeros(T, K, device="cuda"), torch.zeros(1, r, K, device="cuda")
+    x[:, 0], x[:, 1], A[0, 2, 0], A[0, 2, 1] = 1.9921875 * 2.0 ** 63, 1.0, 2.0 ** 64, 2.0 ** 119
+    B = torch.full((1, N, r), 2.0 ** -120, device="cuda").bfloat16()
+    y = gpu_lib.adapter_linear(x.bfloat16(), torch.zeros(N, K, dtype=torch.uint8, device="cuda"), torch.ones(1, 1, device="cuda"),
+                               A.bfloat16(), B, torch.zeros(T, dtype=torch.int32, device="cuda"), out_dtype=torch.float32)
+    # z to 2^-16, zero codes add nothing
+    assert (y - 255.5).abs().max() <= 255.5 * 2.0 ** -16
