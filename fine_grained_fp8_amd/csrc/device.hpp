@@ -185,19 +185,25 @@ __device__ __forceinline__ uint2 quant8_bf16(const uint4& d, float& s) {
 // bits (NaN patterns sort above infinity): s = max(fl32(amax / 448), floor).
 // fl32(amax / 448) is the Markstein form of div448_bf16, which equals the IEEE
 // quotient for every FP32 mantissa (a result below FP32's normal range lies
-// under the floor).  The values were rounded to FP32 themselves, so the
-// quotient is y r with r = 1 / s, within two FP32 ulp of fl32(y / s) (2^-18 of
-// a code's spacing) for a tenth of a division's operations; 448 (1 + 2^-22)
-// still rounds to the code of 448.
+// under the floor).
+// The quotient is y r + y l with 1 / s = r + l in two FP32 numbers, rounded once:
+// within 2^-42 of y / s before that, so the IEEE quotient but where y / s lies
+// that near the middle of two FP32 values (s past 2^100: 2^-30).  One operation
+// a value more than y r, which is up to two FP32 places off.  r is the hardware
+// reciprocal (1 ulp) lowered by two places, so that l > 0 and -0 keeps its sign.
 __device__ __forceinline__ uint2 quant8_f32(const float (&y)[8], uint32_t amax_bits, float& s) {
   if (amax_bits < 0x7F800000u) {
     s = fmaxf(div448_bf16(__uint_as_float(amax_bits)), scale_floor());
-    const float r = recip_online(s);
+    const float r = __uint_as_float(__float_as_uint(__builtin_amdgcn_rcpf(s)) - 2u);
+    const float e = __builtin_fmaf(-s, r, 1.0f), l = r * __builtin_fmaf(e, e, e);
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __builtin_fmaf(y[i], r, y[i] * l);
     int lo = 0, hi = 0;
-    lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0] * r, y[1] * r, lo, false);
-    lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[2] * r, y[3] * r, lo, true);
-    hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[4] * r, y[5] * r, hi, false);
-    hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[6] * r, y[7] * r, hi, true);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], lo, false);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], hi, false);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], hi, true);
     return make_uint2((uint32_t)lo, (uint32_t)hi);
   }
   s = __uint_as_float(amax_bits == 0x7F800000u ? amax_bits : kCanonicalNaN);

@@ -176,15 +176,16 @@ __device__ __forceinline__ float rsqrt_refined(float v) {
 // more runs a lane, fewer rows are in flight per CU and the registers of w and b
 // double.  Bound by memory for plain output (8192 x 7168 BF16: 44.4 us, 5.3
 // TB/s; a copy of the same bytes reaches 4.9 - 5.2) and about evenly by memory
-// and the vector unit with codes (43.4 us, 178 MB; loading the next row ahead 44.6).
-// Measured against it at that size, us plain / with codes: two
-// runs and 512 lanes 45.6 / 42.8, four and 256 lanes 59 / 77, a wave a row with
-// w and b in LDS 61 / 52.
-// The codes are those of the FP32 result: a value within a few FP32 ulp of the
-// middle between two codes may get the other one (2-norm over whole 8192 x 7168
-// arrays against 64 bits 4e-5 - 8e-5, as for an FP32 layer norm followed by
-// a division).  The row's sums, y and the quotient in FP64 would settle those:
-// 81 us.
+// and the vector unit with codes (44.2 us, 178 MB; with the quotient y r, up to two
+// FP32 places off, 42.4).  Measured against it at that size with that quotient,
+// us plain / with codes: the next row loaded ahead - / 44.6 for 43.4, two runs and
+// 512 lanes 45.6 / 42.8, four and 256 lanes 59 / 77, a wave a row with w and b in
+// LDS 61 / 52.
+// The codes are those of the FP32 result: where its sums' rounding moves a value
+// over the middle between two codes it gets the other one (2-norm over whole
+// 4096 - 8192 x 7168 arrays against 64 bits 3.4e-5 - 8.4e-5, an FP32 layer norm
+// followed by a division 3.9e-5 - 9.2e-5).  The row's sums, y and the quotient in
+// FP64 would settle those: 81 us.
 template <typename T, bool kVec, int G, int B, int NV, bool kQuant>
 __global__ __launch_bounds__(B) void layer_norm_kernel(LayerNormProblem p) {
   constexpr int kRows = B / G;

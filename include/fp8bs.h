@@ -456,7 +456,8 @@ fp8_status fp8_dequant_tokens(const uint8_t* msg, int64_t T, int64_t H, int64_t 
  *          scales [cols/128][ld_s >= rows] of y's 1x128 row tiles, in the
  *          operand layout of fp8_quant_act_1x128 ROW, formed from the FP32
  *          values of y (not from BF16-rounded ones) by the same rule; the
- *          quotient y / s may differ from the IEEE one by two FP32 ulp.
+ *          quotient y / s is rounded once to FP32, from within 2^-42 of it
+ *          (scales past 2^100: 2^-30).
  *          Requires cols % 128 == 0 and 16-byte aligned rows and vectors.
  *  Without q any alignment to the element size and any cols up to 16384 is
  *  taken (longer rows: FP8_ERR_UNSUPPORTED).  eps >= 0 (otherwise

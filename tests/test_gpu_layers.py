@@ -753,3 +753,34 @@ def test_adapter_sums_past_the_largest_bf16_value(gpu_lib, T):
                                A.bfloat16(), B, torch.zeros(T, dtype=torch.int32, device="cuda"), out_dtype=torch.float32)
     # z to 2^-16, zero codes add nothing
     assert (y - 255.5).abs().max() <= 255.5 * 2.0 ** -16
+
+
+# ------------------------------------------------------------- the quotient of codes
+
+@pytest.mark.parametrize("span", [(-30, 20), (60, 100)])
+def test_codes_of_values_next_to_a_rounding_boundary(gpu_lib, span):
+    """Rows of equal values have y = 0 + bias, so the bias chooses what is
+    quantized: FP32 values within three places of scale x boundary.  The codes
+    are those of the FP32 quotient y / s (within 2^-42 of it: it may be rounded
+    the other way where it lies that near the middle of two FP32 values)."""
+    g = np.random.default_rng(190)
+    cols = 16384
+    mids = np.concatenate([(np.arange(8, 16) + 0.5) * 2.0 ** (e - 3) for e in range(-6, 9)] + [(np.arange(8) + 0.5) * 2.0 ** -9])
+    mids = mids[mids < 447]
+    x = torch.zeros(1, cols, device="cuda")
+    differ = 0
+    for _ in range(8):
+        amax = np.ldexp(1 + g.random((cols // 128, 1)), g.integers(*span, (cols // 128, 1))).astype(np.float32)
+        s = np.maximum((amax / np.float32(448)).astype(np.float32), np.float32(1e-12))
+        y = (g.choice(mids, (cols // 128, 128)) * s).astype(np.float32)
+        y = (y.view(np.int32) + g.integers(-3, 4, y.shape)).astype(np.int32).view(np.float32)
+        y *= g.choice(np.float32([-1, 1]), y.shape)
+        y[:, :1] = amax
+        y[:, 1] = -0.0
+        q, s_gpu = gpu_lib.layer_norm_quant(x, None, dev(y.reshape(-1)))
+        assert np.array_equal(s_gpu[:, 0].cpu().numpy(), s[:, 0])
+        q = q.cpu().numpy().reshape(y.shape)
+        quot = (y + np.float32(0)).astype(np.float64) / s.astype(np.float64)     # 0 + the bias: +0 for -0
+        either = [e4m3.encode((quot * (1 + d)).astype(np.float32).astype(np.float64)) for d in (-2.0 ** -42, 2.0 ** -42)]
+        differ += ((q != either[0]) & (q != either[1])).sum()
+    assert differ == 0
