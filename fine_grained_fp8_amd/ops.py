@@ -494,13 +494,25 @@ def _same_device(dev, **tensors):
             raise ValueError(f"{name}: on {t.device}, the input is on {dev}")
 
 
+def _row_statistics(rows, cols, device, stream):
+    """Memory for a norm's mean and rstd.  Rows without columns have neither:
+    NaN here, as the library writes nothing then."""
+    mean = _empty(rows, torch.float32, device, stream)
+    rstd = _empty_as(mean, stream)
+    if cols == 0:
+        with torch.cuda.stream(stream):
+            mean.fill_(float("nan"))
+            rstd.fill_(float("nan"))
+    return mean, rstd
+
+
 def layer_norm(x: torch.Tensor, weight=None, bias=None, *, eps: float = 1e-5, return_stats: bool = False,
                out=None, stream=None):
     """Layer norm over the rows of x [rows][cols] (bfloat16 or float32).
 
     weight, bias: optional [cols] vectors of one type (bfloat16 or float32).
     Returns y in x's type, or (y, mean, rstd) with the float32 row statistics
-    that layer_norm_backward takes.
+    that layer_norm_backward takes (NaN for rows without columns).
     """
     lib = _lib.load_library()
     _check_2d("x", x, _FLOATS)
@@ -513,10 +525,7 @@ def layer_norm(x: torch.Tensor, weight=None, bias=None, *, eps: float = 1e-5, re
         _check_2d("out", out, (x.dtype,))
         if out.shape != x.shape:
             raise ValueError(f"out: expected {tuple(x.shape)}, got {tuple(out.shape)}")
-    mean = rstd = None
-    if return_stats:
-        mean = _empty(rows, torch.float32, x.device, stream)
-        rstd = _empty_as(mean, stream)
+    mean, rstd = _row_statistics(rows, cols, x.device, stream) if return_stats else (None, None)
     st = lib.fp8_layer_norm(_ptr(x), rows, cols, x.stride(0), _is_fp32(x), _ptr(weight), _ptr(bias), wt, eps,
                             _ptr(out), out.stride(0), _ptr(mean), _ptr(rstd), None, 0, None, 0, _stream(stream))
     _lib.check("fp8_layer_norm", st)
@@ -538,10 +547,7 @@ def layer_norm_quant(x: torch.Tensor, weight=None, bias=None, *, eps: float = 1e
     q = _empty((rows, cols), torch.uint8, x.device, stream)
     s = _empty((cols // 128, round_up(rows, 4)), torch.float32, x.device, stream)
     y = _empty((rows, cols), x.dtype, x.device, stream) if return_y else None
-    mean = rstd = None
-    if return_stats:
-        mean = _empty(rows, torch.float32, x.device, stream)
-        rstd = _empty_as(mean, stream)
+    mean, rstd = _row_statistics(rows, cols, x.device, stream) if return_stats else (None, None)
     st = lib.fp8_layer_norm(_ptr(x), rows, cols, x.stride(0), _is_fp32(x), _ptr(weight), _ptr(bias), wt, eps,
                             _ptr(y), cols, _ptr(mean), _ptr(rstd), _ptr(q), cols, _ptr(s), s.stride(0),
                             _stream(stream))

@@ -462,7 +462,8 @@ fp8_status fp8_dequant_tokens(const uint8_t* msg, int64_t T, int64_t H, int64_t 
  *  Without q any alignment to the element size and any cols up to 16384 is
  *  taken (longer rows: FP8_ERR_UNSUPPORTED).  eps >= 0 (otherwise
  *  FP8_ERR_SHAPE).  No output may overlap an input or another output.
- *  Sums are FP32 in a fixed order.  rows == 0 or cols == 0 is a no-op.
+ *  Sums are FP32 in a fixed order.  rows == 0 or cols == 0 is a no-op (mean and
+ *  rstd are not written).
  */
 fp8_status fp8_layer_norm(const void* x, int64_t rows, int64_t cols, int64_t ldx, fp8_out_dtype x_dtype,
                           const void* weight, const void* bias, fp8_out_dtype w_dtype, float eps, void* y,

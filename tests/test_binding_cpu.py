@@ -40,7 +40,7 @@ class Recorder:
 
     @contextlib.contextmanager
     def use(self, stream):
-        before, self.current = self.current, stream
+        before, self.current = self.current, stream or self.current
         yield
         self.current = before
 
@@ -144,3 +144,20 @@ BASE_CALLS = {
 def test_outputs_of_the_other_calls_on_another_stream(rec, name, monkeypatch):
     monkeypatch.setattr(torch.Tensor, "is_cuda", True, raising=False)
     check_memory_of_a_call(rec, BASE_CALLS[name], 0)
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_statistics_of_rows_without_columns(rec, side, monkeypatch):
+    """Without columns the library writes nothing: sum / 0 is NaN, and so are
+    both statistics (on the call's stream)."""
+    filled = []
+    fill = torch.Tensor.fill_
+    monkeypatch.setattr(torch.Tensor, "fill_", lambda t, v: (filled.append(rec.current.cuda_stream), fill(t, v))[1])
+    real = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: fill(real(*a, **k), 7))
+    stream = rec.side if side else None
+    for out in (ops.layer_norm(bf16(4, 0), return_stats=True, stream=stream),
+                ops.layer_norm_quant(bf16(4, 0), return_stats=True, stream=stream)):
+        mean, rstd = out[-2:]
+        assert mean.shape == rstd.shape == (4,) and mean.isnan().all() and rstd.isnan().all()
+    assert filled == [2 if side else 1] * 4

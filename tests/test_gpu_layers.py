@@ -137,6 +137,15 @@ def test_layer_norm_empty(gpu_lib):
     assert dx.shape == (0, 72) and (dw == 0).all() and (db == 0).all()
 
 
+def test_layer_norm_of_rows_without_columns(gpu_lib):
+    x = torch.empty(5, 0, device="cuda")
+    for out in (gpu_lib.layer_norm(x, return_stats=True), gpu_lib.layer_norm_quant(x, return_stats=True)):
+        assert out[0].shape == (5, 0)
+        assert all(t.shape == (5,) and t.isnan().all() for t in out[-2:])     # 0 / 0
+    dx, dw, db = gpu_lib.layer_norm_backward(x, x, *out[-2:])
+    assert dx.shape == (5, 0) and dw.shape == db.shape == (0,)
+
+
 def codes_match(q, s, Y, dY):
     """Codes and scales of an FP32 result against FP64 values Y, known to
     within dY: exact but where a quotient is within its error of a boundary."""
