@@ -465,6 +465,12 @@ def quant_act_tiles(x: torch.Tensor, tile: int = 128, rank: int = 1, *, sat_coun
 _FLOATS = (torch.bfloat16, torch.float32)
 
 
+def _float_type(dtype):
+    if dtype not in _FLOATS:
+        raise TypeError(f"out_dtype: {dtype} not in {_FLOATS}")
+    return dtype
+
+
 def _is_fp32(t: torch.Tensor) -> int:
     return _lib.OUT_FP32 if t.dtype == torch.float32 else _lib.OUT_BF16
 
@@ -626,7 +632,7 @@ def moe_few_tokens(x: torch.Tensor, router: torch.Tensor, w13: torch.Tensor, s13
     _check_vec("bias", bias, E, (torch.float32,))
     _same_device(x.device, router=router, w13=w13, s13=s13, w2=w2, s2=s2, bias=bias, out=out)
     if out is None:
-        out = _empty((T, H), out_dtype, x.device, stream)
+        out = _empty((T, H), _float_type(out_dtype), x.device, stream)
     else:
         _check_2d("out", out, _FLOATS)
         if out.shape != x.shape:
@@ -674,7 +680,7 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, sw: torch.Tensor, lora_a: t
     _check_vec("scales", scales, n, (torch.float32,))
     _same_device(x.device, w=w, sw=sw, lora_a=lora_a, lora_b=lora_b, ids=ids, scales=scales, out=out)
     if out is None:
-        out = _empty((T, N), out_dtype, x.device, stream)
+        out = _empty((T, N), _float_type(out_dtype), x.device, stream)
     else:
         _check_2d("out", out, _FLOATS)
         if tuple(out.shape) != (T, N):

@@ -161,3 +161,15 @@ def test_statistics_of_rows_without_columns(rec, side, monkeypatch):
         mean, rstd = out[-2:]
         assert mean.shape == rstd.shape == (4,) and mean.isnan().all() and rstd.isnan().all()
     assert filled == [2 if side else 1] * 4
+
+
+@pytest.mark.parametrize("name", ["moe_few_tokens", "adapter_linear"])
+def test_output_types_that_the_library_does_not_write(rec, name):
+    """Refused: the library writes bfloat16 or float32, and another type's
+    tensor would hold its bits."""
+    for dtype in (torch.float16, torch.float64, torch.int16):
+        with pytest.raises(TypeError):
+            LAYER_CALLS[name](out_dtype=dtype)
+    assert not rec.calls
+    for dtype in (torch.bfloat16, torch.float32):
+        assert LAYER_CALLS[name](out_dtype=dtype) is not None
