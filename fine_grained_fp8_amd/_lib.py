@@ -71,6 +71,9 @@ SIGNATURES = {
     "fp8_abi_version": (ctypes.c_int, []),
 }
 
+# the entry points of api_layers.cpp; the others are api.cpp's
+LAYER_ENTRIES = {n for n in SIGNATURES if n.startswith(("fp8_layer_norm", "fp8_moe_", "fp8_adapter_"))}
+
 _lib = None
 _lock = threading.Lock()
 
@@ -93,8 +96,9 @@ class FP8Error(RuntimeError):
 def load_library(path: str | None = None):
     """Load libfp8bs.so (once).  Raises OSError/RuntimeError if it is absent.
 
-    A library named by `path` may hold a part of the entry points (a host-only
-    build of one file of the ABI); the built library has to have them all."""
+    A library named by `path` may be a host-only build of one source file of the
+    ABI: it has to have all of that file's entry points (the layer operators'
+    or all others).  The built library has to have them all."""
     global _lib
     if _lib is not None:
         return _lib
@@ -107,8 +111,11 @@ def load_library(path: str | None = None):
                 f"{p} is not built; run `python -m fine_grained_fp8_amd.build` "
                 "(there is no CPU fallback)")
         lib = ctypes.CDLL(p)
+        missing = {n for n in SIGNATURES if not hasattr(lib, n)}
+        if missing and (path is None or missing not in (LAYER_ENTRIES, set(SIGNATURES) - LAYER_ENTRIES)):
+            raise RuntimeError(f"{p} lacks {', '.join(sorted(missing))}: build it again")
         for name, (res, args) in SIGNATURES.items():
-            if path is not None and not hasattr(lib, name):
+            if name in missing:
                 continue
             fn = getattr(lib, name)
             fn.restype = res

@@ -173,3 +173,33 @@ def test_output_types_that_the_library_does_not_write(rec, name):
     assert not rec.calls
     for dtype in (torch.bfloat16, torch.float32):
         assert LAYER_CALLS[name](out_dtype=dtype) is not None
+
+
+def test_a_library_named_by_path_has_whole_parts_of_the_abi(tmp_path, monkeypatch):
+    """A build that lacks single entry points (a stale one) is refused when it is
+    loaded, not at the first call; one that holds the entry points of one source
+    file, as the host-only builds of the validation code do, is taken."""
+    import shutil
+    import subprocess
+    from fine_grained_fp8_amd import _lib
+    gcc = shutil.which("gcc")
+    if not gcc:
+        pytest.skip("no C compiler")
+
+    def load(names):
+        src, so = tmp_path / "stub.c", tmp_path / f"lib{len(list(tmp_path.iterdir()))}.so"     # a name of its own
+        src.write_text("\n".join(f"int {n}(void) {{ return 0; }}" for n in names))
+        subprocess.run([gcc, "-shared", "-fPIC", "-o", str(so), str(src)], check=True)
+        monkeypatch.setattr(_lib, "_lib", None)
+        return _lib.load_library(str(so))
+
+    layers = [n for n in _lib.SIGNATURES if n in _lib.LAYER_ENTRIES]
+    base = [n for n in _lib.SIGNATURES if n not in _lib.LAYER_ENTRIES]
+    assert set(_lib.LAYER_ENTRIES) <= set(_lib.SIGNATURES) and len(layers) == 7
+    for names in (base + layers, base, layers):
+        lib = load(names)
+        assert all(hasattr(lib, n) for n in names)
+    for names in (base[1:] + layers, base + layers[:-1], base[:-1], layers[1:], []):
+        with pytest.raises(RuntimeError, match="lacks"):
+            load(names)
+        assert _lib._lib is None
