@@ -12,6 +12,7 @@ namespace {
 
 constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxLd = int64_t{1} << 28;
+constexpr int64_t kMaxBlocks = int64_t{1} << 23;   // a launch holds less than 2^32 threads, here 512 a workgroup
 
 // consecutive 256-byte aligned parts of a caller's workspace
 struct Carver {
@@ -71,6 +72,8 @@ fp8_status moe_shape(int64_t T, int64_t H, int64_t I, int64_t E, int64_t first, 
   if (T > fp8bs::kMoeMaxTokens || k > fp8bs::kMoeMaxTopK || E > fp8bs::kMoeMaxExperts || H > (1 << 20) ||
       I > (1 << 20))
     return FP8_ERR_UNSUPPORTED;
+  // the up product's launch: 512 threads for 16 channels of an expert, and for the routing
+  if (local * (I / 16) + 1 >= kMaxBlocks) return FP8_ERR_UNSUPPORTED;
   return FP8_OK;
 }
 
@@ -81,6 +84,9 @@ fp8_status adapter_shape(int64_t T, int64_t N, int64_t K, int64_t r, int64_t n) 
     return FP8_ERR_UNSUPPORTED;
   // the GEMM's limits: 32-bit scale-table offsets and tile numbers
   if ((K / 128) * ((T + 3) / 4 * 4) * 4 >= (int64_t{1} << 31)) return FP8_ERR_UNSUPPORTED;
+  if (((T + 127) / 128) * ((N + 255) / 256) >= (int64_t{1} << 31)) return FP8_ERR_UNSUPPORTED;
+  // the prompts' shrink: 512 threads for 16 tokens and a share of K
+  if ((T + 15) / 16 * fp8bs::adapter_splits(T, K) >= kMaxBlocks) return FP8_ERR_UNSUPPORTED;
   return FP8_OK;
 }
 

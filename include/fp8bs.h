@@ -512,7 +512,9 @@ int64_t fp8_layer_norm_backward_workspace(int64_t rows, int64_t cols);
  *  ids, gates  optional int32 / FP32 [T][top_k]: the chosen experts (best first) and g_j
  *  H % 128 == 0, I % 128 == 0, 1 <= top_k <= min(16, E), E <= 1024; rows of x,
  *  router and y 16-byte aligned.  T > 64: FP8_ERR_UNSUPPORTED (use the
- *  quantizer and fp8_block_gemm_grouped).  T == 0 is a no-op.
+ *  quantizer and fp8_block_gemm_grouped); so is local * I >= 2^27.  T == 0 is a
+ *  no-op.  The choice is over all E experts: one limited to some groups of them
+ *  is not offered.
  */
 typedef enum { FP8_MOE_SOFTMAX = 0, FP8_MOE_SIGMOID = 1 } fp8_moe_gate;
 fp8_status fp8_moe_few_tokens(int64_t T, int64_t H, int64_t I, int32_t E, int32_t first, int32_t local,
