@@ -793,3 +793,64 @@ def test_codes_of_values_next_to_a_rounding_boundary(gpu_lib, span):
         either = [e4m3.encode((quot * (1 + d)).astype(np.float32).astype(np.float64)) for d in (-2.0 ** -42, 2.0 ** -42)]
         differ += ((q != either[0]) & (q != either[1])).sum()
     assert differ == 0
+
+
+# ------------------------------------------------------------- more of the range
+
+@pytest.mark.parametrize("T,N,K,n,r", [(130, 384, 640, 4, 128), (257, 256, 256, 5, 72), (70, 128, 384, 70, 96),
+                                       (2100, 3968, 1024, 6, 104)])
+def test_adapters_of_high_rank_on_prompts(gpu_lib, T, N, K, n, r):
+    """Three and four products a turn in the GEMM's epilogue, the last case on a
+    tail that is cut along K."""
+    wq, ws, A, B, sc = make_adapters(N, K, n, r, 200)
+    xb = syn.activation_with_outliers(T, K, seed=201)
+    ids = np.random.default_rng(202).integers(-1, n, T).astype(np.int32)
+    if T > 2000:
+        ids = np.repeat(ids[:60], 35)
+    f64 = lambda bits: quant.bf16_to_f32(bits).astype(np.float64)
+    want = layers.adapters(xb, wq, ws, f64(A), f64(B), ids, sc)
+    for out_dtype in (torch.bfloat16, torch.float32):
+        y = gpu_lib.adapter_linear(bf16_dev(xb), dev(tile_codes(wq)), dev(ws), bf16_dev(A), bf16_dev(B), dev(ids),
+                                   scales=dev(sc), out_dtype=out_dtype)
+        check_adapters(y, *want, out_dtype)
+
+
+@pytest.mark.parametrize("T,E,local,k,H,I", [(64, 8, 8, 2, 256, 128), (64, 8, 8, 2, 4096, 256), (64, 4, 3, 1, 640, 256),
+                                             (64, 5, 5, 1, 128, 384)])
+def test_moe_experts_with_more_tokens_than_a_pass_takes(gpu_lib, T, E, local, k, H, I):
+    """9 to 24 tokens an expert on average (passes of 32), and experts with more."""
+    assert 9 <= T * k // E <= 24
+    x0 = quant.bf16_to_f32(syn.gaussian((T, H), seed=210))
+    common = quant.bf16_to_f32(syn.gaussian((1, H), seed=211))
+    xb = syn.f32_to_bf16_bits(0.3 * x0 + common)
+    rb = syn.gaussian((E, H), seed=212, std=H ** -0.5)
+    R, X = quant.bf16_to_f32(rb).astype(np.float64), quant.bf16_to_f32(xb).astype(np.float64)
+    order = np.argsort(-(X @ R.T).mean(axis=0))
+    rb, R = rb[order], R[order]                       # the liked experts first: held ones
+    w13, w2, d = make_experts(local, H, I, 213)
+    y, ids, _ = gpu_lib.moe_few_tokens(bf16_dev(xb), bf16_dev(rb), **d, top_k=k, return_routing=True)
+    ids = ids.cpu().numpy()
+    assert np.bincount(ids.ravel(), minlength=E)[:local].max() > 32
+    Y, _, _, mag, slack = layers.moe(xb, R, w13, w2, k, 0, ids=ids)
+    check_moe(y, Y, mag * 1.01, slack)
+    assert torch.equal(y, gpu_lib.moe_few_tokens(bf16_dev(xb), bf16_dev(rb), **d, top_k=k))
+
+
+@pytest.mark.parametrize("T,H,I,E,first,local,k,gate", [(1, 256, 128, 256, 32, 16, 8, "sigmoid"), (5, 128, 128, 1024, 1000, 24, 16, "softmax"),
+                                                        (8, 384, 256, 65, 0, 65, 4, "softmax")])
+def test_moe_many_experts_for_a_token_or_a_few(gpu_lib, T, H, I, E, first, local, k, gate):
+    """Routers past 64 experts take the launch of their own also for few tokens."""
+    xb = syn.gaussian((T, H), seed=220)
+    rb = syn.gaussian((E, H), seed=221, std=H ** -0.5)
+    bias = np.random.default_rng(222).standard_normal(E).astype(np.float32) * 0.05 if gate == "sigmoid" else None
+    w13, w2, d = make_experts(local, H, I, 223)
+    R, X = quant.bf16_to_f32(rb).astype(np.float64), quant.bf16_to_f32(xb).astype(np.float64)
+    y, ids, _ = gpu_lib.moe_few_tokens(bf16_dev(xb), bf16_dev(rb), **d, top_k=k, gate=gate, first_expert=first,
+                                       bias=None if bias is None else dev(bias), return_routing=True)
+    ids = ids.cpu().numpy()
+    want, _ = layers.route(X @ R.T, k, gate=gate, bias=bias)
+    value = X @ R.T if bias is None else 1 / (1 + np.exp(-(X @ R.T))) + bias
+    dl = 2.0 ** -18 * (np.abs(X) @ np.abs(R).T).max()
+    assert (np.abs(np.take_along_axis(value, ids, 1) - np.take_along_axis(value, want, 1)) <= 2 * dl + 4 * U).all()
+    Y, _, _, mag, slack = layers.moe(xb, R, w13, w2, k, first, ids=ids, gate=gate, bias=bias)
+    check_moe(y, Y, mag * 1.01, slack)
