@@ -1060,11 +1060,15 @@ void project(const AdapterProblem& p, hipStream_t stream) {
 // a workgroup reads all token operands, which count like weights against its
 // CU's load rate; wider outputs take several smaller workgroups a CU.
 // Measured at K x N with rank 32, every token its own adapter, us:
-//   7168 x 18432 (1152 tiles), 48 tokens: 1 tile 82, 2 68, 3 68, 4 78, 5 55;
-//     2 and 3 tiles with 4 waves 65 and 60; 64 tokens: 5 tiles 65, 2 x 4 waves 83;
+//   7168 x 18432 (1152 tiles), 48 tokens: 1 tile 84, 2 70, 3 69, 4 79, 5 57;
+//     2, 3 and 4 tiles with 4 waves 67, 62 and 68; 64 tokens: 5 tiles 66, 3 x 4 waves 76;
+//   7168 x 16384 (1024 tiles), 48 tokens: 72, 55, 68, 51, 54; 4 x 4 waves 52;
+//   7168 x 12288 (768 tiles), 48 tokens: 60, 53, 45, 47, 51; 3 x 4 waves 45;
+//   7168 x 8320 (520 tiles), 48 tokens: 54, 50, 40, 44, 48; 3 x 4 waves 43;
 //   18432 x 7168 (448 tiles), 48 tokens: 81, 63, 68, 75, 81;
 //   4096 x 4096 (256 tiles), 64 tokens: 31, 32, 35, 38, 43;
 //   1536 x 24576 (1536 tiles), 64 tokens: 80, 67, 54, 58, 67; 3 x 4 waves 46.
+// With one token the same order, within a tenth (1024 tiles: 34, 31, 35, 31, 31).
 template <int NT>
 void project_few(const AdapterProblem& p, hipStream_t stream) {
   switch ((p.N / 16 + 255) / 256) {
@@ -1094,7 +1098,12 @@ hipError_t launch_moe_few_tokens(const MoeProblem& p, hipStream_t stream) {
   hipLaunchKernelGGL(moe_prepare_kernel, dim3(router_blocks + quant_blocks(p.T, p.H)), dim3(kB), 0, stream, p,
                      router_blocks);
   const int up = p.local * (p.I / 16);
-  const int per = p.T * p.top_k / p.E;   // tokens that an expert gets on average
+  // Tokens that an expert gets on average: how many groups of 16 a workgroup
+  // takes in a pass over an expert's weights.  Measured with 1 / 2 / 4 groups, us a
+  // call, all experts held, 64 tokens: on average 8 of them at 2048 x 1408 46 / 50 / 61,
+  // 24 67 / 64 / 78; at 7168 x 2048 8 87 / 87 / 100, 10 91 / 93 / 105, 16 112 / 106 / 119,
+  // 25 101 / 88 / 95, 32 88 / 79 / 81, 64 76 / 68 / 65; 32 tokens, 16 64 / 60 / 67.
+  const int per = p.T * p.top_k / p.E;
   if (p.T <= kW && p.E <= 64) {
     hipLaunchKernelGGL((moe_up_kernel<1, false>), dim3(1 + up), dim3(kB), 0, stream, p, 1);
   } else {
@@ -1103,10 +1112,10 @@ hipError_t launch_moe_few_tokens(const MoeProblem& p, hipStream_t stream) {
     else if (p.E <= 256) hipLaunchKernelGGL(moe_route_kernel<4>, route, dim3(256), 0, stream, p);
     else hipLaunchKernelGGL(moe_route_kernel<kMoeMaxExperts / 64>, route, dim3(256), 0, stream, p);
     if (per <= 8) hipLaunchKernelGGL((moe_up_kernel<1, true>), dim3(up), dim3(kB), 0, stream, p, 0);
-    else if (per <= 24) hipLaunchKernelGGL((moe_up_kernel<2, true>), dim3(up), dim3(kB), 0, stream, p, 0);
+    else if (per <= 32) hipLaunchKernelGGL((moe_up_kernel<2, true>), dim3(up), dim3(kB), 0, stream, p, 0);
     else hipLaunchKernelGGL((moe_up_kernel<4, true>), dim3(up), dim3(kB), 0, stream, p, 0);
   }
-  const int span = per <= 8 ? 16 : per <= 24 ? 32 : 64;
+  const int span = per <= 8 ? 16 : per <= 32 ? 32 : 64;
   hipLaunchKernelGGL(moe_quant_kernel, dim3(1 + quant_blocks((int64_t)p.T * p.top_k, p.I)), dim3(kB), 0, stream, p,
                      span);
   if (span == 16) down<1>(p, stream);
