@@ -376,7 +376,7 @@ __device__ __forceinline__ void up_sums(const MoeProblem& p, int el, int tile, c
 //    a launch (about 4 us); with more tokens every workgroup would repeat too
 //    many sums over the shares.
 //    64 tokens on 64 experts of 2048 x 1408: 63 us for 369 MB (5.8 TB/s); 8 of 64
-//    experts of 7168 x 2048, 32 tokens: 40 us for 229 MB (5.7 TB/s); one token on
+//    experts of 7168 x 2048, 32 tokens: 41 us for 208 MB (5.0 TB/s); one token on
 //    two experts: 13 - 16 us for 59 MB.  Without the block loaded ahead 97 us in
 //    the first case, with three blocks a wave in flight (spilled) 400.
 template <int NT, bool kRouted>
@@ -564,8 +564,9 @@ struct DownLoads {
 //    `cuts` workgroups share a tile's units: one compute unit loads about 25
 //    GB/s here, so that 128 of them would take twice as long as 256.  Each
 //    leaves its FP32 sums in the workspace for one more small launch, about 4
-//    us; a count of arrivals in this one cost 40 us, because every workgroup
-//    has to write back its XCD's L2 before it counts.
+//    us; a count of arrivals in this one cost 40 us: its release makes every
+//    workgroup write back its XCD's L2 (sums written through to memory ahead of a
+//    relaxed count have not been tried).
 //    64 tokens on 64 experts of 2048 x 1408: 39 us for 185 MB, uncut 61; 8 experts
 //    of 7168 x 2048, 32 tokens: 24 us for 117 MB (4.9 TB/s).
 template <int NT, int DW>

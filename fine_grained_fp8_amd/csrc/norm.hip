@@ -515,7 +515,10 @@ void grad_any(const LayerNormGradProblem& p, hipStream_t stream) {
   else if (p.cols <= 8192) grad_cfg<T, kVec, 1024, 1024, 1>(p, stream);
   else grad_cfg<T, kVec, 1024, 1024, 2>(p, stream);
 }
-// rows a workgroup of the backward pass has in hand at a time
+// Rows a workgroup of the backward pass has in hand at a time.  Few short rows
+// fill the launch unevenly: 20011 x 128 are 313 groups of 64 for 256 workgroups,
+// two turns for 1.2 turns' work, and FP32 rows are not loaded ahead (10.4 us for
+// 31 MB, the shares' sum 3.9 more).
 int64_t grad_rows(int64_t cols) {
   return cols <= 128 ? 64 : cols <= 512 ? 16 : cols <= 1024 ? 8 : cols <= 2048 ? 4 : cols <= 4096 ? 2 : 1;
 }
