@@ -32,6 +32,13 @@ from .ops import (  # noqa: F401
     layer_norm_backward,
     moe_few_tokens,
     adapter_linear,
+    block_gemm_gated,
+    block_gemm_gated_quant,
+    gated_backward,
+    gated_backward_quant,
+    quant_act_cols,
+    head_norm_rotary,
+    head_norm_rotary_backward,
 )
 
 __all__ = [
@@ -39,4 +46,6 @@ __all__ = [
     "block_gemm_noalloc", "block_gemm_fused_quant", "block_gemm_grouped", "amax_history_update", "cast_e4m3", "message_bytes", "pack_tokens",
     "unpack_tokens", "dequant_tokens", "gemm_promotion", "quant_act_tiles", "probe_mfma", "probe_recip_online", "probe_gemm_split", "round_up",
     "layer_norm", "layer_norm_quant", "layer_norm_backward", "moe_few_tokens", "adapter_linear",
+    "block_gemm_gated", "block_gemm_gated_quant", "gated_backward", "gated_backward_quant", "quant_act_cols",
+    "head_norm_rotary", "head_norm_rotary_backward",
 ]

@@ -20,12 +20,30 @@ TILE_ROW, TILE_COL, TILE_COL_TILED = 0, 1, 2
 LAYOUT = {"fprop": 0, "dgrad": 1, "wgrad": 2, "dgrad_t": 3, "fprop_tiled": 4, "dgrad_t_tiled": 5, "wgrad_tiled": 6}
 OUT_BF16, OUT_FP32 = 0, 1
 MOE_GATE = {"softmax": 0, "sigmoid": 1}
+ACTIVATION = {"silu": 0, "gelu": 1}
+HEAD_NORM = {None: 0, "rms": 1, "layer": 2}
 
 # name -> (restype, argtypes); mirrors include/fp8bs.h
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _F = ctypes.c_float
+
+
+class Heads(ctypes.Structure):
+    """fp8_heads"""
+    _fields_ = [("x", _P), ("heads", _I64), ("ld_token", _I64), ("ld_head", _I64), ("weight", _P), ("y", _P),
+                ("ldy_token", _I64), ("ldy_head", _I64)]
+
+
+class HeadsGrad(ctypes.Structure):
+    """fp8_heads_grad"""
+    _fields_ = [("x", _P), ("heads", _I64), ("ld_token", _I64), ("ld_head", _I64), ("weight", _P), ("dy", _P),
+                ("lddy_token", _I64), ("lddy_head", _I64), ("dx", _P), ("lddx_token", _I64), ("lddx_head", _I64),
+                ("dweight", _P)]
+
+
+_HEAD_ARGS = [ctypes.c_int, ctypes.c_int, _F, _I64, _P, _I32, _I32, ctypes.POINTER(_I64), _P, _I32]
 SIGNATURES = {
     "fp8_quant_act_1x128": (ctypes.c_int, [_P, _I64, _I64, _I64, ctypes.c_int, _P, _I64, _P, _I64,
                                            _P, _P, _P, _P]),
@@ -67,12 +85,26 @@ SIGNATURES = {
     "fp8_adapter_linear": (ctypes.c_int, [_I64, _I64, _I64, _I32, _I32, _P, _I64, _P, _P, _I64, _P, _P, _P, _P,
                                           _P, ctypes.c_int, _I64, _P, _I64, _P]),
     "fp8_adapter_linear_workspace": (_I64, [_I64, _I64, _I64, _I32, _I32]),
+    "fp8_block_gemm_gated": (ctypes.c_int, [_I64, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _I64, ctypes.c_int, _P,
+                                            ctypes.c_int, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P]),
+    "fp8_block_gemm_gated_workspace": (_I64, [_I64, _I64, _I64]),
+    "fp8_gated_backward": (ctypes.c_int, [_I64, _I64, _P, _I64, _P, _I64, ctypes.c_int, _P, _I64, _P, _I64, _P, _I64,
+                                          _P, _I64, _P, _I64, _P, _P, _I64, _P]),
+    "fp8_quant_act_cols": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _I64, _P]),
+    "fp8_head_norm_rotary": (ctypes.c_int, [_I64, _I64, ctypes.c_int, ctypes.POINTER(Heads), ctypes.POINTER(Heads),
+                                            *_HEAD_ARGS, _P]),
+    "fp8_head_norm_rotary_backward": (ctypes.c_int, [_I64, _I64, ctypes.c_int, ctypes.POINTER(HeadsGrad),
+                                                     ctypes.POINTER(HeadsGrad), *_HEAD_ARGS, _P, _I64, _P]),
+    "fp8_head_norm_rotary_backward_workspace": (_I64, [_I64, _I64, _I64, _I64]),
     "fp8_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "fp8_abi_version": (ctypes.c_int, []),
 }
 
-# the entry points of api_layers.cpp; the others are api.cpp's
+# the entry points of api_layers.cpp and of api_blocks.cpp; the others are api.cpp's
 LAYER_ENTRIES = {n for n in SIGNATURES if n.startswith(("fp8_layer_norm", "fp8_moe_", "fp8_adapter_"))}
+BLOCK_ENTRIES = {n for n in SIGNATURES
+                 if n.startswith(("fp8_block_gemm_gated", "fp8_gated_", "fp8_quant_act_cols", "fp8_head_"))}
+_PARTS = (LAYER_ENTRIES, BLOCK_ENTRIES, set(SIGNATURES) - LAYER_ENTRIES - BLOCK_ENTRIES)
 
 _lib = None
 _lock = threading.Lock()
@@ -97,8 +129,8 @@ def load_library(path: str | None = None):
     """Load libfp8bs.so (once).  Raises OSError/RuntimeError if it is absent.
 
     A library named by `path` may be a host-only build of one source file of the
-    ABI: it has to have all of that file's entry points (the layer operators'
-    or all others).  The built library has to have them all."""
+    ABI: it has to have all of that file's entry points, and of another's all or
+    none.  The built library has to have them all."""
     global _lib
     if _lib is not None:
         return _lib
@@ -112,7 +144,8 @@ def load_library(path: str | None = None):
                 "(there is no CPU fallback)")
         lib = ctypes.CDLL(p)
         missing = {n for n in SIGNATURES if not hasattr(lib, n)}
-        if missing and (path is None or missing not in (LAYER_ENTRIES, set(SIGNATURES) - LAYER_ENTRIES)):
+        whole = all(part <= missing or not part & missing for part in _PARTS)
+        if missing and (path is None or not whole or len(missing) == len(SIGNATURES)):
             raise RuntimeError(f"{p} lacks {', '.join(sorted(missing))}: build it again")
         for name, (res, args) in SIGNATURES.items():
             if name in missing:

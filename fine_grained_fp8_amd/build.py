@@ -21,7 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libfp8bs.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["api.cpp", "quant.hip", "gemm.hip", "payload.hip", "accum.hip", "tiles.hip", "probe.hip", "fused.hip",
-           "api_layers.cpp", "norm.hip", "few.hip"]
+           "api_layers.cpp", "norm.hip", "few.hip",
+           "api_blocks.cpp", "gated.hip", "heads.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

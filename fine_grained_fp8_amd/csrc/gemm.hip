@@ -47,6 +47,7 @@
 #include <type_traits>
 
 #include "device.hpp"
+#include "gate.hpp"
 #include "kernels.hpp"
 
 namespace fp8bs {
@@ -136,10 +137,12 @@ __device__ __forceinline__ v8i read_operand_t(const uint8_t* tile, int n_sub, in
 // group in the grouped case.  Tiles are numbered group by group (grouped) or
 // in the GroupM-swizzled order.  Returns false when b lies past the last
 // group.
+// kWidth: output columns of a tile.
+template <int kWidth = BN>
 __device__ __forceinline__ bool decode_tile_index(const GemmProblem& p, bool grouped, int64_t b,
                                                   int64_t& m0, int64_t& m_end, int64_t& n0,
                                                   const uint8_t*& Bp, const float*& sBp) {
-  const int64_t tiles_n = (p.N + BN - 1) / BN;
+  const int64_t tiles_n = (p.N + kWidth - 1) / kWidth;
   Bp = p.B;
   sBp = p.sB;
   if (grouped) {
@@ -171,7 +174,7 @@ __device__ __forceinline__ bool decode_tile_index(const GemmProblem& p, bool gro
     int64_t tm, tn;
     grouped_order(b, tiles_m, tiles_n, tm, tn);
     m0 = tm * BM;
-    n0 = tn * BN;
+    n0 = tn * kWidth;
     m_end = p.M;
   }
   return true;
@@ -597,9 +600,15 @@ constexpr int kDScaleStage = 2048;
 constexpr int kDOutStage = 16384;              // epilogue staging per wave: 128 x 64 BF16 or 64 x 64 FP32
 constexpr int kDWOps = 8;                      // weight loads per block
 
-template <int kLayout, bool kOutF32, bool kGrouped, bool kTiledB, bool kAdapters = false>
+// kGated: C = act(A W1^T) (A W3^T) elementwise, B the 2 N rows of W1 and then W3.
+// A tile is 128 output columns; a wave has 32 of them, its 64 weight rows being
+// their 32 rows of W1 (subtiles 0 and 1) and of W3 (2 and 3), so that a lane ends
+// with both factors of its outputs.
+template <int kLayout, bool kOutF32, bool kGrouped, bool kTiledB, bool kAdapters = false, bool kGated = false>
 __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProblem p, int64_t total_tiles) {
   static_assert(kLayout != kDgrad, "Dgrad reads the weights transposed through LDS");
+  static_assert(!kGated || (kLayout == kFprop && kTiledB && !kGrouped && !kAdapters && !kOutF32), "gated Fprop");
+  constexpr int kWidth = kGated ? BN / 2 : BN;   // output columns of a tile
   __shared__ __attribute__((aligned(1024))) uint8_t lds_a0[kDStage];
   __shared__ __attribute__((aligned(1024))) uint8_t lds_a1[kDStage];
   __shared__ __attribute__((aligned(1024))) uint8_t lds_a2[kDStage];
@@ -723,16 +732,19 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
   // registers; row-major: lane reads 16 B of its row; operand-tiled (ldb ==
   // K): the wave's 16-row groups are 2 KB tiles per K block, each half one
   // 1 KB run
-  const uint32_t off_w = kTiledB ? (uint32_t)(wave * 4 * KB * 2048 + lane * 16)
+  const uint32_t off_w = kTiledB ? (uint32_t)(wave * (kGated ? 2 : 4) * KB * 2048 + lane * 16)
                                  : (uint32_t)((wave * 64 + lrow) * (int)p.ldb + lgrp * 16);
   const uint32_t w_istride = kTiledB ? (uint32_t)(KB * 2048) : (uint32_t)(16 * p.ldb);
   const uint32_t w_hstride = kTiledB ? 1024u : 64u;
   const uint32_t w_kstride = kTiledB ? 2048u : (uint32_t)BK;
+  // gated: the rows of W3 lie N rows behind those of W1, their scales N / 128 rows
+  const uint32_t w_up = kGated ? (uint32_t)(p.N * p.K) - 2u * (uint32_t)(KB * 2048) : 0u;
+  const uint32_t sw_lane = kGated && lane >= 32 ? (uint32_t)((p.N / 128) * p.ld_sb) * 4u : 0u;
   // weight-side scales: Fprop / Dgrad_T - the wave's 128x128 weight block
   // (every lane fetches the same float; Fprop's table is [N/128][K/128],
   // Dgrad_T reads the forward table [K/128][N/128]); Wgrad - the workgroup's
   // 256 per-column scales
-  const int64_t sw_elems = kLayout == kFprop ? (p.N / 128) * p.ld_sb
+  const int64_t sw_elems = kLayout == kFprop ? (kGated ? 2 : 1) * (p.N / 128) * p.ld_sb
                                              : (kLayout == kDgradT ? (p.K / BK) * p.ld_sb : 0);
   const uint32_t sw_kstride = kLayout == kFprop ? 4u : (uint32_t)p.ld_sb * 4u;
   // decode work id `id` into the next-tile state and set up its buffer
@@ -763,7 +775,7 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
     }
     int64_t tm0, tm_end, tn0;
     if (group_lds ? !decode_tile_lds(p, gtab, lane, b, tm0, tm_end, tn0, Bp, sBp)
-                  : !decode_tile_index(p, kGrouped, b, tm0, tm_end, tn0, Bp, sBp))
+                  : !decode_tile_index<kWidth>(p, kGrouped, b, tm0, tm_end, tn0, Bp, sBp))
       return false;
     nx_m0 = uniform_i64(tm0);
     nx_m_end = uniform_i64(tm_end);
@@ -771,13 +783,15 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
     Bp = uniform_ptr(Bp);
     sBp = uniform_ptr(sBp);
     nx_rows_m = (int)(nx_m_end - nx_m0 < BM ? nx_m_end - nx_m0 : BM);
-    nx_rows_n = (int)(p.N - nx_n0 < BN ? p.N - nx_n0 : BN);
+    // gated: rows n0 .. of W1 up to the end of the tile's rows of W3 (the host
+    // keeps that below 2^31 bytes)
+    nx_rows_n = kGated ? (int)p.N + kWidth : (int)(p.N - nx_n0 < BN ? p.N - nx_n0 : BN);
     nx_rsrc_x = __builtin_amdgcn_make_buffer_rsrc((void*)(p.A + nx_m0 * p.lda), (short)0, nx_rows_m * (int)p.lda,
                                                   (int)kRsrcWord3);
     nx_rsrc_w = __builtin_amdgcn_make_buffer_rsrc((void*)(Bp + nx_n0 * p.ldb), (short)0, nx_rows_n * (int)p.ldb,
                                                   (int)kRsrcWord3);
     nx_rsrc_sw = __builtin_amdgcn_make_buffer_rsrc((void*)sBp, (short)0, (int)(sw_elems * 4), (int)kRsrcWord3);
-    const int64_t nbw = (nx_n0 + 64 * wave) / 128;
+    const int64_t nbw = kGated ? nx_n0 / 128 : (nx_n0 + 64 * wave) / 128;
     nx_sw_off = kLayout == kFprop ? (uint32_t)(nbw * p.ld_sb) * 4u : (uint32_t)nbw * 4u;
     nx_sa = p.sA + nx_m0;
     nx_sb = sBp + nx_n0;
@@ -857,14 +871,16 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(sc + kDWScaleOff), 16, (uint32_t)(lane * 16), 0, 0,
                                                  0);
       } else {
-        // the wave's weight-block scale (every lane fetches the same float)
+        // the wave's weight-block scale (every lane fetches the same float; gated:
+        // lanes 0-31 that of W1, 32-63 that of W3)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc_sw, (lds_ptr_t)(sc + kDWScaleOff + wave * 256), 4,
-                                                 sw_off + (uint32_t)kb * sw_kstride, 0, 0, 0);
+                                                 sw_off + (uint32_t)kb * sw_kstride + sw_lane, 0, 0, 0);
       }
     } else {
       const int i = (op - kDDmaOps) >> 1, h = (op - kDDmaOps) & 1;
       const v4i v = __builtin_amdgcn_raw_buffer_load_b128(
-          rsrc_w, off_w + (uint32_t)kb * w_kstride, (uint32_t)i * w_istride + (uint32_t)h * w_hstride, 0);
+          rsrc_w, off_w + (uint32_t)kb * w_kstride,
+          (uint32_t)i * w_istride + (uint32_t)h * w_hstride + (kGated && i >= 2 ? w_up : 0u), 0);
       wr[i][4 * h + 0] = v[0];
       wr[i][4 * h + 1] = v[1];
       wr[i][4 * h + 2] = v[2];
@@ -899,9 +915,9 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
   constexpr int kMid = 5;
   v8i bxa, bxb;                     // block kb+1: token-side operand rows 0, 1
   float tn[DNJ];                    // block kb+1: token-side scales
-  float wn = 1.f;                   // block kb+1: weight-side block scale
+  float wn = 1.f, wu = 1.f;         // block kb+1: weight-side block scale (gated: of W1 and of W3)
   v4f Pl[DNI];                      // last row of partial sums of block kb-1
-  float cl = 0.f;                   // and its scale
+  float cl = 0.f, clu = 0.f;        // and its scale (gated: two)
   auto zero_state = [&]() {
 #pragma unroll
     for (int i = 0; i < DNI; ++i) {
@@ -909,7 +925,7 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
       for (int j = 0; j < DNJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
       Pl[i] = v4f{0.f, 0.f, 0.f, 0.f};
     }
-    cl = 0.f;
+    cl = clu = 0.f;
   };
 
   auto read_tn = [&](const uint8_t* scn, int half) {
@@ -923,6 +939,7 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
     const uint8_t* stn = tile_of(stage);
     const uint8_t* scn = scl_of(stage);
     if constexpr (kBlockW) wn = reinterpret_cast<const float*>(scn + kDWScaleOff)[wave * 64];
+    if constexpr (kGated) wu = reinterpret_cast<const float*>(scn + kDWScaleOff)[wave * 64 + 32];
     read_tn(scn, 0);
     read_tn(scn, 1);
     bxa = pair(stn + x_lo, stn + x_hi);
@@ -951,7 +968,7 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
 
     // c[j] (this block's scale of token subtile j) is formed in row j and
     // first used in row j+1
-    float c[DNJ];
+    float c[DNJ], cu[DNJ];
     float4 rs[DNI];
     if constexpr (kLayout == kWgrad) {
       const float* swl = reinterpret_cast<const float*>(sc + kDWScaleOff);
@@ -997,11 +1014,12 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
         const v4f zero = {0.f, 0.f, 0.f, 0.f};
         Pc[i] = mfma_e4m3_16x16x128(wc[i], bj, zero);
         __builtin_amdgcn_sched_barrier(0);
-        if (j > 0) fold(acc[i][j - 1], Pp[i], c[j - 1], i);
-        else if constexpr (kBlockW) fold(acc[i][DNJ - 1], Pl[i], cl, i);
+        if (j > 0) fold(acc[i][j - 1], Pp[i], kGated && i >= 2 ? cu[j - 1] : c[j - 1], i);
+        else if constexpr (kBlockW) fold(acc[i][DNJ - 1], Pl[i], kGated && i >= 2 ? clu : cl, i);
         if (i == 1) {
           const float t = kBlockW ? tn[j] * wn : tn[j];
           c[j] = live ? t : 0.f;
+          if constexpr (kGated) cu[j] = live ? tn[j] * wu : 0.f;
         }
         if (j + 2 < DNJ) {
           if (i == 0) bxl[j + 2] = *reinterpret_cast<const v4i*>(st + x_lo + (j + 2) * 2048);
@@ -1032,6 +1050,7 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
           if (i == 1) read_tn(scn, 1);
           if constexpr (kBlockW) {
             if (i == 2) wn = reinterpret_cast<const float*>(scn + kDWScaleOff)[wave * 64];
+            if (kGated && i == 2) wu = reinterpret_cast<const float*>(scn + kDWScaleOff)[wave * 64 + 32];
           }
         }
         // instruction order = source order: one MFMA, then the fold of the
@@ -1053,6 +1072,7 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
 #pragma unroll
       for (int i = 0; i < DNI; ++i) Pl[i] = ((DNJ - 1) & 1) ? P1[i] : P0[i];
       cl = c[DNJ - 1];
+      if constexpr (kGated) clu = cu[DNJ - 1];
     } else {
 #pragma unroll
       for (int i = 0; i < DNI; ++i) fold(acc[i][DNJ - 1], ((DNJ - 1) & 1) ? P1[i] : P0[i], c[DNJ - 1], i);
@@ -1292,6 +1312,117 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
       }
     }
   };
+  // ---- gated epilogue: h = act(gate) up, and what is asked for of gate | up ----
+  // All four waves' 128 columns x 128 rows meet in the staging areas, so that the
+  // stores write whole row segments (256 bytes of BF16, 128 of codes) and a row's
+  // 1x128 tile, spread over the waves, has its maximum.  The barriers wait for
+  // LDS alone: the next item's loads stay in flight.
+  auto lds_barrier = [&]() {
+    __asm__ volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));   // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __asm__ volatile("" ::: "memory");
+  };
+  auto stage = [&](int q) -> uint8_t* { return q == 0 ? lds_z0 : q == 1 ? lds_z1 : q == 2 ? lds_z2 : lds_z3; };
+  auto store_tile_gated = [&](int64_t em0, int64_t em_end, int64_t en0) {
+    const GatedEpilogue& ge = p.gated;
+    // BF16: rows 0-63 in one area, 64-127 in the next; 16-byte chunks XOR-swizzled by row
+    auto put_bf16 = [&](int area, int i, int j, const v4f& r) {
+      typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+      const int m = j * 16 + lrow, ch = wave * 4 + (i & 1) * 2 + (lgrp >> 1);
+      *reinterpret_cast<v4bf*>(stage(area + (j >> 2)) + (m & 63) * 256 + ((ch ^ (m & 15)) << 4) + (lgrp & 1) * 8) =
+          __builtin_convertvector(r, v4bf);
+    };
+    auto store_bf16 = [&](int area, uint16_t* base, int64_t ld) {
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const int row = wave * 32 + t * 4 + (lane >> 4), ch = lane & 15;
+        const v4i v = *reinterpret_cast<const v4i*>(stage(area + (wave >> 1)) + (row & 63) * 256 + ((ch ^ (row & 15)) << 4));
+        if (em0 + row < em_end)
+          __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(base + (em0 + row) * ld + ch * 8));
+      }
+    };
+    if (ge.gate_up != nullptr) {
+#pragma unroll
+      for (int j = 0; j < DNJ; ++j)
+#pragma unroll
+        for (int i = 0; i < DNI; ++i) put_bf16(i < 2 ? 0 : 2, i, j, acc[i][j]);
+      lds_barrier();
+      store_bf16(0, ge.gate_up + en0, ge.ld_gu);
+      store_bf16(2, ge.gate_up + p.N + en0, ge.ld_gu);
+      lds_barrier();
+    }
+#pragma unroll
+    for (int j = 0; j < DNJ; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float a = acc[i][j][v];
+          acc[i][j][v] = a * logistic(ge.gelu ? gelu_argument(a) : a) * acc[i + 2][j][v];
+        }
+    if (ge.q != nullptr) {
+      uint32_t* most = reinterpret_cast<uint32_t*>(lds_z2);   // [wave][row]
+#pragma unroll
+      for (int j = 0; j < DNJ; ++j) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) m = max(m, __float_as_uint(acc[i][j][v]) & 0x7FFFFFFFu);
+        const auto h = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+        m = max(h[0], h[1]);
+        const auto f = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+        m = max(f[0], f[1]);
+        if (lgrp == 0) most[wave * BM + j * 16 + lrow] = m;
+      }
+      lds_barrier();
+#pragma unroll
+      for (int j = 0; j < DNJ; ++j) {
+        const int m = j * 16 + lrow;
+        const uint32_t t = max(max(most[m], most[BM + m]), max(most[2 * BM + m], most[3 * BM + m]));
+        const float y[8] = {acc[0][j][0], acc[0][j][1], acc[0][j][2], acc[0][j][3],
+                            acc[1][j][0], acc[1][j][1], acc[1][j][2], acc[1][j][3]};
+        float s;
+        const uint2 q = quant8_f32(y, t, s);
+        uint8_t* row = lds_z0 + m * 128 + lgrp * 4;
+        *reinterpret_cast<uint32_t*>(row + (((wave * 2) ^ (m & 7)) << 4)) = q.x;
+        *reinterpret_cast<uint32_t*>(row + (((wave * 2 + 1) ^ (m & 7)) << 4)) = q.y;
+        if ((j >> 1) == wave && lgrp == 0 && em0 + m < em_end) ge.s[(en0 >> 7) * ge.ld_s + em0 + m] = s;
+      }
+      lds_barrier();
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int row = wave * 32 + t * 8 + (lane >> 3), ch = lane & 7;
+        const v4i v = *reinterpret_cast<const v4i*>(lds_z0 + row * 128 + ((ch ^ (row & 7)) << 4));
+        if (em0 + row < em_end)
+          __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(ge.q + (em0 + row) * ge.ldq + en0 + ch * 16));
+      }
+    } else if (p.out_fp32) {
+#pragma unroll
+      for (int j = 0; j < DNJ; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int m = j * 16 + lrow, ch = wave * 8 + i * 4 + lgrp;
+          *reinterpret_cast<v4f*>(stage(j >> 1) + (m & 31) * 512 + ((ch ^ (m & 15)) << 4)) = acc[i][j];
+        }
+      lds_barrier();
+#pragma unroll
+      for (int t = 0; t < 16; ++t) {
+        const int row = wave * 32 + t * 2 + (lane >> 5), ch = lane & 31;
+        const v4i v = *reinterpret_cast<const v4i*>(stage(wave) + (row & 31) * 512 + ((ch ^ (row & 15)) << 4));
+        float* dst = reinterpret_cast<float*>(p.C) + (em0 + row) * p.ldc + en0 + ch * 4;
+        if (em0 + row < em_end) __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(dst));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < DNJ; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) put_bf16(0, i, j, acc[i][j]);
+      lds_barrier();
+      store_bf16(0, reinterpret_cast<uint16_t*>(p.C) + en0, p.ldc);
+    }
+  };
   zero_state();
   issue_prologue();
   // Each work item decodes the next one first.  Its last round (padded
@@ -1353,7 +1484,8 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
 #pragma unroll
     for (int i = 0; i < DNI; ++i)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) acc[i][DNJ - 1][v] = __builtin_fmaf(Pl[i][v], cl, acc[i][DNJ - 1][v]);
+      for (int v = 0; v < 4; ++v)
+        acc[i][DNJ - 1][v] = __builtin_fmaf(Pl[i][v], kGated && i >= 2 ? clu : cl, acc[i][DNJ - 1][v]);
   }
   const int64_t em0 = m0, em_end = m_end, en0 = n0;
   const int erows_m = rows_m, erows_n = rows_n;
@@ -1429,11 +1561,13 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
     if (tid == 0) p.ws_count[et] = 0u;
     // the split path ends here and never reaches the K loop again (the
     // compiler's wait analysis would otherwise carry its loads into the loop)
-    if constexpr (kAdapters) store_tile_adapters(em0, em_end, en0, id0, id1);
+    if constexpr (kGated) store_tile_gated(em0, em_end, en0);
+    else if constexpr (kAdapters) store_tile_adapters(em0, em_end, en0, id0, id1);
     else store_tile(em0, em_end, en0, erows_m, erows_n);
     return;
   }
-  if constexpr (kAdapters) store_tile_adapters(em0, em_end, en0, id0, id1);
+  if constexpr (kGated) store_tile_gated(em0, em_end, en0);
+  else if constexpr (kAdapters) store_tile_adapters(em0, em_end, en0, id0, id1);
   else store_tile(em0, em_end, en0, erows_m, erows_n);
   if (!more) {
     wait_vm<0>();   // the reloads streamed by the last round land before the workgroup ends
@@ -1458,6 +1592,11 @@ hipError_t launch_typed(const GemmProblem& p, hipStream_t stream, int64_t grid, 
   } else {
     grid = persistent_grid(grid);
     if constexpr (kLayout == kFprop && !kGrouped) {
+      if (p.gated.on) {
+        hipLaunchKernelGGL((block_gemm_direct_kernel<kFprop, false, false, true, false, true>), dim3((unsigned)grid),
+                           dim3(kThreads), 0, stream, p, total);
+        return hipGetLastError();
+      }
       if (p.adapters.ids != nullptr) {
         if (p.out_fp32)
           hipLaunchKernelGGL((block_gemm_direct_kernel<kFprop, true, false, true, true>), dim3((unsigned)grid),
@@ -1563,7 +1702,7 @@ hipError_t attach_static_workspace(GemmProblem& p, hipStream_t stream) {
 }
 
 hipError_t launch_gemm(const GemmProblem& p, hipStream_t stream) {
-  const int64_t tiles_n = (p.N + BN - 1) / BN;
+  const int64_t tiles_n = p.gated.on ? p.N / (BN / 2) : (p.N + BN - 1) / BN;
   if (p.groups > 0) {
     // upper bound on per-group M tiles without reading the device offsets
     const int64_t total = ((p.M + BM - 1) / BM + p.groups) * tiles_n;

@@ -66,6 +66,20 @@ struct AdapterEpilogue {
   int r, n;              // r % 8 == 0
 };
 
+// The gated feed-forward's epilogue of an Fprop product with tiled B (on != 0): B
+// has 2 N rows, W1's and then W3's, and C = act(A W1^T) (A W3^T).  With q the
+// result leaves as the codes and scales of its 1x128 row tiles instead of C.
+struct GatedEpilogue {
+  int on;
+  int gelu;              // act: GELU (tanh form); otherwise SiLU
+  uint16_t* gate_up;     // optional: BF16 [M][ld_gu], A W1^T and then A W3^T (2 N columns)
+  int64_t ld_gu;
+  uint8_t* q;            // optional: codes [M][ldq]
+  int64_t ldq;
+  float* s;              // with q: scales [N / 128][ld_s]
+  int64_t ld_s;
+};
+
 struct GemmProblem {
   int layout;            // GemmLayout
   int64_t M, N, K;
@@ -91,6 +105,7 @@ struct GemmProblem {
   uint32_t* ws_count;
   int64_t ws_slots;
   AdapterEpilogue adapters;   // FPROP with tiled B, not grouped
+  GatedEpilogue gated;        // the same
 };
 
 hipError_t launch_gemm(const GemmProblem& p, hipStream_t stream);

@@ -175,7 +175,7 @@ __device__ __forceinline__ int cols_tile_word(int row, int word) {
 
 template <bool kTiled>
 __global__ __launch_bounds__(256) void quant_cols_kernel(
-    const uint16_t* __restrict__ x, int64_t cols, int64_t ldx, int64_t ncb, int64_t nbr,
+    const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ldx, int64_t ncb, int64_t nbr,
     int64_t nblocks, uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ scales,
     int64_t ld_s, float* __restrict__ amax_out) {
   __shared__ uint32_t tile[8 * 544];
@@ -190,7 +190,9 @@ __global__ __launch_bounds__(256) void quant_cols_kernel(
       const int64_t col = lc0 + cc * 8;
       uint4 val = make_uint4(0, 0, 0, 0);
       const uint16_t* src = x + (lr0 + row) * ldx + col;
-      if (col + 8 <= cols) {
+      if (lr0 + row >= rows) {
+        // past the last row (ragged rows): zeros
+      } else if (col + 8 <= cols) {
         val = *reinterpret_cast<const uint4*>(src);
       } else if (col < cols) {               // ragged last chunk: stay inside the row
         uint32_t h[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -561,15 +563,15 @@ hipError_t launch_quant_cols(const uint16_t* x, int64_t rows, int64_t cols, int6
                              uint8_t* q, int64_t ldq, float* scales, int64_t ld_s,
                              float* amax_out, bool tiled, hipStream_t stream) {
   const int64_t ncb = (cols + 63) / 64;
-  const int64_t nblocks = (rows / 128) * ncb;
-  const int64_t nbr = rows / 128;
+  const int64_t nblocks = ((rows + 127) / 128) * ncb;
+  const int64_t nbr = (rows + 127) / 128;
   const int64_t grid = nblocks;                // one block per workgroup (as the dual kernel)
   if (tiled)
     hipLaunchKernelGGL(quant_cols_kernel<true>, dim3((unsigned)grid), dim3(256), 0, stream,
-                       x, cols, ldx, ncb, nbr, nblocks, q, ldq, scales, ld_s, amax_out);
+                       x, rows, cols, ldx, ncb, nbr, nblocks, q, ldq, scales, ld_s, amax_out);
   else
     hipLaunchKernelGGL(quant_cols_kernel<false>, dim3((unsigned)grid), dim3(256), 0, stream,
-                       x, cols, ldx, ncb, nbr, nblocks, q, ldq, scales, ld_s, amax_out);
+                       x, rows, cols, ldx, ncb, nbr, nblocks, q, ldq, scales, ld_s, amax_out);
   return hipGetLastError();
 }
 

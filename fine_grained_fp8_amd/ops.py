@@ -692,3 +692,291 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, sw: torch.Tensor, lora_a: t
                                 _ptr(ws), nbytes, _stream(stream))
     _lib.check("fp8_adapter_linear", st)
     return out
+
+
+def _on_current_device(name, t):
+    """Launches go to the current device: a tensor of another one is refused."""
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _activation(name):
+    if name not in _lib.ACTIVATION:
+        raise ValueError(f"activation: {name!r} not in {sorted(_lib.ACTIVATION)}")
+    return _lib.ACTIVATION[name]
+
+
+def _gated(A, sA, w13, s13, activation, quant, return_gate_up, out_dtype, out, stream):
+    lib = _lib.load_library()
+    act = _activation(activation)
+    _check_2d("A", A, (torch.uint8, torch.float8_e4m3fn))
+    _check_2d("sA", sA, (torch.float32,))
+    _check_2d("s13", s13, (torch.float32,))
+    _on_current_device("A", A)
+    M, K = A.shape
+    if w13.dim() != 2 or w13.shape[0] % 2 != 0:
+        raise ValueError(f"w13: expected [2 I][K], got {tuple(w13.shape)}")
+    I = w13.shape[0] // 2
+    _check_codes("w13", w13, (2 * I, K))
+    if sA.shape[0] < K // 128 or sA.shape[1] < M or s13.shape[0] < 2 * I // 128 or s13.shape[1] < K // 128:
+        raise ValueError(f"sA {tuple(sA.shape)}, s13 {tuple(s13.shape)}: expected at least {(K // 128, M)} and "
+                         f"{(2 * I // 128, K // 128)}")
+    _same_device(A.device, sA=sA, w13=w13, s13=s13, out=out)
+    q = s = gate_up = None
+    if quant:
+        q = _empty((M, I), torch.uint8, A.device, stream)
+        s = _empty((I // 128, round_up(M, 4)), torch.float32, A.device, stream)
+    elif out is None:
+        out = _empty((M, I), _float_type(out_dtype), A.device, stream)
+    else:
+        _check_2d("out", out, _FLOATS)
+        if tuple(out.shape) != (M, I):
+            raise ValueError(f"out: expected {(M, I)}, got {tuple(out.shape)}")
+    if return_gate_up:
+        gate_up = _empty((M, 2 * I), torch.bfloat16, A.device, stream)
+    nbytes = lib.fp8_block_gemm_gated_workspace(M, I, K)
+    ws = _workspace(nbytes, A.device, stream)
+    st = lib.fp8_block_gemm_gated(
+        M, I, K, _ptr(A), A.stride(0), _ptr(sA), sA.stride(0), _ptr(w13), _ptr(s13), s13.stride(0), act,
+        _ptr(out), _lib.OUT_BF16 if out is None else _is_fp32(out), 0 if out is None else out.stride(0),
+        _ptr(gate_up), 2 * I, _ptr(q), I, _ptr(s), 0 if s is None else s.stride(0), _ptr(ws), nbytes, _stream(stream))
+    _lib.check("fp8_block_gemm_gated", st)
+    return out, q, s, gate_up
+
+
+def block_gemm_gated(A: torch.Tensor, sA: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor, *,
+                     activation: str = "silu", return_gate_up: bool = False, out_dtype=torch.bfloat16, out=None,
+                     stream=None):
+    """The gated feed-forward product on FP8 codes: h = act(A W1^T) * (A W3^T).
+
+    A [M][K] codes, sA [K/128][>=M] (quant_act_1x128 or layer_norm_quant); w13
+    [2 I][K]: operand-tiled codes of quant_weight_128x128(..., tiled=True) of the
+    I rows of W1 and then the I rows of W3, s13 [2 I/128][>=K/128] their block
+    scales.  activation: "silu" or "gelu" (tanh form).  Returns h [M][I] in
+    out_dtype (bfloat16 or float32), or with return_gate_up (h, gate_up): the two
+    projections in bfloat16 [M][2 I], which gated_backward_quant takes.
+    """
+    h, _, _, gate_up = _gated(A, sA, w13, s13, activation, False, return_gate_up, out_dtype, out, stream)
+    return (h, gate_up) if return_gate_up else h
+
+
+def block_gemm_gated_quant(A: torch.Tensor, sA: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor, *,
+                           activation: str = "silu", return_gate_up: bool = False, stream=None):
+    """block_gemm_gated with the 1x128 quantization of h in its epilogue, from the
+    FP32 values: (q [M][I] uint8, s [I/128][round_up(M, 4)] float32), the operand of
+    the down product; return_gate_up appends gate_up."""
+    _, q, s, gate_up = _gated(A, sA, w13, s13, activation, True, return_gate_up, None, None, stream)
+    return (q, s, gate_up) if return_gate_up else (q, s)
+
+
+def _gated_backward(dh, gate_up, activation, stream, d=None, q=None, s=None, qt=None, st=None, ht=None, sht=None):
+    lib = _lib.load_library()
+    T, I = dh.shape
+    status = lib.fp8_gated_backward(
+        T, I, _ptr(dh), dh.stride(0), _ptr(gate_up), gate_up.stride(0), _activation(activation), _ptr(d), 2 * I,
+        _ptr(q), 2 * I, _ptr(s), 0 if s is None else s.stride(0), _ptr(qt), round_up(T, 128), _ptr(st), 2 * I,
+        _ptr(ht), _ptr(sht), 0 if sht is None else sht.stride(0), _stream(stream))
+    _lib.check("fp8_gated_backward", status)
+
+
+def _check_gated_backward(dh, gate_up):
+    _check_2d("dh", dh, (torch.bfloat16,))
+    _check_2d("gate_up", gate_up, (torch.bfloat16,))
+    if gate_up.shape != (dh.shape[0], 2 * dh.shape[1]):
+        raise ValueError(f"gate_up: expected {(dh.shape[0], 2 * dh.shape[1])}, got {tuple(gate_up.shape)}")
+    _on_current_device("dh", dh)
+    _same_device(dh.device, gate_up=gate_up)
+    return dh.shape
+
+
+def gated_backward(dh: torch.Tensor, gate_up: torch.Tensor, *, activation: str = "silu", stream=None):
+    """Gradient of h = act(a) * u for dh [T][I] bfloat16 and gate_up = [a | u]
+    [T][2 I] bfloat16 (I a multiple of 128): [da | du] [T][2 I] bfloat16."""
+    T, I = _check_gated_backward(dh, gate_up)
+    d = _empty((T, 2 * I), torch.bfloat16, dh.device, stream)
+    _gated_backward(dh, gate_up, activation, stream, d=d)
+    return d
+
+
+def gated_backward_quant(dh: torch.Tensor, gate_up: torch.Tensor, *, activation: str = "silu", return_h: bool = False,
+                         stream=None):
+    """gated_backward with both orientations of its result's codes in one pass,
+    formed from FP32 values: (q [T][2 I] uint8, s [2 I/128][round_up(T, 4)]) of the
+    1x128 row tiles for "dgrad_t_tiled", and (qt [2 I][Tp], st [Tp/128][2 I]) of the
+    128x1 column tiles, transposed, for the A side of "wgrad_tiled".  Any T; Tp = T
+    rounded up to 128, the rows past T counting as zeros (quant_act_cols pads the
+    other operand alike).  return_h appends (ht [I][Tp], sht [Tp/128][I]): h's column
+    tiles, operand-tiled, for the weight gradient of the down projection."""
+    T, I = _check_gated_backward(dh, gate_up)
+    Tp, dev = round_up(T, 128), dh.device
+    q = _empty((T, 2 * I), torch.uint8, dev, stream)
+    s = _empty((2 * I // 128, round_up(T, 4)), torch.float32, dev, stream)
+    qt = _empty((2 * I, Tp), torch.uint8, dev, stream)
+    st = _empty((Tp // 128, 2 * I), torch.float32, dev, stream)
+    ht = sht = None
+    if return_h:
+        ht = _empty((I, Tp), torch.uint8, dev, stream)
+        sht = _empty((Tp // 128, I), torch.float32, dev, stream)
+    _gated_backward(dh, gate_up, activation, stream, None, q, s, qt, st, ht, sht)
+    return (q, s, qt, st, ht, sht) if return_h else (q, s, qt, st)
+
+
+def quant_act_cols(x: torch.Tensor, *, stream=None):
+    """quant_act_1x128(x, "col_tiled") for any number of rows: (q [cols][Tp] uint8,
+    operand-tiled, s [Tp/128][cols] float32) with Tp = rows rounded up to 128, the rows
+    past the last one counting as zeros.  x: bfloat16 [rows][cols], cols a multiple
+    of 128."""
+    lib = _lib.load_library()
+    _check_2d("x", x, _BF16)
+    _on_current_device("x", x)
+    rows, cols = x.shape
+    Tp = round_up(rows, 128)
+    q = _empty((cols, Tp), torch.uint8, x.device, stream)
+    s = _empty((Tp // 128, cols), torch.float32, x.device, stream)
+    st = lib.fp8_quant_act_cols(_ptr(x), rows, cols, x.stride(0), _ptr(q), _ptr(s), s.stride(0), _stream(stream))
+    _lib.check("fp8_quant_act_cols", st)
+    return q, s
+
+
+def _check_heads(name, t, like=None):
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name}: expected [tokens][heads][dim] with contiguous channels, got shape {tuple(t.shape)} "
+                         f"strides {t.stride()}")
+    if t.dtype not in _FLOATS:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {_FLOATS}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor")
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
+        raise ValueError(f"{name}: expected {tuple(like.shape)} {like.dtype}, got {tuple(t.shape)} {t.dtype}")
+
+
+def _head_sets(q, k):
+    """The sets that are there; tokens, head size and type, which they share."""
+    sets = [(n, t) for n, t in (("q", q), ("k", k)) if t is not None]
+    if not sets:
+        raise ValueError("q, k: at least one is required")
+    for name, t in sets:
+        _check_heads(name, t)
+    first = sets[0][1]
+    _on_current_device(sets[0][0], first)
+    for name, t in sets:
+        if t.shape[0] != first.shape[0] or t.shape[2] != first.shape[2] or t.dtype != first.dtype:
+            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} beside {tuple(first.shape)} {first.dtype}")
+    return first
+
+
+def _head_arguments(first, weights, norm, eps, positions, freq, sections, adjacent):
+    """(arguments between the sets and the stream, what has to live through the call)"""
+    if norm not in _lib.HEAD_NORM:
+        raise ValueError(f"norm: {norm!r} not in {list(_lib.HEAD_NORM)}")
+    T, _, dim = first.shape
+    wt = _lib.OUT_BF16
+    seen = None
+    for name, w in weights.items():
+        _check_vec(name, w, dim, _FLOATS)
+        if w is not None:
+            if norm is None:
+                raise ValueError(f"{name}: without a norm there is no weight")
+            if seen is not None and w.dtype != seen:
+                raise TypeError(f"{name}: {w.dtype} beside {seen}: one type is required")
+            seen = w.dtype
+            wt = _is_fp32(w)
+    _same_device(first.device, positions=positions, freq=freq, **weights)
+    if (positions is None) != (freq is None):
+        raise ValueError("positions and freq: both or neither")
+    rot, nbytes, axes, counts = 0, 8, 1, None
+    if freq is not None:
+        _check_vec("freq", freq, freq.numel(), (torch.float64,))
+        rot = 2 * freq.numel()
+        axes = 1 if sections is None else len(sections)
+        if positions.dtype not in (torch.int32, torch.int64) or not positions.is_contiguous() or \
+                tuple(positions.shape) not in ((T, axes), (T,) if axes == 1 else (T, axes)):
+            raise ValueError(f"positions: contiguous int32 or int64 {(T, axes)} required, got {positions.dtype} "
+                             f"{tuple(positions.shape)}")
+        nbytes = positions.element_size()
+        if sections is not None:
+            counts = (ctypes.c_int64 * axes)(*sections)
+    return (wt, _lib.HEAD_NORM[norm], eps, rot, _ptr(positions), nbytes, axes, counts, _ptr(freq), int(adjacent))
+
+
+def _head_outputs(out, q, k, stream):
+    given = out if out is not None else (None, None)
+    made = []
+    for name, t, o in (("q", q, given[0]), ("k", k, given[1])):
+        if t is None or o is None:
+            made.append(None if t is None else _empty(t.shape, t.dtype, t.device, stream))
+            continue
+        _check_heads(f"out ({name})", o, t)
+        _same_device(t.device, out=o)
+        made.append(o)
+    return made
+
+
+def head_norm_rotary(q: torch.Tensor, k, positions=None, freq=None, *, q_weight=None, k_weight=None, norm="rms",
+                     eps: float = 1e-6, sections=None, adjacent: bool = False, out=None, stream=None):
+    """Norm of each query and key head and the rotation by the token's position, in one pass.
+
+    q [tokens][heads][dim], k [tokens][heads_k][dim] (bfloat16 or float32, either may be
+    None): any strides with contiguous channels, as views of a fused projection have
+    them.  norm: "rms", "layer" or None; q_weight, k_weight: optional [dim] vectors of one
+    type.  freq: float64 device vector of the rotated pairs' frequencies (rot/2 of them;
+    rot <= dim, the other channels pass through), usually
+    base ** (-2 i / rot); the angle is formed in FP64.  positions: int32 or int64
+    [tokens], or [tokens][axes] with sections = how many consecutive pairs follow each
+    axis (time, height, width; up to 4).  adjacent: pairs (2 i, 2 i + 1) instead of
+    (i, i + rot/2).  positions = freq = None: the norm alone.
+    out: optional (q_out, k_out) of q's and k's shapes and type, any strides.
+    Returns (q_out, k_out), None for a set that is None.
+    """
+    lib = _lib.load_library()
+    first = _head_sets(q, k)
+    args = _head_arguments(first, dict(q_weight=q_weight, k_weight=k_weight), norm, eps, positions, freq, sections, adjacent)
+    _same_device(first.device, q=q, k=k)
+    made = _head_outputs(out, q, k, stream)
+    sets = []
+    for t, w, o in ((q, q_weight, made[0]), (k, k_weight, made[1])):
+        sets.append(None if t is None else ctypes.byref(
+            _lib.Heads(_ptr(t), t.shape[1], t.stride(0), t.stride(1), _ptr(w), _ptr(o), o.stride(0), o.stride(1))))
+    st = lib.fp8_head_norm_rotary(first.shape[0], first.shape[2], _is_fp32(first), *sets, *args, _stream(stream))
+    _lib.check("fp8_head_norm_rotary", st)
+    return tuple(made)
+
+
+def head_norm_rotary_backward(dq: torch.Tensor, dk, q, k, positions=None, freq=None, *, q_weight=None, k_weight=None,
+                              norm="rms", eps: float = 1e-6, sections=None, adjacent: bool = False, out=None, stream=None):
+    """Gradients of head_norm_rotary, from its inputs: (dq_in, dk_in, dq_weight, dk_weight).
+
+    dq, dk: the gradients of its outputs (of the inputs' type; None with the set); q, k and the
+    other arguments as in the forward pass.  With norm=None q and k may be None and
+    there are no weight gradients (None); otherwise those are float32 [dim], the
+    sums over tokens and heads (also where the weight is None: of ones).  out:
+    optional (dq_in, dk_in) tensors.
+    """
+    lib = _lib.load_library()
+    first = _head_sets(dq, dk)
+    args = _head_arguments(first, dict(q_weight=q_weight, k_weight=k_weight), norm, eps, positions, freq, sections, adjacent)
+    _same_device(first.device, dq=dq, dk=dk, q=q, k=k)
+    made = _head_outputs(out, dq, dk, stream)
+    T, _, dim = first.shape
+    sets, grads, heads = [], [], []
+    for name, d, x, w, o in (("q", dq, q, q_weight, made[0]), ("k", dk, k, k_weight, made[1])):
+        heads.append(0 if d is None else d.shape[1])
+        if d is None:
+            sets.append(None)
+            grads.append(None)
+            continue
+        if norm is not None:
+            if x is None:
+                raise ValueError(f"{name}: required with a norm")
+            _check_heads(name, x, d)
+        else:
+            x = d
+        dw = None if norm is None else _empty(dim, torch.float32, d.device, stream)
+        grads.append(dw)
+        sets.append(ctypes.byref(_lib.HeadsGrad(_ptr(x), d.shape[1], x.stride(0), x.stride(1), _ptr(w), _ptr(d), d.stride(0),
+                                                d.stride(1), _ptr(o), o.stride(0), o.stride(1), _ptr(dw))))
+    nbytes = 0 if norm is None else lib.fp8_head_norm_rotary_backward_workspace(T, *heads, dim)
+    ws = _workspace(nbytes, first.device, stream)
+    st = lib.fp8_head_norm_rotary_backward(T, dim, _is_fp32(first), *sets, *args, _ptr(ws), nbytes, _stream(stream))
+    _lib.check("fp8_head_norm_rotary_backward", st)
+    return (*made, *grads)

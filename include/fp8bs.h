@@ -549,6 +549,136 @@ fp8_status fp8_adapter_linear(int64_t T, int64_t N, int64_t K, int32_t rank, int
                               void* stream);
 int64_t fp8_adapter_linear_workspace(int64_t T, int64_t N, int64_t K, int32_t rank, int32_t adapters);
 
+/*
+ * Operators between a layer's FP8 products: the gated feed-forward block and the
+ * norms of query and key heads with the position rotation.  Conventions and
+ * workspaces as for the layer operators above.
+ */
+
+/*
+ * fp8_block_gemm_gated - the gated feed-forward product on FP8 codes: both
+ * projections, the activation and the elementwise product in one pass.
+ *     a = A W1^T,  u = A W3^T          (as fp8_block_gemm FPROP: FP32 sums)
+ *     h = act(a) * u
+ *     act(a) = a / (1 + exp(-a))                                  (FP8_ACT_SILU)
+ *            = a / (1 + exp(-2 sqrt(2/pi) (a + 0.044715 a^3)))    (FP8_ACT_GELU, tanh form)
+ *  A, sA   codes [M][lda >= K] and scales [K/128][ld_sa >= M] (1x128 row tiles)
+ *  W13     operand-tiled codes of [2 I][K]: the I rows of W1, then those of W3
+ *  s13     FP32 [2 I/128][ld_s13 >= K/128]
+ *  h       [M][ldh >= I] of h_dtype (BF16 or FP32), rounded once from FP32; or NULL:
+ *  q, scales  instead of h: the codes [M][ldq >= I] and scales [I/128][ld_s >= M]
+ *          of h's 1x128 row tiles, formed from the FP32 values (as
+ *          fp8_layer_norm's codes are).  One of h and q is given, not both
+ *          (FP8_ERR_NULL, FP8_ERR_UNSUPPORTED).
+ *  gate_up optional BF16 [M][ld_gu >= 2 I]: a, then u (the backward pass reads it)
+ *  Any M; K % 128 == 0, I % 128 == 0; limits and alignment as for fp8_block_gemm, and
+ *  (I + 128) K < 2^31.  Up to 64 rows run on a kernel of their own that is bound
+ *  by reading W13; more on the block GEMM's persistent kernel (with its
+ *  per-stream workspace, but while the stream is being captured).  M == 0 is a
+ *  no-op.
+ */
+typedef enum { FP8_ACT_SILU = 0, FP8_ACT_GELU = 1 } fp8_activation;
+fp8_status fp8_block_gemm_gated(int64_t M, int64_t I, int64_t K, const uint8_t* A, int64_t lda, const float* sA,
+                                int64_t ld_sa, const uint8_t* W13, const float* s13, int64_t ld_s13,
+                                fp8_activation act, void* h, fp8_out_dtype h_dtype, int64_t ldh, void* gate_up,
+                                int64_t ld_gu, uint8_t* q, int64_t ldq, float* scales, int64_t ld_s,
+                                void* workspace, int64_t workspace_bytes, void* stream);
+int64_t fp8_block_gemm_gated_workspace(int64_t M, int64_t I, int64_t K);
+
+/*
+ * fp8_gated_backward - gradients of h = act(a) * u, up to the operands of the
+ * two projections' Dgrad and Wgrad products:
+ *     d = [dh * u * act'(a) | dh * act(a)]        ([T][2 I], FP32)
+ *  dh       BF16 [T][ld_dh >= I];  gate_up  BF16 [T][ld_gu >= 2 I]: a, then u
+ *  d        optional BF16 [T][ld_d >= 2 I], rounded once
+ *  q, scales     optional: codes [T][ldq >= 2 I] and scales [2 I/128][ld_s >= T] of d's 1x128
+ *           row tiles (Dgrad's token side)
+ *  qt, scales_t  optional: codes [2 I][ldqt >= Tp] and scales [Tp/128][ld_st >= 2 I] of its 128x1
+ *           column tiles, transposed (Wgrad's A side); Tp = T rounded up to 128, the
+ *           rows past T counting as zeros
+ *  ht, scales_ht optional: operand-tiled codes of h's column tiles, [I][Tp], and scales
+ *           [Tp/128][ld_sht >= I] (Wgrad's B side of the down projection)
+ *  All codes are formed from the FP32 values.  At least one output is given;
+ *  scales come with their codes.  I % 128 == 0; any T; rows 16-byte aligned; T == 0 is a no-op.
+ */
+fp8_status fp8_gated_backward(int64_t T, int64_t I, const void* dh, int64_t ld_dh, const void* gate_up,
+                              int64_t ld_gu, fp8_activation act, void* d, int64_t ld_d, uint8_t* q, int64_t ldq,
+                              float* scales, int64_t ld_s, uint8_t* qt, int64_t ldqt, float* scales_t, int64_t ld_st,
+                              uint8_t* ht, float* scales_ht, int64_t ld_sht, void* stream);
+
+/*
+ * fp8_quant_act_cols - fp8_quant_act_1x128 COL_TILED for any number of rows: the
+ * operand-tiled codes of x^T, [cols][Tp] with Tp = rows rounded up to 128, and scales
+ * [Tp/128][ld_s >= cols]; the rows past the last one count as zeros.  x BF16
+ * [rows][ldx >= cols], cols % 128 == 0.
+ */
+fp8_status fp8_quant_act_cols(const void* x, int64_t rows, int64_t cols, int64_t ldx, uint8_t* q, float* scales,
+                              int64_t ld_s, void* stream);
+
+/*
+ * fp8_head_norm_rotary - norm of each query and key head and the rotation of its
+ * pairs by the token's position, in one pass:
+ *     n = x                                              (FP8_HEAD_NONE)
+ *       = x * rstd * w,  rstd = 1 / sqrt(sum x^2 / dim + eps)              (FP8_HEAD_RMS)
+ *       = (x - mean) * rstd * w,  rstd from sum (x - mean)^2               (FP8_HEAD_LAYER)
+ *     (y1, y2) = (n1 cos t - n2 sin t, n2 cos t + n1 sin t),  t = position * freq[pair]
+ *  q, k       the heads, each optional (NULL or heads == 0), not both:
+ *    x        of x_dtype, element e of head h of token t at x + t ld_token + h ld_head + e: either token by
+ *             token (ld_head >= dim, ld_token >= (heads - 1) ld_head + dim) or head by head
+ *             (ld_token >= dim, ld_head >= (tokens - 1) ld_token + dim)
+ *    weight   [dim] of w_dtype, optional (NULL: ones); none with FP8_HEAD_NONE
+ *    y        as x, at its own strides, rounded once from FP32
+ *  rot        channels 0 .. rot - 1 rotate (even, <= dim): pairs (i, i + rot/2), or (2 i, 2 i + 1)
+ *             with `adjacent`; the others pass through.  0: no rotation.
+ *  positions  int32 or int64 (position_bytes 4 or 8) [tokens][axes], contiguous; may be negative
+ *  axes       1 .. 4; sections (HOST array [axes], NULL with one axis): how many
+ *             consecutive pairs follow each axis, rot/2 in all
+ *  freq       FP64 [rot/2]; the angle is formed in FP64, so that positions of millions keep
+ *             their last bits
+ *  dim        even, 2 .. 1024; eps >= 0.  Any alignment to the element size is taken; 16-byte
+ *             aligned heads with dim % 16 == 0 and rot % 16 == 0 are moved in 16-byte
+ *             pieces.  No output may overlap an input or another output (the two
+ *             outputs may lie side by side within each token's row).
+ *  tokens == 0 is a no-op.
+ */
+typedef enum { FP8_HEAD_NONE = 0, FP8_HEAD_RMS = 1, FP8_HEAD_LAYER = 2 } fp8_head_norm;
+typedef struct {
+  const void* x;
+  int64_t heads, ld_token, ld_head;
+  const void* weight;
+  void* y;
+  int64_t ldy_token, ldy_head;
+} fp8_heads;
+fp8_status fp8_head_norm_rotary(int64_t tokens, int64_t dim, fp8_out_dtype x_dtype, const fp8_heads* q,
+                                const fp8_heads* k, fp8_out_dtype w_dtype, fp8_head_norm norm, float eps, int64_t rot,
+                                const void* positions, int32_t position_bytes, int32_t axes, const int64_t* sections,
+                                const double* freq, int32_t adjacent, void* stream);
+
+/*
+ * fp8_head_norm_rotary_backward - its gradients, from the same x (read again: the norms'
+ * statistics are formed anew).
+ *  x, weight  as in the forward pass (x is not read with FP8_HEAD_NONE and may be NULL)
+ *  dy, dx     of x_dtype, [tokens][heads][dim] at strides as x's
+ *  dweight    optional FP32 [dim]: the sum over tokens and heads (tokens == 0 writes
+ *             zeros); none with FP8_HEAD_NONE.  Fixed order: results repeat bit for bit.
+ */
+typedef struct {
+  const void* x;
+  int64_t heads, ld_token, ld_head;
+  const void* weight;
+  const void* dy;
+  int64_t lddy_token, lddy_head;
+  void* dx;
+  int64_t lddx_token, lddx_head;
+  float* dweight;
+} fp8_heads_grad;
+fp8_status fp8_head_norm_rotary_backward(int64_t tokens, int64_t dim, fp8_out_dtype x_dtype, const fp8_heads_grad* q,
+                                         const fp8_heads_grad* k, fp8_out_dtype w_dtype, fp8_head_norm norm, float eps,
+                                         int64_t rot, const void* positions, int32_t position_bytes, int32_t axes,
+                                         const int64_t* sections, const double* freq, int32_t adjacent,
+                                         void* workspace, int64_t workspace_bytes, void* stream);
+int64_t fp8_head_norm_rotary_backward_workspace(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim);
+
 /* Static string naming a status; never NULL. */
 const char* fp8_status_string(fp8_status s);
 
