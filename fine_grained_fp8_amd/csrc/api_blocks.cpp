@@ -143,7 +143,7 @@ extern "C" {
 int64_t fp8_block_gemm_gated_workspace(int64_t M, int64_t I, int64_t K) {
   if (gated_shape(M, I, K) != FP8_OK) return -1;
   if (M > fp8bs::kGatedFewTokens) return 0;
-  const int cuts = fp8bs::gated_few_cuts(I, K);
+  const int64_t cuts = fp8bs::gated_few_cuts(M, I, K);
   return (cuts > 1 ? 2 * cuts : 1) * M * I * 4;
 }
 
@@ -197,7 +197,7 @@ fp8_status fp8_block_gemm_gated(int64_t M, int64_t I, int64_t K, const uint8_t* 
     p.W = W13; p.sW = s13; p.ld_sw = ld_s13;
     p.C = h; p.ldc = ldh; p.out_fp32 = e == 4;
     p.gated = ge;
-    p.cuts = fp8bs::gated_few_cuts(I, K);
+    p.cuts = fp8bs::gated_few_cuts(M, I, K);
     p.parts = static_cast<float*>(workspace);
     return launched(fp8bs::launch_gated_few(p, s));
   }

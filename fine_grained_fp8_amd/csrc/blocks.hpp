@@ -15,8 +15,8 @@ namespace fp8bs {
 // ---- the gated product for up to kGatedFewTokens tokens ----
 constexpr int kGatedFewTokens = 64;
 constexpr int kGatedMaxCuts = 8;
-// Workgroups that share the K blocks of a 16-channel tile
-int gated_few_cuts(int64_t N, int64_t K);
+// Workgroups that share the K blocks of a tile of channels
+int gated_few_cuts(int64_t M, int64_t N, int64_t K);
 struct GatedFewProblem {
   int M;
   int64_t N, K;
@@ -32,7 +32,7 @@ struct GatedFewProblem {
   int out_fp32;
   GatedEpilogue gated;
   // workspace
-  int cuts;               // gated_few_cuts(N, K)
+  int cuts;               // gated_few_cuts(M, N, K)
   float* parts;           // [cuts][M][2 N] if cuts > 1; otherwise [M][N], h of a call for codes
 };
 hipError_t launch_gated_few(const GatedFewProblem& p, hipStream_t stream);

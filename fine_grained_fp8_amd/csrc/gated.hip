@@ -5,8 +5,10 @@
 //   a = X W1^T, u = X W3^T,  h = act(a) u,  act(a) = a logistic(v(a))
 //   da = dh u act'(a),  du = dh act(a)
 //   act'(a) = z + a z (1 - z) v'(a),  z = logistic(v(a))
-#include "device.hpp"
+#include <atomic>
+
 #include "blocks.hpp"
+#include "device.hpp"
 #include "gate.hpp"
 #include "rows.hpp"
 
@@ -32,6 +34,10 @@ __device__ __forceinline__ v8bf codes_to_bf16(int lo, int hi) {
   return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+constexpr int64_t kMaxLds = 163840;
+constexpr int kRowWaves = 8;                     // waves of a workgroup of the kernel for up to 16 tokens
+constexpr int64_t kRowBlockLds = 2048 + 64;      // its LDS for one K block: 16 tokens' codes and scales
+
 // A 128-wide K block of a 16-row operand: a lane's 32 codes (bytes 16 g.. and
 // 64 + 16 g.. for lane group g).
 struct Block {
@@ -55,20 +61,66 @@ __device__ __forceinline__ float gated(float a, float u, int gelu) {
   return a * logistic(gelu ? gelu_argument(a) : a) * u;
 }
 
-// A workgroup has RT tiles of 16 channels, the gate rows and the up rows of
-// each, for every token; its PW waves deal the K blocks of its share (`cuts`
-// workgroups share a tile's), the next block's weights loaded before the
-// present one's products.  The products convert the codes to BF16: exact, with
-// FP32 sums.
-template <int NT, int RT, int PW>
-__global__ __launch_bounds__(PW * 64, 2) void gated_few_kernel(GatedFewProblem p) {
-  __shared__ v4f part[PW][RT][2][64];
+// wait until at most n vector-memory operations of this wave are outstanding and
+// all LDS and scalar ones are done
+template <int n>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(n >= 0 && n < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((n & 15) | (7 << 4) | (0 << 8) | ((n >> 4) << 14));
+}
+
+// 4 channels of a token, from n: the sums for the finishing launch, or what the call
+// asked for
+__device__ __forceinline__ void leave(const GatedFewProblem& p, int cut, int t, int64_t n, const v4f& a, const v4f& u) {
+  if (p.cuts > 1) {
+    float* at = p.parts + ((int64_t)cut * p.M + t) * 2 * p.N + n;
+    *reinterpret_cast<v4f*>(at) = a;
+    *reinterpret_cast<v4f*>(at + p.N) = u;
+    return;
+  }
+  if (p.gated.gate_up != nullptr) {
+    uint16_t* at = p.gated.gate_up + t * p.gated.ld_gu + n;
+    *reinterpret_cast<v4bf*>(at) = __builtin_convertvector(a, v4bf);
+    *reinterpret_cast<v4bf*>(at + p.N) = __builtin_convertvector(u, v4bf);
+  }
+  v4f h;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) h[v] = gated(a[v], u[v], p.gated.gelu);
+  if (p.gated.q != nullptr) *reinterpret_cast<v4f*>(p.parts + t * p.N + n) = h;
+  else if (p.out_fp32) *reinterpret_cast<v4f*>(static_cast<float*>(p.C) + t * p.ldc + n) = h;
+  else *reinterpret_cast<v4bf*>(static_cast<uint16_t*>(p.C) + t * p.ldc + n) = __builtin_convertvector(h, v4bf);
+}
+
+// Up to 16 tokens.  A workgroup has RT tiles of 16 channels, the gate rows and
+// the up rows of each; its eight waves deal the K blocks of its share (all of
+// K, unless its codes would not fit LDS).  The weights go from memory straight
+// into MFMA operand registers, D blocks of a wave in flight.  The token codes are
+// copied into LDS first (DMA, in operand order: 1 KB for 16 tokens and 64 bytes of
+// K), so that the loop's only loads from memory are weights: loads return in the
+// order of their issue, and a token operand asked for in the loop would wait for
+// all weights asked for before it.
+// What bounds it: reading the weights (one token, 7168 x 18432: 264 MB in 51 us, 5.2
+// TB/s), and for small ones the latency of a launch and of the first load (7168 x 2048,
+// 29 MB: 10.4 us; 2048 x 1408: 5.1).
+template <int RT, int D>
+__global__ __launch_bounds__(kRowWaves * 64) void gated_row_kernel(GatedFewProblem p) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];   // codes [share][2048], scales [share][16]; then sums
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lrow = lane & 15, lgrp = lane >> 4;
   const int kb_n = (int)(p.K / 128), M = p.M;
   const int cut = blockIdx.x % p.cuts, group = blockIdx.x / p.cuts;
-  const int kb0 = (int)((int64_t)kb_n * cut / p.cuts), kb1 = (int)((int64_t)kb_n * (cut + 1) / p.cuts);
+  const int kb0 = (int)((int64_t)kb_n * cut / p.cuts), kb1 = (int)((int64_t)kb_n * (cut + 1) / p.cuts), share = kb1 - kb0;
   const int tiles = (int)(p.N / 16);
+  // the token codes; tokens past the last one lie outside of the buffer and read as zero
+  using lds_u8 = __attribute__((address_space(3))) uint8_t;
+  const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)p.A, (short)0, (int)((M - 1) * p.lda + p.K), 0x00020000);
+  for (int o = wave; o < share * 2; o += kRowWaves) {
+    const uint32_t at = lrow < M ? (uint32_t)(lrow * (int)p.lda + (kb0 + o / 2) * 128 + (o & 1) * 64 + lgrp * 16) : 0xFFFFFF00u;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)((lds_u8*)lds + o * 1024), 16, at, 0, 0, 0);
+  }
+  float* scales = reinterpret_cast<float*>(lds + share * 2048);
+  for (int i = threadIdx.x; i < share * 16; i += kRowWaves * 64)
+    scales[i] = (i & 15) < M ? p.sA[(int64_t)(kb0 + i / 16) * p.ld_sa + (i & 15)] : 0.f;
   const uint8_t* w[RT][2];
   const float* s[RT][2];
 #pragma unroll
@@ -80,17 +132,9 @@ __global__ __launch_bounds__(PW * 64, 2) void gated_few_kernel(GatedFewProblem p
       s[i][g] = p.sW + ((int64_t)g * (tiles / 8) + t / 8) * p.ld_sw;
     }
   }
-  const uint8_t* x[NT];
-  const float* sx[NT];
-  v4f acc[RT][2][NT];
+  v4f acc[RT][2];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int t = min(j * 16 + lrow, M - 1);
-    x[j] = p.A + t * p.lda + lgrp * 16;
-    sx[j] = p.sA + t;
-#pragma unroll
-    for (int i = 0; i < RT; ++i) acc[i][0][j] = acc[i][1][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  }
+  for (int i = 0; i < RT; ++i) acc[i][0] = acc[i][1] = v4f{0.f, 0.f, 0.f, 0.f};
   auto fetch = [&](int kb, Block (&b)[RT][2]) {
 #pragma unroll
     for (int i = 0; i < RT; ++i)
@@ -100,83 +144,205 @@ __global__ __launch_bounds__(PW * 64, 2) void gated_few_kernel(GatedFewProblem p
         b[i][g] = Block{*reinterpret_cast<const gv4i*>(at), *reinterpret_cast<const gv4i*>(at + 1024)};
       }
   };
-  const int last = kb1 - 1;
-  auto step = [&](int kb, const Block (&b)[RT][2], Block (&next)[RT][2]) {
-    Block xb[NT];
-    float c[NT];
+  __asm__ volatile("" ::: "memory");
+  Block b[D][RT][2];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const uint8_t* at = x[j] + kb * 128;
-      xb[j] = Block{*reinterpret_cast<const gv4i*>(at), *reinterpret_cast<const gv4i*>(at + 64)};
-      c[j] = sx[j][(int64_t)kb * p.ld_sa];
-    }
-    __asm__ volatile("" ::: "memory");
-    fetch(min(kb + PW, last), next);     // past the wave's last block: one that is not used
-    Bf16Block xf[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) xf[j] = to_bf16(xb[j]);
+  for (int d = 0; d < D; ++d)
+    if (kb0 + wave + d * kRowWaves < kb1) fetch(kb0 + wave + d * kRowWaves, b[d]);
+  // the wave's copies into LDS have landed when only the D blocks asked for after
+  // them are outstanding; a bare barrier, which leaves those in flight
+  __asm__ volatile("" ::: "memory");
+  if (kb0 + wave + (D - 1) * kRowWaves < kb1) wait_loads<D * RT * 4>();
+  else wait_loads<0>();
+  __builtin_amdgcn_s_barrier();
+  __asm__ volatile("" ::: "memory");
+  auto products = [&](int kb, const Block (&b)[RT][2]) {
+    const uint8_t* at = lds + (kb - kb0) * 2048 + lane * 16;
+    const float sc = scales[(kb - kb0) * 16 + lrow];
+    const Bf16Block x = to_bf16(Block{*reinterpret_cast<const gv4i*>(at), *reinterpret_cast<const gv4i*>(at + 1024)});
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const Bf16Block wf = to_bf16(b[i][g]);
-        const float f = s[i][g][kb];
+        const float c = sc * s[i][g][kb];
+        const v4f q = block_product(to_bf16(b[i][g]), x);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[i][g][v] = __builtin_fmaf(q[v], c, acc[i][g][v]);
+      }
+  };
+  for (int k0 = kb0 + wave; k0 < kb1; k0 += D * kRowWaves) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const int kb = k0 + d * kRowWaves;
+      if (kb >= kb1) break;
+      products(kb, b[d]);
+      if (kb + D * kRowWaves < kb1) fetch(kb + D * kRowWaves, b[d]);
+    }
+  }
+  v4f (*part)[RT][2][64] = reinterpret_cast<v4f (*)[RT][2][64]>(lds);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    part[wave][i][0][lane] = acc[i][0];
+    part[wave][i][1][lane] = acc[i][1];
+  }
+  __syncthreads();
+  for (int i = wave; i < RT; i += kRowWaves) {
+    v4f a = part[0][i][0][lane], u = part[0][i][1][lane];
+#pragma unroll
+    for (int q = 1; q < kRowWaves; ++q) {
+      a += part[q][i][0][lane];
+      u += part[q][i][1][lane];
+    }
+    const int tile = group * RT + i;
+    if (lrow < M && tile < tiles) leave(p, cut, lrow, tile * 16 + lgrp * 4, a, u);
+  }
+}
+
+// 17 to 64 tokens (NT groups of 16).  A wave has RT tiles of 16 channels, the gate
+// rows and the up rows of each, for every token; a workgroup's four waves have
+// neighbouring tiles, and `cuts` workgroups share the K blocks.  Weights go from memory straight into MFMA operand
+// registers; the token codes, which the waves share, through LDS by DMA.  Both are
+// asked for D blocks ahead, in the order they are needed (loads return in the
+// order of their issue); one barrier a block.  Measured against the waves dealing the
+// K blocks, each with its own token operands (as for up to 16 tokens), us: 64
+// tokens, 7168 x 18432 58 for 99 (a workgroup's tokens are read once for its four
+// waves), 48 tokens, 7168 x 2048 14.3 for 15.6, 64 tokens, 2048 x 1408 10.4 for 10.0; one
+// token, 7168 x 2048 11.8 for 9.8.  kExact: products of the codes as BF16, exact with FP32
+// sums, so that FP32 values, scales and codes do not move with the FP8 instruction's
+// truncation (64 tokens, 7168 x 18432: 70 us for 58).
+template <int NT, int RT, int D, bool kExact>
+__global__ __launch_bounds__(256) void gated_few_kernel(GatedFewProblem p) {
+  constexpr int kTokens = NT * 2048, kStage = kTokens + 256 + 4 * 256;   // codes, token scales, each wave's two weight scales
+  constexpr int kXOps = (NT * 2 + 3) / 4, kOps = kXOps + 2 + 4 * RT;     // loads of a wave for one block
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];        // [D + 1][kStage]
+  using lds_u8 = __attribute__((address_space(3))) uint8_t;
+  using lds_ptr = __attribute__((address_space(3))) void*;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lrow = lane & 15, lgrp = lane >> 4;
+  const int kb_n = (int)(p.K / 128), M = p.M, tiles = (int)(p.N / 16);
+  const int cut = blockIdx.x % p.cuts, t0 = (blockIdx.x / p.cuts * 4 + wave) * RT;   // the wave's first tile
+  const int kb0 = (int)((int64_t)kb_n * cut / p.cuts), n = (int)((int64_t)kb_n * (cut + 1) / p.cuts) - kb0;
+  // buffers end behind the last token and the last scale: what lies past them reads as zero
+  const __amdgpu_buffer_rsrc_t rsrc_x = __builtin_amdgcn_make_buffer_rsrc((void*)p.A, (short)0, (int)((M - 1) * p.lda + p.K), 0x00020000);
+  const __amdgpu_buffer_rsrc_t rsrc_s =
+      __builtin_amdgcn_make_buffer_rsrc((void*)p.sW, (short)0, (int)(2 * (p.N / 128) * p.ld_sw * 4), 0x00020000);
+  // DMA instruction o of a block: rows 8 o .. + 7, 128 bytes each, 16-byte chunks XOR-swizzled by row & 7
+  const uint32_t x_off = (uint32_t)((lane >> 3) * (int)p.lda + (((lane & 7) ^ (lane >> 3)) << 4));
+  const uint32_t s_off = (uint32_t)((t0 / 8 + (lane >= 32 ? tiles / 8 : 0)) * (int)p.ld_sw) * 4u;
+  const uint8_t* w[RT][2];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int g = 0; g < 2; ++g) w[i][g] = p.W + ((int64_t)g * tiles + t0 + i) * kb_n * 2048 + lane * 16;
+  v8i b[D][RT][2];
+  auto issue_shared = [&](int k, int stage) {
+    lds_u8* st = (lds_u8*)lds + stage * kStage;
+    const int kb = kb0 + k;
+#pragma unroll
+    for (int q = 0; q < kXOps; ++q) {
+      int o = wave * kXOps + q;
+      if constexpr (kXOps * 4 != NT * 2) o = o < NT * 2 ? o : NT * 2 - 1;       // again: every wave counts the same loads
+      const uint32_t at = x_off + (uint32_t)(kb * 128 + o * 8 * (int)p.lda);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc_x, (lds_ptr)(st + o * 1024), 16, at, 0, 0, 0);
+    }
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)(p.sA + (int64_t)kb * p.ld_sa), (short)0, M * 4, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(st + kTokens), 4, (uint32_t)lane * 4u, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc_s, (lds_ptr)(st + kTokens + 256 + wave * 256), 4, s_off + (uint32_t)kb * 4u, 0, 0, 0);
+    __asm__ volatile("" ::: "memory");
+  };
+  auto issue_weights = [&](int k, v8i (&f)[RT][2]) {
+    const int kb = kb0 + k;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const gv4i lo = *reinterpret_cast<const gv4i*>(w[i][g] + (int64_t)kb * 2048);
+        const gv4i hi = *reinterpret_cast<const gv4i*>(w[i][g] + (int64_t)kb * 2048 + 1024);
+        f[i][g] = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      }
+    __asm__ volatile("" ::: "memory");
+  };
+  v4f acc[RT][2][NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < RT; ++i) acc[i][0][j] = acc[i][1][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  auto operand = [&](const v8i& v) {
+    if constexpr (kExact)
+      return Bf16Block{{codes_to_bf16(v[0], v[1]), codes_to_bf16(v[2], v[3]), codes_to_bf16(v[4], v[5]), codes_to_bf16(v[6], v[7])}};
+    else
+      return v;
+  };
+  auto products = [&](int stage, const v8i (&f)[RT][2]) {
+    const uint8_t* st = lds + stage * kStage;
+    const float* sx = reinterpret_cast<const float*>(st + kTokens) + lrow;
+    const float* sw = reinterpret_cast<const float*>(st + kTokens + 256 + wave * 256);
+    const float cg = sw[0], cu = sw[32];
+    const uint8_t* at = st + lrow * 128;
+    decltype(operand(v8i{})) x[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const gv4i lo = *reinterpret_cast<const gv4i*>(at + j * 2048 + ((lgrp ^ (lrow & 7)) << 4));
+      const gv4i hi = *reinterpret_cast<const gv4i*>(at + j * 2048 + (((4 + lgrp) ^ (lrow & 7)) << 4));
+      x[j] = operand(v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+    }
+    float c[2][NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const float t = sx[j * 16];
+      c[0][j] = t * cg;
+      c[1][j] = t * cu;
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const auto wf = operand(f[i][g]);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          const v4f q = block_product(wf, xf[j]);
-          const float cj = c[j] * f;
+          v4f q;
+          if constexpr (kExact) q = block_product(wf, x[j]);
+          else q = mfma_e4m3_16x16x128(wf, x[j], v4f{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-          for (int v = 0; v < 4; ++v) acc[i][g][j][v] = __builtin_fmaf(q[v], cj, acc[i][g][j][v]);
+          for (int v = 0; v < 4; ++v) acc[i][g][j][v] = __builtin_fmaf(q[v], c[g][j], acc[i][g][j][v]);
         }
       }
   };
-  if (kb0 + wave < kb1) {
-    Block b0[RT][2], b1[RT][2];
-    fetch(kb0 + wave, b0);
-    for (int kb = kb0 + wave;; kb += 2 * PW) {
-      step(kb, b0, b1);
-      if (kb + PW >= kb1) break;
-      step(kb + PW, b1, b0);
-      if (kb + 2 * PW >= kb1) break;
-    }
+  // Past the share's last block its loads are asked for again (not used), so that
+  // every step counts the same loads.
+#pragma unroll
+  for (int d = 0; d < D; ++d) {
+    issue_shared(d < n ? d : n - 1, d);
+    issue_weights(d < n ? d : n - 1, b[d]);
+  }
+  int stage = 0;
+  auto step = [&](int k, v8i (&f)[RT][2]) {
+    wait_loads<(D - 1) * kOps>();
+    __builtin_amdgcn_s_barrier();
+    __asm__ volatile("" ::: "memory");
+    const int ahead = k + D < n ? k + D : n - 1;
+    issue_shared(ahead, stage == 0 ? D : stage - 1);     // the stage of the step before: every wave is past its reads
+    products(stage, f);
+    __builtin_amdgcn_sched_barrier(0);
+    issue_weights(ahead, f);
+    stage = stage == D ? 0 : stage + 1;
+  };
+  int k = 0;
+  for (; k + D <= n; k += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) step(k + d, b[d]);
   }
 #pragma unroll
+  for (int d = 0; d < D - 1; ++d)
+    if (k + d < n) step(k + d, b[d]);
+  wait_loads<0>();     // the loads asked for again land before the workgroup's LDS goes
+#pragma unroll
   for (int j = 0; j < NT; ++j) {
-    if (j != 0) __syncthreads();
+    const int t = j * 16 + lrow;
+    if (t >= M) continue;
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      part[wave][i][0][lane] = acc[i][0][j];
-      part[wave][i][1][lane] = acc[i][1][j];
-    }
-    __syncthreads();
-    for (int i = wave; i < RT; i += PW) {
-      v4f a = part[0][i][0][lane], u = part[0][i][1][lane];
-#pragma unroll
-      for (int q = 1; q < PW; ++q) {
-        a += part[q][i][0][lane];
-        u += part[q][i][1][lane];
-      }
-      const int t = j * 16 + lrow, tile = group * RT + i;
-      if (t >= M || tile >= tiles) continue;
-      const int64_t n = tile * 16 + lgrp * 4;
-      if (p.cuts > 1) {
-        float* at = p.parts + ((int64_t)cut * M + t) * 2 * p.N + n;
-        *reinterpret_cast<v4f*>(at) = a;
-        *reinterpret_cast<v4f*>(at + p.N) = u;
-        continue;
-      }
-      if (p.gated.gate_up != nullptr) {
-        uint16_t* at = p.gated.gate_up + t * p.gated.ld_gu + n;
-        *reinterpret_cast<v4bf*>(at) = __builtin_convertvector(a, v4bf);
-        *reinterpret_cast<v4bf*>(at + p.N) = __builtin_convertvector(u, v4bf);
-      }
-      v4f h;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) h[v] = gated(a[v], u[v], p.gated.gelu);
-      if (p.gated.q != nullptr) *reinterpret_cast<v4f*>(p.parts + t * p.N + n) = h;
-      else if (p.out_fp32) *reinterpret_cast<v4f*>(static_cast<float*>(p.C) + t * p.ldc + n) = h;
-      else *reinterpret_cast<v4bf*>(static_cast<uint16_t*>(p.C) + t * p.ldc + n) = __builtin_convertvector(h, v4bf);
-    }
+    for (int i = 0; i < RT; ++i) leave(p, cut, t, (int64_t)(t0 + i) * 16 + lgrp * 4, acc[i][0][j], acc[i][1][j]);
   }
 }
 
@@ -235,17 +401,48 @@ __global__ __launch_bounds__(256) void gated_finish_kernel(GatedFewProblem p) {
   }
 }
 
-template <int NT, int RT, int PW>
-void few(const GatedFewProblem& p, hipStream_t stream) {
-  const int64_t tiles = p.N / 16;
-  hipLaunchKernelGGL((gated_few_kernel<NT, RT, PW>), dim3((unsigned)((tiles + RT - 1) / RT * p.cuts)), dim3(PW * 64), 0,
-                     stream, p);
+// A launch with its dynamic LDS.  More than 64 KB has to be announced, once for
+// each kernel and device.
+template <auto kKernel>
+hipError_t start(int64_t grid, int block, int64_t lds, const GatedFewProblem& p, hipStream_t stream) {
+  static std::atomic<uint64_t> announced{0};       // a bit for each device
+  if (lds > 65536) {
+    int dev = -1;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t{1} << dev : 0;
+    if ((announced.load(std::memory_order_relaxed) & bit) == 0) {
+      e = hipFuncSetAttribute(reinterpret_cast<const void*>(kKernel), hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLds);
+      if (e != hipSuccess) return e;
+      announced.fetch_or(bit, std::memory_order_relaxed);
+    }
+  }
+  hipLaunchKernelGGL(kKernel, dim3((unsigned)grid), dim3(block), lds, stream, p);
+  return hipGetLastError();
 }
 
+// tiles of a workgroup of the kernel for up to 16 tokens: one workgroup for each of the 256 CUs
+int row_tiles(int64_t N) {
+  const int64_t n = (N / 16 + 255) / 256;
+  return (int)(n < 5 ? n : 5);
+}
+template <int RT, int D>
+hipError_t row(const GatedFewProblem& p, hipStream_t stream) {
+  const int64_t share = (p.K / 128 + p.cuts - 1) / p.cuts, sums = (int64_t)kRowWaves * RT * 2048;
+  const int64_t codes = share * kRowBlockLds;
+  return start<gated_row_kernel<RT, D>>((p.N / 16 + RT - 1) / RT * p.cuts, kRowWaves * 64, codes > sums ? codes : sums, p, stream);
+}
+
+template <int NT, int RT, int D, bool kExact>
+hipError_t few(const GatedFewProblem& p, hipStream_t stream) {
+  return start<gated_few_kernel<NT, RT, D, kExact>>(p.N / (64 * RT) * p.cuts, 256, (D + 1) * (NT * 2048 + 1280), p, stream);
+}
 template <int NT>
-void few_tiles(const GatedFewProblem& p, hipStream_t stream) {
-  if (p.N / 16 * p.cuts <= 512) few<NT, 1, 8>(p, stream);
-  else few<NT, 2, 4>(p, stream);
+hipError_t few_tokens(const GatedFewProblem& p, hipStream_t stream) {
+  // FP32 results and codes: exact products
+  if (p.gated.q != nullptr || p.out_fp32) return few<NT, 1, 3, true>(p, stream);
+  if (p.N / 64 >= 256) return few<NT, 2, 2, false>(p, stream);
+  return few<NT, 1, 3, false>(p, stream);
 }
 
 // ===========================================================================
@@ -430,21 +627,28 @@ __global__ __launch_bounds__(kGB) void gated_backward_kernel(GatedGradProblem p)
 
 }  // namespace
 
-int gated_few_cuts(int64_t N, int64_t K) {
-  const int64_t tiles = N / 16, kb = K / 128;
-  int64_t c = (256 + tiles - 1) / tiles;
-  if (c > kGatedMaxCuts) c = kGatedMaxCuts;
-  if (c > kb) c = kb;
-  return (int)c;
+int gated_few_cuts(int64_t M, int64_t N, int64_t K) {
+  const int64_t kb = K / 128;
+  if (M <= 16) return (int)((kb + kMaxLds / kRowBlockLds - 1) / (kMaxLds / kRowBlockLds));
+  const int64_t groups = N / 64, most = kb / 4 < kGatedMaxCuts ? kb / 4 : kGatedMaxCuts;
+  const int64_t c = 256 / groups < most ? 256 / groups : most;
+  return (int)(c > 1 ? c : 1);
 }
 
 hipError_t launch_gated_few(const GatedFewProblem& p, hipStream_t stream) {
-  switch ((p.M + 15) / 16) {
-    case 1: few_tiles<1>(p, stream); break;
-    case 2: few_tiles<2>(p, stream); break;
-    case 3: few_tiles<3>(p, stream); break;
-    default: few_tiles<4>(p, stream); break;
+  hipError_t e;
+  if (p.M <= 16) {
+    switch (row_tiles(p.N)) {
+      case 1: e = row<1, 2>(p, stream); break;
+      case 2: e = row<2, 1>(p, stream); break;
+      case 3: e = row<3, 1>(p, stream); break;
+      case 4: e = row<4, 1>(p, stream); break;
+      default: e = row<5, 1>(p, stream); break;
+    }
+  } else {
+    e = p.M <= 32 ? few_tokens<2>(p, stream) : p.M <= 48 ? few_tokens<3>(p, stream) : few_tokens<4>(p, stream);
   }
+  if (e != hipSuccess) return e;
   if (p.cuts > 1 || p.gated.q != nullptr) {
     const int64_t groups = p.M * (p.N / 128);
     hipLaunchKernelGGL(gated_finish_kernel, dim3((unsigned)((groups + 15) / 16)), dim3(256), 0, stream, p);
