@@ -8,6 +8,7 @@ ld = round_up(rows, 4) for 1x128 row tiles.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -463,6 +464,8 @@ def quant_act_tiles(x: torch.Tensor, tile: int = 128, rank: int = 1, *, sat_coun
 
 
 _FLOATS = (torch.bfloat16, torch.float32)
+_FP32 = (torch.float32,)
+_CODES = (torch.uint8, torch.float8_e4m3fn)
 
 
 def _float_type(dtype):
@@ -706,40 +709,57 @@ def _activation(name):
     return _lib.ACTIVATION[name]
 
 
+# what the library answers for these sizes, asked for once (a call into it takes
+# half a microsecond)
+@functools.lru_cache(maxsize=4096)
+def _gated_workspace(M, I, K):
+    return _lib.load_library().fp8_block_gemm_gated_workspace(M, I, K)
+
+
+@functools.lru_cache(maxsize=4096)
+def _heads_workspace(T, heads_q, heads_k, dim):
+    return _lib.load_library().fp8_head_norm_rotary_backward_workspace(T, heads_q, heads_k, dim)
+
+
 def _gated(A, sA, w13, s13, activation, quant, return_gate_up, out_dtype, out, stream):
     lib = _lib.load_library()
     act = _activation(activation)
-    _check_2d("A", A, (torch.uint8, torch.float8_e4m3fn))
-    _check_2d("sA", sA, (torch.float32,))
-    _check_2d("s13", s13, (torch.float32,))
+    _check_2d("A", A, _CODES)
+    _check_2d("sA", sA, _FP32)
+    _check_2d("s13", s13, _FP32)
     _on_current_device("A", A)
     M, K = A.shape
-    if w13.dim() != 2 or w13.shape[0] % 2 != 0:
+    rows = w13.shape[0] if w13.dim() == 2 else 1
+    if rows % 2 != 0:
         raise ValueError(f"w13: expected [2 I][K], got {tuple(w13.shape)}")
-    I = w13.shape[0] // 2
-    _check_codes("w13", w13, (2 * I, K))
-    if sA.shape[0] < K // 128 or sA.shape[1] < M or s13.shape[0] < 2 * I // 128 or s13.shape[1] < K // 128:
+    I = rows // 2
+    _check_codes("w13", w13, (rows, K))
+    if sA.shape[0] < K // 128 or sA.shape[1] < M or s13.shape[0] < rows // 128 or s13.shape[1] < K // 128:
         raise ValueError(f"sA {tuple(sA.shape)}, s13 {tuple(s13.shape)}: expected at least {(K // 128, M)} and "
-                         f"{(2 * I // 128, K // 128)}")
-    _same_device(A.device, sA=sA, w13=w13, s13=s13, out=out)
+                         f"{(rows // 128, K // 128)}")
+    dev = A.device
+    _same_device(dev, sA=sA, w13=w13, s13=s13, out=out)
     q = s = gate_up = None
+    ldh = ld_s = h_type = 0
     if quant:
-        q = _empty((M, I), torch.uint8, A.device, stream)
-        s = _empty((I // 128, round_up(M, 4)), torch.float32, A.device, stream)
-    elif out is None:
-        out = _empty((M, I), _float_type(out_dtype), A.device, stream)
+        ld_s = round_up(M, 4)
+        q = _empty((M, I), torch.uint8, dev, stream)
+        s = _empty((I // 128, ld_s), torch.float32, dev, stream)
     else:
-        _check_2d("out", out, _FLOATS)
-        if tuple(out.shape) != (M, I):
-            raise ValueError(f"out: expected {(M, I)}, got {tuple(out.shape)}")
+        if out is None:
+            out = _empty((M, I), _float_type(out_dtype), dev, stream)
+        else:
+            _check_2d("out", out, _FLOATS)
+            if out.shape != (M, I):
+                raise ValueError(f"out: expected {(M, I)}, got {tuple(out.shape)}")
+        ldh, h_type = out.stride(0), _is_fp32(out)
     if return_gate_up:
-        gate_up = _empty((M, 2 * I), torch.bfloat16, A.device, stream)
-    nbytes = lib.fp8_block_gemm_gated_workspace(M, I, K)
-    ws = _workspace(nbytes, A.device, stream)
+        gate_up = _empty((M, rows), torch.bfloat16, dev, stream)
+    nbytes = _gated_workspace(M, I, K)
+    ws = _workspace(nbytes, dev, stream) if nbytes != 0 else None
     st = lib.fp8_block_gemm_gated(
-        M, I, K, _ptr(A), A.stride(0), _ptr(sA), sA.stride(0), _ptr(w13), _ptr(s13), s13.stride(0), act,
-        _ptr(out), _lib.OUT_BF16 if out is None else _is_fp32(out), 0 if out is None else out.stride(0),
-        _ptr(gate_up), 2 * I, _ptr(q), I, _ptr(s), 0 if s is None else s.stride(0), _ptr(ws), nbytes, _stream(stream))
+        M, I, K, A.data_ptr(), A.stride(0), sA.data_ptr(), sA.stride(0), w13.data_ptr(), s13.data_ptr(), s13.stride(0), act,
+        _ptr(out), h_type, ldh, _ptr(gate_up), rows, _ptr(q), I, _ptr(s), ld_s, _ptr(ws), nbytes, _stream(stream))
     _lib.check("fp8_block_gemm_gated", st)
     return out, q, s, gate_up
 
@@ -838,78 +858,79 @@ def quant_act_cols(x: torch.Tensor, *, stream=None):
     return q, s
 
 
-def _check_heads(name, t, like=None):
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError(f"{name}: expected [tokens][heads][dim] with contiguous channels, got shape {tuple(t.shape)} "
-                         f"strides {t.stride()}")
-    if t.dtype not in _FLOATS:
-        raise TypeError(f"{name}: dtype {t.dtype} not in {_FLOATS}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a device tensor")
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
-        raise ValueError(f"{name}: expected {tuple(like.shape)} {like.dtype}, got {tuple(t.shape)} {t.dtype}")
+def _check_heads(name, t, dtype, dev, T, heads, dim):
+    """t is [T][heads][dim] (heads None: any number) of this type on this device; its strides."""
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected [tokens][heads][dim], got shape {tuple(t.shape)}")
+    strides, shape = t.stride(), t.shape
+    if strides[2] != 1 and dim > 1:
+        raise ValueError(f"{name}: the channels have to be contiguous, got strides {strides}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if shape[0] != T or shape[2] != dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name}: expected {(T, 'any' if heads is None else heads, dim)}, got {tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
+    return strides
 
 
-def _head_sets(q, k):
-    """The sets that are there; tokens, head size and type, which they share."""
-    sets = [(n, t) for n, t in (("q", q), ("k", k)) if t is not None]
-    if not sets:
+def _first_heads(q, k):
+    """(type, device index, T, dim) that the sets share, and the device."""
+    t = q if q is not None else k
+    if t is None:
         raise ValueError("q, k: at least one is required")
-    for name, t in sets:
-        _check_heads(name, t)
-    first = sets[0][1]
-    _on_current_device(sets[0][0], first)
-    for name, t in sets:
-        if t.shape[0] != first.shape[0] or t.shape[2] != first.shape[2] or t.dtype != first.dtype:
-            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} beside {tuple(first.shape)} {first.dtype}")
-    return first
+    if t.dim() != 3 or t.dtype not in _FLOATS:
+        raise TypeError(f"q, k: expected [tokens][heads][dim] of {_FLOATS}, got {tuple(t.shape)} {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError("q, k: must be device tensors")
+    _on_current_device("q, k", t)
+    return t.dtype, t.get_device(), t.shape[0], t.shape[2], t.device
 
 
-def _head_arguments(first, weights, norm, eps, positions, freq, sections, adjacent):
-    """(arguments between the sets and the stream, what has to live through the call)"""
+def _head_arguments(dev, T, dim, wq, wk, norm, eps, positions, freq, sections, adjacent):
+    """The arguments between the sets and the workspace or stream."""
     if norm not in _lib.HEAD_NORM:
         raise ValueError(f"norm: {norm!r} not in {list(_lib.HEAD_NORM)}")
-    T, _, dim = first.shape
     wt = _lib.OUT_BF16
-    seen = None
-    for name, w in weights.items():
-        _check_vec(name, w, dim, _FLOATS)
+    for name, w in (("q_weight", wq), ("k_weight", wk)):
         if w is not None:
-            if norm is None:
-                raise ValueError(f"{name}: without a norm there is no weight")
-            if seen is not None and w.dtype != seen:
-                raise TypeError(f"{name}: {w.dtype} beside {seen}: one type is required")
-            seen = w.dtype
+            _check_vec(name, w, dim, _FLOATS)
+            if norm is None or w.get_device() != dev:
+                raise ValueError(f"{name}: on {w.device} (expected cuda:{dev}), or given without a norm")
             wt = _is_fp32(w)
-    _same_device(first.device, positions=positions, freq=freq, **weights)
-    if (positions is None) != (freq is None):
+    if wq is not None and wk is not None and wq.dtype != wk.dtype:
+        raise TypeError(f"q_weight is {wq.dtype} and k_weight {wk.dtype}: one type is required")
+    if freq is None:
+        if positions is not None:
+            raise ValueError("positions and freq: both or neither")
+        return wt, _lib.HEAD_NORM[norm], eps, 0, None, 8, 1, None, None, 0
+    if positions is None:
         raise ValueError("positions and freq: both or neither")
-    rot, nbytes, axes, counts = 0, 8, 1, None
-    if freq is not None:
-        _check_vec("freq", freq, freq.numel(), (torch.float64,))
-        rot = 2 * freq.numel()
-        axes = 1 if sections is None else len(sections)
-        if positions.dtype not in (torch.int32, torch.int64) or not positions.is_contiguous() or \
-                tuple(positions.shape) not in ((T, axes), (T,) if axes == 1 else (T, axes)):
-            raise ValueError(f"positions: contiguous int32 or int64 {(T, axes)} required, got {positions.dtype} "
-                             f"{tuple(positions.shape)}")
-        nbytes = positions.element_size()
-        if sections is not None:
-            counts = (ctypes.c_int64 * axes)(*sections)
-    return (wt, _lib.HEAD_NORM[norm], eps, rot, _ptr(positions), nbytes, axes, counts, _ptr(freq), int(adjacent))
+    pairs = freq.numel()
+    _check_vec("freq", freq, pairs, (torch.float64,))
+    axes, counts = 1, None
+    if sections is not None:
+        axes = len(sections)
+        counts = (ctypes.c_int64 * axes)(*sections)
+    shape = positions.shape
+    if positions.dtype not in (torch.int64, torch.int32) or not positions.is_contiguous() or \
+            not (shape == (T, axes) or (axes == 1 and shape == (T,))):
+        raise ValueError(f"positions: contiguous int32 or int64 {(T, axes)} required, got {positions.dtype} {tuple(shape)}")
+    if positions.get_device() != dev or freq.get_device() != dev:
+        raise ValueError(f"positions on {positions.device}, freq on {freq.device}: expected cuda:{dev}")
+    return (wt, _lib.HEAD_NORM[norm], eps, 2 * pairs, positions.data_ptr(), 8 if positions.dtype == torch.int64 else 4, axes,
+            counts, freq.data_ptr(), 1 if adjacent else 0)
 
 
-def _head_outputs(out, q, k, stream):
-    given = out if out is not None else (None, None)
-    made = []
-    for name, t, o in (("q", q, given[0]), ("k", k, given[1])):
-        if t is None or o is None:
-            made.append(None if t is None else _empty(t.shape, t.dtype, t.device, stream))
-            continue
-        _check_heads(f"out ({name})", o, t)
-        _same_device(t.device, out=o)
-        made.append(o)
-    return made
+def _head_output(name, given, like, index, shape, stream):
+    """The set's output (a new contiguous tensor unless one is given) and its strides."""
+    if given is not None:
+        return given, _check_heads(name, given, like.dtype, index, *shape)
+    if stream is None:      # the shorter call
+        made = torch.empty_like(like, memory_format=torch.contiguous_format)
+    else:
+        made = _empty(shape, like.dtype, like.device, stream)
+    return made, (shape[1] * shape[2], shape[2])
 
 
 def head_norm_rotary(q: torch.Tensor, k, positions=None, freq=None, *, q_weight=None, k_weight=None, norm="rms",
@@ -929,17 +950,22 @@ def head_norm_rotary(q: torch.Tensor, k, positions=None, freq=None, *, q_weight=
     Returns (q_out, k_out), None for a set that is None.
     """
     lib = _lib.load_library()
-    first = _head_sets(q, k)
-    args = _head_arguments(first, dict(q_weight=q_weight, k_weight=k_weight), norm, eps, positions, freq, sections, adjacent)
-    _same_device(first.device, q=q, k=k)
-    made = _head_outputs(out, q, k, stream)
-    sets = []
-    for t, w, o in ((q, q_weight, made[0]), (k, k_weight, made[1])):
-        sets.append(None if t is None else ctypes.byref(
-            _lib.Heads(_ptr(t), t.shape[1], t.stride(0), t.stride(1), _ptr(w), _ptr(o), o.stride(0), o.stride(1))))
-    st = lib.fp8_head_norm_rotary(first.shape[0], first.shape[2], _is_fp32(first), *sets, *args, _stream(stream))
+    dtype, dev, T, dim, _ = _first_heads(q, k)
+    args = _head_arguments(dev, T, dim, q_weight, k_weight, norm, eps, positions, freq, sections, adjacent)
+    given = (None, None) if out is None else out
+    made, sets = [None, None], [None, None]
+    for i, t, w in ((0, q, q_weight), (1, k, k_weight)):
+        if t is None:
+            continue
+        name = "qk"[i]
+        strides, heads = _check_heads(name, t, dtype, dev, T, None, dim), t.shape[1]
+        o, to = _head_output("out: " + name, given[i], t, dev, (T, heads, dim), stream)
+        made[i] = o
+        sets[i] = _lib.Heads(t.data_ptr(), heads, strides[0], strides[1], _ptr(w), o.data_ptr(), to[0], to[1])
+    st = lib.fp8_head_norm_rotary(T, dim, _lib.OUT_FP32 if dtype == torch.float32 else _lib.OUT_BF16, sets[0], sets[1], *args,
+                                  _stream(stream))
     _lib.check("fp8_head_norm_rotary", st)
-    return tuple(made)
+    return made[0], made[1]
 
 
 def head_norm_rotary_backward(dq: torch.Tensor, dk, q, k, positions=None, freq=None, *, q_weight=None, k_weight=None,
@@ -953,30 +979,31 @@ def head_norm_rotary_backward(dq: torch.Tensor, dk, q, k, positions=None, freq=N
     optional (dq_in, dk_in) tensors.
     """
     lib = _lib.load_library()
-    first = _head_sets(dq, dk)
-    args = _head_arguments(first, dict(q_weight=q_weight, k_weight=k_weight), norm, eps, positions, freq, sections, adjacent)
-    _same_device(first.device, dq=dq, dk=dk, q=q, k=k)
-    made = _head_outputs(out, dq, dk, stream)
-    T, _, dim = first.shape
-    sets, grads, heads = [], [], []
-    for name, d, x, w, o in (("q", dq, q, q_weight, made[0]), ("k", dk, k, k_weight, made[1])):
-        heads.append(0 if d is None else d.shape[1])
+    dtype, dev, T, dim, device = _first_heads(dq, dk)
+    args = _head_arguments(dev, T, dim, q_weight, k_weight, norm, eps, positions, freq, sections, adjacent)
+    given = (None, None) if out is None else out
+    made, sets, grads, count = [None, None], [None, None], [None, None], [0, 0]
+    for i, d, x, w in ((0, dq, q, q_weight), (1, dk, k, k_weight)):
         if d is None:
-            sets.append(None)
-            grads.append(None)
             continue
-        if norm is not None:
-            if x is None:
-                raise ValueError(f"{name}: required with a norm")
-            _check_heads(name, x, d)
-        else:
+        name = "qk"[i]
+        strides, heads = _check_heads("d" + name, d, dtype, dev, T, None, dim), d.shape[1]
+        count[i] = heads
+        of = strides
+        if norm is None:
             x = d
-        dw = None if norm is None else _empty(dim, torch.float32, d.device, stream)
-        grads.append(dw)
-        sets.append(ctypes.byref(_lib.HeadsGrad(_ptr(x), d.shape[1], x.stride(0), x.stride(1), _ptr(w), _ptr(d), d.stride(0),
-                                                d.stride(1), _ptr(o), o.stride(0), o.stride(1), _ptr(dw))))
-    nbytes = 0 if norm is None else lib.fp8_head_norm_rotary_backward_workspace(T, *heads, dim)
-    ws = _workspace(nbytes, first.device, stream)
-    st = lib.fp8_head_norm_rotary_backward(T, dim, _is_fp32(first), *sets, *args, _ptr(ws), nbytes, _stream(stream))
+        elif x is None:
+            raise ValueError(f"{name}: required with a norm")
+        else:
+            of = _check_heads(name, x, dtype, dev, T, heads, dim)
+            grads[i] = _empty(dim, torch.float32, device, stream)
+        o, to = _head_output("out: d" + name, given[i], d, dev, (T, heads, dim), stream)
+        made[i] = o
+        sets[i] = _lib.HeadsGrad(x.data_ptr(), heads, of[0], of[1], _ptr(w), d.data_ptr(), strides[0], strides[1], o.data_ptr(),
+                                 to[0], to[1], _ptr(grads[i]))
+    nbytes = 0 if norm is None else _heads_workspace(T, count[0], count[1], dim)
+    ws = _workspace(nbytes, device, stream) if nbytes != 0 else None
+    st = lib.fp8_head_norm_rotary_backward(T, dim, _lib.OUT_FP32 if dtype == torch.float32 else _lib.OUT_BF16, sets[0], sets[1],
+                                           *args, _ptr(ws), nbytes, _stream(stream))
     _lib.check("fp8_head_norm_rotary_backward", st)
-    return (*made, *grads)
+    return made[0], made[1], grads[0], grads[1]

@@ -14,8 +14,13 @@ from test_binding_cpu import Recorder, bf16, codes, scales
 
 @pytest.fixture
 def rec(monkeypatch):
-    monkeypatch.setattr(ops, "_check_heads", lambda *a, **k: None)
-    return Recorder(monkeypatch)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True, raising=False)     # the stand-ins pass as device tensors
+    monkeypatch.setattr(ops, "_on_current_device", lambda *a: None)
+    ops._gated_workspace.cache_clear()
+    ops._heads_workspace.cache_clear()
+    yield Recorder(monkeypatch)
+    ops._gated_workspace.cache_clear()
+    ops._heads_workspace.cache_clear()
 
 
 ROTARY = dict(positions=torch.arange(4), freq=torch.ones(32, dtype=torch.float64))
@@ -38,8 +43,8 @@ def addresses(args):
     for a in args:
         if isinstance(a, int):
             yield a
-        elif hasattr(a, "_obj"):
-            yield from (getattr(a._obj, n) for n, t in a._obj._fields_ if t is ctypes.c_void_p)
+        elif isinstance(a, ctypes.Structure):
+            yield from (getattr(a, n) for n, t in a._fields_ if t is ctypes.c_void_p)
 
 
 @pytest.mark.parametrize("name", CALLS)
