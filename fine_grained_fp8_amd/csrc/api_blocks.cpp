@@ -325,7 +325,7 @@ fp8_status fp8_head_norm_rotary(int64_t tokens, int64_t dim, fp8_out_dtype x_dty
 
 int64_t fp8_head_norm_rotary_backward_workspace(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim) {
   if (!head_sizes(tokens, q_heads, k_heads, dim) || !head_limits(tokens, q_heads, k_heads, dim)) return -1;
-  return fp8bs::head_grad_parts(tokens, q_heads, k_heads, dim) * 2 * dim * 4;
+  return fp8bs::head_grad_parts(tokens, q_heads, k_heads, dim) * dim * 4;
 }
 
 fp8_status fp8_head_norm_rotary_backward(int64_t tokens, int64_t dim, fp8_out_dtype x_dtype, const fp8_heads_grad* q,

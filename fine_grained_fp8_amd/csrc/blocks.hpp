@@ -83,11 +83,11 @@ struct HeadProblem {
   const void* positions;           // int32 or int64 [T][axes]
   const double* freq;              // [rot / 2] or null (rot == 0)
   HeadSet set[2];                  // queries, keys (heads == 0: none)
-  float* partial;                  // backward: [head_grad_parts][2][dim]
+  float* partial;                  // backward: [head_grad_parts][dim]
 };
 enum HeadNorm { kHeadNone = 0, kHeadRms = 1, kHeadLayer = 2 };
 hipError_t launch_head_norm_rotary(const HeadProblem& p, hipStream_t stream);
-// workgroups of the backward pass, each with its share of the weights' gradients
+// workgroups of the backward pass at most, each with its share of a weight's gradient
 int64_t head_grad_parts(int64_t T, int64_t q_heads, int64_t k_heads, int64_t dim);
 hipError_t launch_head_norm_rotary_backward(const HeadProblem& p, hipStream_t stream);
 
