@@ -467,17 +467,19 @@ __device__ __forceinline__ float tile_scale_f32(uint32_t amax_bits, ScaleInverse
 }
 __device__ __forceinline__ float quotient(float y, const ScaleInverse& i) { return __builtin_fmaf(y, i.r, y * i.l); }
 
-constexpr int kGB = 512, kGW = kGB / 64;   // threads and waves of a workgroup
-constexpr int kGR = 4;                     // rows of a lane
-
 // One 128 x 128 block of tokens x channels: dh, gate and up are read once, da
 // and du (and h) stay in registers as FP32 for both orientations' codes.  Lane
-// (sub, l16) of wave w has rows 16 w + 4 sub .. + 3 and channels 8 l16 .. + 7, so
-// that a row tile is one 16-lane DPP row, and four codes of a column one
-// dword; the columns' maxima and the transposed codes meet in LDS.  Tokens past
-// the last one are zeros, which the transposed codes are padded with.
-template <bool kH>
-__global__ __launch_bounds__(kGB) void gated_backward_kernel(GatedGradProblem p) {
+// (sub, l16) of wave w has kGR consecutive rows and channels 8 l16 .. + 7, so that a row
+// tile is one 16-lane DPP row and a column's codes are packed in the lane; the
+// columns' maxima and the transposed codes meet in LDS.  Tokens past the last one are
+// zeros, which the transposed codes are padded with.
+// Bound by memory with the vector unit close behind: 4096 x 18432, 755 MB, 170 us (4.4
+// TB/s; BF16 gradients alone 140).  The registers decide: at most 128 let two workgroups
+// of 512 lanes share a CU (left to the compiler, 131: one, 222 us); with h three
+// sets of values need 1024 lanes of two rows (242 us; four rows: 342 with spills).
+template <bool kH, int kGR, int kWavesPerSimd>
+__global__ __launch_bounds__(2048 / kGR, kWavesPerSimd) void gated_backward_kernel(GatedGradProblem p) {
+  constexpr int kGW = 32 / kGR, kGB = kGW * 64;              // waves and threads: kGR rows a lane
   constexpr int kSets = kH ? 3 : 2;                          // da, du, h
   __shared__ uint32_t most[kSets][kGW][128];
   __shared__ __attribute__((aligned(16))) float inv[kSets][2][128];
@@ -486,7 +488,7 @@ __global__ __launch_bounds__(kGB) void gated_backward_kernel(GatedGradProblem p)
   const int sub = lane >> 4, l16 = lane & 15;
   const int64_t ncb = p.I / 128, nrb = (p.T + 127) / 128;
   const int64_t rb = blockIdx.x / ncb, cb = blockIdx.x % ncb;
-  const int64_t r0 = rb * 128 + wave * 16 + sub * 4, c0 = cb * 128 + l16 * 8;
+  const int64_t r0 = rb * 128 + wave * 4 * kGR + sub * kGR, c0 = cb * 128 + l16 * 8;
 
   float y[kSets][kGR][8];
   {
@@ -593,13 +595,21 @@ __global__ __launch_bounds__(kGB) void gated_backward_kernel(GatedGradProblem p)
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const ScaleInverse v{r[k], l[k]};
-      float q[4];
+      float q[kGR];
 #pragma unroll
       for (int i = 0; i < kGR; ++i) q[i] = quotient(y[m][i][k], v);
+      // row 4 kGR wave + kGR sub of the column's 128: 16-byte chunk, place in it
+      const int row = wave * 4 * kGR + sub * kGR;
+      uint8_t* at = &codes[m][(l16 * 8 + k) * 128 + (((row >> 4) ^ (l16 & 7)) << 4) + (row & 15)];
       int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
-      w = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
-      if (!(r[k] > 0.0f)) w = (int)pack4_sat_nan(q[0], q[1], q[2], q[3]);   // an infinite or NaN scale
-      *reinterpret_cast<uint32_t*>(&codes[m][(l16 * 8 + k) * 128 + ((wave ^ (l16 & 7)) << 4) + sub * 4]) = (uint32_t)w;
+      if constexpr (kGR == 4) {
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
+        if (!(r[k] > 0.0f)) w = (int)pack4_sat_nan(q[0], q[1], q[2], q[3]);   // an infinite or NaN scale
+        *reinterpret_cast<uint32_t*>(at) = (uint32_t)w;
+      } else {
+        if (!(r[k] > 0.0f)) w = (int)pack4_sat_nan(q[0], q[1], 0.f, 0.f);
+        *reinterpret_cast<uint16_t*>(at) = (uint16_t)w;
+      }
     }
   }
   __syncthreads();
@@ -607,7 +617,7 @@ __global__ __launch_bounds__(kGB) void gated_backward_kernel(GatedGradProblem p)
   for (int m = 0; m < 2; ++m) {
     if (p.qt == nullptr) break;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 1024 / kGB; ++i) {
       const int at = i * kGB + threadIdx.x, c = at >> 3, ch = at & 7;
       const gv4i v = *reinterpret_cast<const gv4i*>(&codes[m][c * 128 + ((ch ^ ((c >> 3) & 7)) << 4)]);
       __builtin_nontemporal_store(v, reinterpret_cast<gv4i*>(p.qt + (m * p.I + cb * 128 + c) * p.ldqt + rb * 128 + ch * 16));
@@ -616,7 +626,7 @@ __global__ __launch_bounds__(kGB) void gated_backward_kernel(GatedGradProblem p)
   if constexpr (kH) {
     // operand tiles: 16 columns x 128 tokens are 2 KB, lane 16 g + c of half h: tokens 64 h + 16 g ..
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 1024 / kGB; ++i) {
       const int at = i * kGB + threadIdx.x, c = (at >> 7) * 16 + (at & 15), ch = (at >> 4) & 7;
       const gv4i v = *reinterpret_cast<const gv4i*>(&codes[2][c * 128 + ((ch ^ ((c >> 3) & 7)) << 4)]);
       uint8_t* tile = p.ht + ((cb * 8 + (at >> 7)) * nrb + rb) * 2048;
@@ -658,8 +668,8 @@ hipError_t launch_gated_few(const GatedFewProblem& p, hipStream_t stream) {
 
 hipError_t launch_gated_backward(const GatedGradProblem& p, hipStream_t stream) {
   const dim3 grid((unsigned)((p.T + 127) / 128 * (p.I / 128)));
-  if (p.ht != nullptr) hipLaunchKernelGGL(gated_backward_kernel<true>, grid, dim3(kGB), 0, stream, p);
-  else hipLaunchKernelGGL(gated_backward_kernel<false>, grid, dim3(kGB), 0, stream, p);
+  if (p.ht != nullptr) hipLaunchKernelGGL((gated_backward_kernel<true, 2, 4>), grid, dim3(1024), 0, stream, p);
+  else hipLaunchKernelGGL((gated_backward_kernel<false, 4, 4>), grid, dim3(512), 0, stream, p);
   return hipGetLastError();
 }
 
