@@ -142,9 +142,8 @@ extern "C" {
 
 int64_t fp8_block_gemm_gated_workspace(int64_t M, int64_t I, int64_t K) {
   if (gated_shape(M, I, K) != FP8_OK) return -1;
-  if (M > fp8bs::kGatedFewTokens) return 0;
   const int64_t cuts = fp8bs::gated_few_cuts(M, I, K);
-  return (cuts > 1 ? 2 * cuts : 1) * M * I * 4;
+  return (cuts > 1 ? 2 * cuts : cuts) * M * I * 4;
 }
 
 fp8_status fp8_block_gemm_gated(int64_t M, int64_t I, int64_t K, const uint8_t* A, int64_t lda, const float* sA,
@@ -190,14 +189,14 @@ fp8_status fp8_block_gemm_gated(int64_t M, int64_t I, int64_t K, const uint8_t* 
   ge.gate_up = static_cast<uint16_t*>(gate_up);
   ge.ld_gu = ld_gu;
   ge.q = q; ge.ldq = ldq; ge.s = scales; ge.ld_s = ld_s;
-  if (M <= fp8bs::kGatedFewTokens) {
+  if (const int cuts = fp8bs::gated_few_cuts(M, I, K); cuts > 0) {
     fp8bs::GatedFewProblem p{};
     p.M = static_cast<int>(M); p.N = I; p.K = K;
     p.A = A; p.lda = lda; p.sA = sA; p.ld_sa = ld_sa;
     p.W = W13; p.sW = s13; p.ld_sw = ld_s13;
     p.C = h; p.ldc = ldh; p.out_fp32 = e == 4;
     p.gated = ge;
-    p.cuts = fp8bs::gated_few_cuts(M, I, K);
+    p.cuts = cuts;
     p.parts = static_cast<float*>(workspace);
     return launched(fp8bs::launch_gated_few(p, s));
   }

@@ -12,10 +12,10 @@
 
 namespace fp8bs {
 
-// ---- the gated product for up to kGatedFewTokens tokens ----
-constexpr int kGatedFewTokens = 64;
+// ---- the gated product for few tokens ----
+constexpr int kGatedExactTokens = 64;    // up to so many: FP32 values and codes from exact products
 constexpr int kGatedMaxCuts = 8;
-// Workgroups that share the K blocks of a tile of channels
+// Workgroups that share the K blocks of a tile of channels; 0: the block GEMM is faster
 int gated_few_cuts(int64_t M, int64_t N, int64_t K);
 struct GatedFewProblem {
   int M;

@@ -1,6 +1,6 @@
-// The gated feed-forward block's own kernels for gfx950: the product for up to
-// 64 tokens, and the backward pass up to the operands of Dgrad and Wgrad.
-// (More tokens: the block GEMM with its gated epilogue, gemm.hip.)
+// The gated feed-forward block's own kernels for gfx950: the product for few tokens,
+// and the backward pass up to the operands of Dgrad and Wgrad.  (More tokens: the
+// block GEMM with its gated epilogue, gemm.hip.)
 //
 //   a = X W1^T, u = X W3^T,  h = act(a) u,  act(a) = a logistic(v(a))
 //   da = dh u act'(a),  du = dh act(a)
@@ -199,9 +199,10 @@ __global__ __launch_bounds__(kRowWaves * 64) void gated_row_kernel(GatedFewProbl
   }
 }
 
-// 17 to 64 tokens (NT groups of 16).  A wave has RT tiles of 16 channels, the gate
-// rows and the up rows of each, for every token; a workgroup's four waves have
-// neighbouring tiles, and `cuts` workgroups share the K blocks.  Weights go from memory straight into MFMA operand
+// From 17 tokens, in blocks of 16 NT, to where the block GEMM takes over.  A wave has RT
+// tiles of 16 channels, the gate rows and the up rows of each, for every token of its
+// block; a workgroup's four waves have neighbouring tiles, and `cuts` workgroups share
+// the K blocks.  Weights go from memory straight into MFMA operand
 // registers; the token codes, which the waves share, through LDS by DMA.  Both are
 // asked for D blocks ahead, in the order they are needed (loads return in the
 // order of their issue); one barrier a block.  Measured against the waves dealing the
@@ -210,7 +211,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void gated_row_kernel(GatedFewProbl
 // waves), 48 tokens, 7168 x 2048 14.3 for 15.6, 64 tokens, 2048 x 1408 10.4 for 10.0; one
 // token, 7168 x 2048 11.8 for 9.8.  kExact: products of the codes as BF16, exact with FP32
 // sums, so that FP32 values, scales and codes do not move with the FP8 instruction's
-// truncation (64 tokens, 7168 x 18432: 70 us for 58).
+// truncation (up to 64 tokens; 64 of them, 7168 x 18432: 70 us for 58).
 template <int NT, int RT, int D, bool kExact>
 __global__ __launch_bounds__(256) void gated_few_kernel(GatedFewProblem p) {
   constexpr int kTokens = NT * 2048, kStage = kTokens + 256 + 4 * 256;   // codes, token scales, each wave's two weight scales
@@ -220,11 +221,15 @@ __global__ __launch_bounds__(256) void gated_few_kernel(GatedFewProblem p) {
   using lds_ptr = __attribute__((address_space(3))) void*;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lrow = lane & 15, lgrp = lane >> 4;
-  const int kb_n = (int)(p.K / 128), M = p.M, tiles = (int)(p.N / 16);
-  const int cut = blockIdx.x % p.cuts, t0 = (blockIdx.x / p.cuts * 4 + wave) * RT;   // the wave's first tile
+  const int kb_n = (int)(p.K / 128), tiles = (int)(p.N / 16);
+  // workgroups of the same tiles follow each other: the token blocks, and for each the cuts
+  const int blocks = (p.M + NT * 16 - 1) / (NT * 16);
+  const int cut = blockIdx.x % p.cuts, block = blockIdx.x / p.cuts % blocks;
+  const int t0 = (blockIdx.x / p.cuts / blocks * 4 + wave) * RT;                     // the wave's first tile
+  const int m0 = block * NT * 16, M = min(p.M - m0, NT * 16);
   const int kb0 = (int)((int64_t)kb_n * cut / p.cuts), n = (int)((int64_t)kb_n * (cut + 1) / p.cuts) - kb0;
   // buffers end behind the last token and the last scale: what lies past them reads as zero
-  const __amdgpu_buffer_rsrc_t rsrc_x = __builtin_amdgcn_make_buffer_rsrc((void*)p.A, (short)0, (int)((M - 1) * p.lda + p.K), 0x00020000);
+  const __amdgpu_buffer_rsrc_t rsrc_x = __builtin_amdgcn_make_buffer_rsrc((void*)(p.A + m0 * p.lda), (short)0, (int)((M - 1) * p.lda + p.K), 0x00020000);
   const __amdgpu_buffer_rsrc_t rsrc_s =
       __builtin_amdgcn_make_buffer_rsrc((void*)p.sW, (short)0, (int)(2 * (p.N / 128) * p.ld_sw * 4), 0x00020000);
   // DMA instruction o of a block: rows 8 o .. + 7, 128 bytes each, 16-byte chunks XOR-swizzled by row & 7
@@ -246,7 +251,7 @@ __global__ __launch_bounds__(256) void gated_few_kernel(GatedFewProblem p) {
       const uint32_t at = x_off + (uint32_t)(kb * 128 + o * 8 * (int)p.lda);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc_x, (lds_ptr)(st + o * 1024), 16, at, 0, 0, 0);
     }
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)(p.sA + (int64_t)kb * p.ld_sa), (short)0, M * 4, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)(p.sA + (int64_t)kb * p.ld_sa + m0), (short)0, M * 4, 0x00020000);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(st + kTokens), 4, (uint32_t)lane * 4u, 0, 0, 0);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc_s, (lds_ptr)(st + kTokens + 256 + wave * 256), 4, s_off + (uint32_t)kb * 4u, 0, 0, 0);
     __asm__ volatile("" ::: "memory");
@@ -337,12 +342,62 @@ __global__ __launch_bounds__(256) void gated_few_kernel(GatedFewProblem p) {
   for (int d = 0; d < D - 1; ++d)
     if (k + d < n) step(k + d, b[d]);
   wait_loads<0>();     // the loads asked for again land before the workgroup's LDS goes
+  if constexpr (RT == 2) {
+    if (p.gated.q != nullptr && p.cuts == 1) {
+      // the workgroup has whole 1x128 tiles: their maxima over the waves, the codes
+      // through LDS into whole rows
+      __syncthreads();
+      uint32_t* most = reinterpret_cast<uint32_t*>(lds + NT * 2048);      // [wave][16 NT]
+      float h[NT][8];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          h[j][v] = gated(acc[v >> 2][0][j][v & 3], acc[v >> 2][1][j][v & 3], p.gated.gelu);
+          m = max(m, __float_as_uint(h[j][v]) & 0x7FFFFFFFu);
+        }
+        const auto a = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+        m = max(a[0], a[1]);
+        const auto c = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+        m = max(c[0], c[1]);
+        if (lgrp == 0) most[wave * NT * 16 + j * 16 + lrow] = m;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int t = j * 16 + lrow;
+        const uint32_t m = max(max(most[t], most[NT * 16 + t]), max(most[2 * NT * 16 + t], most[3 * NT * 16 + t]));
+        float sc;
+        const uint2 q = quant8_f32(h[j], m, sc);
+        uint8_t* row = lds + t * 128 + lgrp * 4;
+        *reinterpret_cast<uint32_t*>(row + (((wave * 2) ^ (t & 7)) << 4)) = q.x;
+        *reinterpret_cast<uint32_t*>(row + (((wave * 2 + 1) ^ (t & 7)) << 4)) = q.y;
+        if (wave == 0 && lgrp == 0 && t < M) p.gated.s[(t0 / 8) * p.gated.ld_s + m0 + t] = sc;
+        if (p.gated.gate_up != nullptr && t < M) {
+          uint16_t* at = p.gated.gate_up + (m0 + t) * p.gated.ld_gu + t0 * 16 + lgrp * 4;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            *reinterpret_cast<v4bf*>(at + i * 16) = __builtin_convertvector(acc[i][0][j], v4bf);
+            *reinterpret_cast<v4bf*>(at + p.N + i * 16) = __builtin_convertvector(acc[i][1][j], v4bf);
+          }
+        }
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < M * 8; i += 256) {
+        const int t = i >> 3, ch = i & 7;
+        *reinterpret_cast<gv4i*>(p.gated.q + (m0 + t) * p.gated.ldq + (t0 / 8) * 128 + ch * 16) =
+            *reinterpret_cast<const gv4i*>(lds + t * 128 + ((ch ^ (t & 7)) << 4));
+      }
+      return;
+    }
+  }
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int t = j * 16 + lrow;
     if (t >= M) continue;
 #pragma unroll
-    for (int i = 0; i < RT; ++i) leave(p, cut, t, (int64_t)(t0 + i) * 16 + lgrp * 4, acc[i][0][j], acc[i][1][j]);
+    for (int i = 0; i < RT; ++i) leave(p, cut, m0 + t, (int64_t)(t0 + i) * 16 + lgrp * 4, acc[i][0][j], acc[i][1][j]);
   }
 }
 
@@ -435,13 +490,23 @@ hipError_t row(const GatedFewProblem& p, hipStream_t stream) {
 
 template <int NT, int RT, int D, bool kExact>
 hipError_t few(const GatedFewProblem& p, hipStream_t stream) {
-  return start<gated_few_kernel<NT, RT, D, kExact>>(p.N / (64 * RT) * p.cuts, 256, (D + 1) * (NT * 2048 + 1280), p, stream);
+  const int64_t blocks = (p.M + NT * 16 - 1) / (NT * 16);
+  return start<gated_few_kernel<NT, RT, D, kExact>>(p.N / (64 * RT) * blocks * p.cuts, 256, (D + 1) * (NT * 2048 + 1280), p, stream);
+}
+// FP32 results and codes of up to 64 tokens
+bool exact_products(const GatedFewProblem& p) {
+  return p.M <= kGatedExactTokens && (p.gated.q != nullptr || p.out_fp32);
+}
+// 64 or 128 channels a workgroup: 128 where 64 give more workgroups than CUs (64 tokens,
+// 7168 x 18432: 58 us for 67; 1333 tokens, 2048 x 1408: 17.4 for 18.4; 512 tokens, 7168 x
+// 2048, 256 workgroups: 49 for 35)
+bool whole_tiles(const GatedFewProblem& p) {
+  return p.M > 16 && !exact_products(p) && (p.M + 63) / 64 * (p.N / 64) > 256;
 }
 template <int NT>
 hipError_t few_tokens(const GatedFewProblem& p, hipStream_t stream) {
-  // FP32 results and codes: exact products
-  if (p.gated.q != nullptr || p.out_fp32) return few<NT, 1, 3, true>(p, stream);
-  if (p.N / 64 >= 256) return few<NT, 2, 2, false>(p, stream);
+  if (exact_products(p)) return few<NT, 1, 3, true>(p, stream);
+  if (whole_tiles(p)) return few<NT, 2, 2, false>(p, stream);
   return few<NT, 1, 3, false>(p, stream);
 }
 
@@ -637,10 +702,20 @@ __global__ __launch_bounds__(2048 / kGR, kWavesPerSimd) void gated_backward_kern
 
 }  // namespace
 
+// Which kernel.  The block GEMM's tiles are 128 tokens x 128 channels, one a CU: with
+// few of them most CUs idle, and workgroups of up to 64 tokens and 64 or 128 channels are
+// faster.  Measured, us, GEMM / these: 128 tokens, 7168 x 2048 (16 tiles) 55 / 17; 300, 2048 x
+// 1408 (33) 19 / 11; 512, 7168 x 2048 (64) 53 / 35; 1333, 2048 x 1408 (121) 20 / 17; 1024, 7168 x
+// 2048 (128) 52 / 50; 256, 2048 x 8192 (128) 21 / 24; 65, 7168 x 18432 (144) 66 / 86; 512, 7168 x
+// 7168 (224) 62 / 113.
+// K is cut so that every CU has a workgroup; a cut adds partial sums and the
+// finishing launch, about what 6 to 8 blocks of K take: 48 tokens, 7168 x 2048, with 1 / 2
+// / 4 / 8 cuts 26 / 18 / 15 / 14; 256 tokens 29 / 24 / 24 / 30; 300 tokens, 2048 x 1408 11 / 14 / 18.
 int gated_few_cuts(int64_t M, int64_t N, int64_t K) {
   const int64_t kb = K / 128;
   if (M <= 16) return (int)((kb + kMaxLds / kRowBlockLds - 1) / (kMaxLds / kRowBlockLds));
-  const int64_t groups = N / 64, most = kb / 4 < kGatedMaxCuts ? kb / 4 : kGatedMaxCuts;
+  if (M > 64 && (M + 127) / 128 * (N / 128) >= 128) return 0;
+  const int64_t groups = (M + 63) / 64 * (N / 64), most = (kb - 8) / 6 < kGatedMaxCuts ? (kb - 8) / 6 : kGatedMaxCuts;
   const int64_t c = 256 / groups < most ? 256 / groups : most;
   return (int)(c > 1 ? c : 1);
 }
@@ -659,8 +734,9 @@ hipError_t launch_gated_few(const GatedFewProblem& p, hipStream_t stream) {
     e = p.M <= 32 ? few_tokens<2>(p, stream) : p.M <= 48 ? few_tokens<3>(p, stream) : few_tokens<4>(p, stream);
   }
   if (e != hipSuccess) return e;
-  if (p.cuts > 1 || p.gated.q != nullptr) {
-    const int64_t groups = p.M * (p.N / 128);
+  // sums of cut tiles; codes of tiles that no workgroup has whole
+  if (p.cuts > 1 || (p.gated.q != nullptr && !whole_tiles(p))) {
+    const int64_t groups = (int64_t)p.M * (p.N / 128);
     hipLaunchKernelGGL(gated_finish_kernel, dim3((unsigned)((groups + 15) / 16)), dim3(256), 0, stream, p);
   }
   return hipGetLastError();

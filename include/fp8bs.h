@@ -572,10 +572,11 @@ int64_t fp8_adapter_linear_workspace(int64_t T, int64_t N, int64_t K, int32_t ra
  *          (FP8_ERR_NULL, FP8_ERR_UNSUPPORTED).
  *  gate_up optional BF16 [M][ld_gu >= 2 I]: a, then u (the backward pass reads it)
  *  Any M; K % 128 == 0, I % 128 == 0; limits and alignment as for fp8_block_gemm, and
- *  (I + 128) K < 2^31.  Up to 64 rows run on a kernel of their own that is bound
- *  by reading W13; more on the block GEMM's persistent kernel (with its
- *  per-stream workspace, but while the stream is being captured).  M == 0 is a
- *  no-op.
+ *  (I + 128) K < 2^31.  Few rows run on kernels of their own; more on the block
+ *  GEMM's persistent kernel (with its per-stream workspace, but while the stream
+ *  is being captured).  With up to 16 rows, and with up to 64 where h is FP32 or
+ *  codes, the products are exact; otherwise they are the FP8 matrix
+ *  instruction's.  M == 0 is a no-op.
  */
 typedef enum { FP8_ACT_SILU = 0, FP8_ACT_GELU = 1 } fp8_activation;
 fp8_status fp8_block_gemm_gated(int64_t M, int64_t I, int64_t K, const uint8_t* A, int64_t lda, const float* sA,

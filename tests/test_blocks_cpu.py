@@ -43,12 +43,12 @@ def gated(lib, **c):
     return call(lib.fp8_block_gemm_gated, GATED, base, c)
 
 
-@pytest.mark.parametrize("M", [8, 200])
+@pytest.mark.parametrize("M", [8, 200, 16384])
 def test_gated_validation(lib, M):
     def g(**c):
-        return gated(lib, **{"M": M, "ld_sa": M, "ld_s": M, **c})
+        return gated(lib, **{"M": M, "ld_sa": M, "ld_s": M, "ws": P[9], **c})
     f = lib.fp8_block_gemm_gated_workspace
-    assert f(8, 256, 384) > 0 and f(200, 256, 384) == 0 and f(8, 200, 384) == -1 and f(-1, 256, 384) == -1
+    assert f(8, 256, 384) > 0 and f(5000, 2048, 384) == 0 and f(8, 200, 384) == -1 and f(-1, 256, 384) == -1
     assert g() in PASSED and g(gu=None) in PASSED and g(ht=1) in PASSED and g(act=1) in PASSED
     codes = dict(h=None, q=P[6], s=P[7])
     assert g(**codes) in PASSED and g(**codes, gu=None) in PASSED
@@ -72,8 +72,8 @@ def test_gated_validation(lib, M):
     for k, v in (("h", P[0]), ("h", P[1]), ("h", P[2] + 4096), ("gu", P[3]), ("gu", P[4] + 256)):
         assert g(**{k: v}) == ALIAS, (k, v)
     assert g(**{**codes, "q": P[5]}) == ALIAS and g(**{**codes, "s": P[6]}) == ALIAS and g(**{**codes, "s": P[1]}) == ALIAS
-    if M <= 64:
-        assert g(ws=None) == NULL and g(bytes=64) == SHAPE and g(ws=P[8] + 4) == ALIGN
+    if f(M, 256, 384) > 0:
+        assert g(ws=None) == NULL and g(bytes=64) == SHAPE and g(ws=P[9] + 4) == ALIGN
         assert g(ws=P[0]) == ALIAS and g(ws=P[4]) == ALIAS
     else:
         assert g(ws=None, bytes=0) in PASSED

@@ -96,7 +96,7 @@ GATED = [  # M, K, I, kind
     (1, 128, 128, "silu"), (1, 1024, 384, "gelu"), (2, 256, 1408, "silu"), (15, 384, 256, "gelu"), (16, 128, 2048, "silu"),
     (17, 2048, 128, "silu"), (31, 640, 512, "gelu"), (33, 256, 4224, "silu"), (48, 1024, 256, "silu"), (49, 512, 8320, "gelu"),
     (64, 128, 384, "silu"), (64, 896, 2176, "gelu"), (5, 16384, 128, "silu"), (33, 4096, 256, "gelu"), (40, 384, 16384, "silu"),
-    (65, 128, 128, "silu"), (100, 384, 256, "gelu"), (128, 512, 128, "silu"), (129, 1024, 384, "silu"), (300, 640, 1408, "gelu"),
+    (65, 4096, 128, "gelu"), (200, 8192, 256, "silu"), (1000, 256, 1920, "gelu"), (65, 128, 128, "silu"), (90, 256, 16384, "silu"), (100, 384, 256, "gelu"), (128, 512, 128, "silu"), (129, 1024, 384, "silu"), (300, 640, 1408, "gelu"),
     (1333, 256, 512, "silu"),
 ]
 
@@ -126,7 +126,7 @@ def test_block_gemm_gated(gpu_lib, case):
 
 def test_gated_split_tail_and_wide_few(gpu_lib):
     """272 tiles (16 of them cut along K on 256 CUs), and a few tokens at a wide output."""
-    for M, K, I in ((2100, 1024, 2048), (3, 7168, 2048), (20, 1024, 18432), (7, 1024, 18432)):
+    for M, K, I in ((2100, 1024, 2048), (700, 1024, 2560), (3, 7168, 2048), (20, 1024, 18432), (7, 1024, 18432)):
         g = Gated(M, K, I, "silu", seed=5)
         rows = np.unique(np.concatenate([np.arange(0, M, 97), [M - 1]]))
         y = gpu_lib.block_gemm_gated(*g.args, out_dtype=torch.float32)
