@@ -8,8 +8,9 @@
 //   dx = rstd (g - sum g / D - xhat sum(g xhat) / D)   (rms: without the second term)
 //   dw = sum over tokens and heads of d xhat
 //
-// Bound by memory: every head is read once and written once (forward 8192 tokens of 64 + 8
-// heads of 128, BF16: 57 us, 5.3 TB/s; backward 32 + 8 heads 53 + 5 us, 252 MB).  A head lives in
+// Bound by memory: every head is read once and written once (8192 tokens of 64 + 8 heads of
+// 128, BF16, nothing cached: forward 62 us, 302 MB; a copy of as much 57; without norm and
+// rotation the same).  A head lives in
 // the registers of G lanes, 8 pairs a lane: both elements of a pair meet in one
 // lane for either order of pairs, so the rotation moves nothing between lanes,
 // and the lane's eight angles serve all heads of the token.  A wave works on 64 / G
@@ -24,6 +25,7 @@ namespace {
 
 constexpr int kHB = 256, kHW = kHB / 64;   // threads and waves of a workgroup
 constexpr int kMaxGradParts = 1280;        // workgroups of the backward pass: see divide()
+constexpr int kForwardBlocks = 1280;       // and of the forward pass
 
 typedef int hv4i __attribute__((ext_vector_type(4)));
 typedef int hv2i __attribute__((ext_vector_type(2)));
@@ -36,8 +38,10 @@ struct Raw {
   int d[2 * kWords];                                      // two runs of R elements
 };
 
-// How a lane's 2 R elements of a head lie: two runs of R moved in whole accesses, its
-// pairs (k, R + k) for halves or (2 k, 2 k + 1) for adjacent pairs; or (kScalar)
+// How a lane's 2 R elements of a head lie: two runs of R, neighbouring lanes' side by side,
+// moved in whole accesses: R l .. and rot / 2 + R l .. with pairs (k, R + k) for halves (the
+// channels that do not rotate likewise as two halves), R l .. and D / 2 + R l .. with pairs
+// (2 k, 2 k + 1) for adjacent ones; or (kScalar)
 // element by element, pairs (k, R + k), for heads that are not 16-byte aligned or
 // whose size or rotated part is no multiple of 16.
 enum Mode { kHalves = 0, kAdjacent = 1, kScalar = 2 };
@@ -72,17 +76,20 @@ struct Lane {
   int adjacent;
   // element of register v (0 .. 2 R - 1); past the head's end: >= dim
   __device__ __forceinline__ int element(int v) const {
-    if constexpr (kMode == kAdjacent) return l * 2 * R + v;
+    if constexpr (kMode == kAdjacent) return (v < R ? 0 : dim / 2 - R) + l * R + v;
     if constexpr (kMode == kHalves) {
       if (R * l < half_rot) return v < R ? l * R + v : half_rot + l * R + v - R;
-      return l * 2 * R + v;
+      return 2 * half_rot + l * R - half_rot + (v < R ? v : dim / 2 - half_rot + v - R);
     }
     const int i = pair(v % R), second = v / R;
     if (2 * i >= dim) return dim;
     if (!adjacent && i < half_rot) return i + second * half_rot;
     return 2 * i + second;
   }
-  __device__ __forceinline__ int pair(int k) const { return kMode == kScalar ? k * G + l : l * R + k; }
+  __device__ __forceinline__ int pair(int k) const {
+    if constexpr (kMode == kAdjacent) return (k < R / 2 ? 0 : dim / 4 - R / 2) + l * (R / 2) + k;
+    return kMode == kScalar ? k * G + l : l * R + k;
+  }
   __device__ __forceinline__ bool on() const { return kMode == kScalar ? true : l * 2 * R < dim; }
   static __device__ __forceinline__ int first(int k) { return kMode == kAdjacent ? 2 * k : k; }
   static __device__ __forceinline__ int second(int k) { return kMode == kAdjacent ? 2 * k + 1 : R + k; }
@@ -130,13 +137,7 @@ struct Lane {
       else v[k] = (k & 1) ? bf16_hi((uint32_t)r.d[k / 2]) : bf16_lo((uint32_t)r.d[k / 2]);
     }
   }
-  template <typename T>
-  __device__ __forceinline__ void load(const T* p, float (&v)[2 * R]) const {
-    Raw<T, R> r;
-    fetch(p, r);
-    unpack(r, v);
-  }
-  template <typename T>
+  template <bool kStream, typename T>
   __device__ __forceinline__ void store(T* p, const float (&v)[2 * R]) const {
     constexpr int kWords = Raw<T, R>::kWords;
     if constexpr (kMode == kScalar) {
@@ -159,61 +160,78 @@ struct Lane {
           else d[i] = bf16_pair(v[run * R + 2 * i], v[run * R + 2 * i + 1]);
         }
         if constexpr (kWords == 2) {
-          *reinterpret_cast<hv2i*>(q) = hv2i{d[0], d[1]};
+          if constexpr (kStream) __builtin_nontemporal_store(hv2i{d[0], d[1]}, reinterpret_cast<hv2i*>(q));
+          else *reinterpret_cast<hv2i*>(q) = hv2i{d[0], d[1]};
         } else {
 #pragma unroll
-          for (int i = 0; i < kWords; i += 4)
-            *reinterpret_cast<hv4i*>(q + i * 4 / (int)sizeof(T)) = hv4i{d[i], d[i + 1], d[i + 2], d[i + 3]};
+          for (int i = 0; i < kWords; i += 4) {
+            const hv4i v = {d[i], d[i + 1], d[i + 2], d[i + 3]};
+            hv4i* at = reinterpret_cast<hv4i*>(q + i * 4 / (int)sizeof(T));
+            if constexpr (kStream) __builtin_nontemporal_store(v, at);
+            else *at = v;
+          }
         }
       }
     }
   }
 
-  // a weight vector (null: ones)
-  __device__ __forceinline__ void load_weight(const void* w, int is_f32, float (&v)[2 * R]) const {
-    if (w == nullptr) {
+  // The lane's elements of a weight in LDS.
+  __device__ __forceinline__ void weight(const float* w, float (&v)[2 * R]) const {
+    if constexpr (kMode == kScalar) {
 #pragma unroll
-      for (int k = 0; k < 2 * R; ++k) v[k] = 1.f;
-    } else if (is_f32) {
-      load(static_cast<const float*>(w), v);
+      for (int k = 0; k < 2 * R; ++k) v[k] = w[min(element(k), dim - 1)];
     } else {
-      load(static_cast<const uint16_t*>(w), v);
+#pragma unroll
+      for (int k = 0; k < 2 * R; k += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(w + (on() ? element(k) : 0));
+        v[k] = a.x; v[k + 1] = a.y; v[k + 2] = a.z; v[k + 3] = a.w;
+      }
     }
   }
 
-  // The angles of the lane's pairs at token t (pairs that do not rotate: whatever).
-  // Everything is asked for before anything is computed.
-  __device__ __forceinline__ void angles(const HeadProblem& p, int64_t t, float (&c)[R], float (&s)[R]) const {
+  // cos and sin of the lane's pairs at token t (pairs that do not rotate: whatever).  The
+  // wave's lanes form the token's angles once between them and share them through
+  // `shared` (one pair of floats for each rotated pair): each lane for itself, 64 / G
+  // times over, cost 20000 tokens of 16 + 4 heads of
+  // 64 38 us for 32 (with the walk below).
+  __device__ __forceinline__ void angles(const HeadProblem& p, int64_t t, float2* shared, float (&c)[R], float (&s)[R]) const {
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       c[k] = 1.f;
       s[k] = 0.f;
     }
     if (half_rot == 0) return;
-    double f[R], pos[R];
-#pragma unroll
-    for (int k = 0; k < R; ++k) f[k] = p.freq[min(pair(k), half_rot - 1)];
     auto position = [&](int64_t at) {
       return p.pos64 ? (double)static_cast<const int64_t*>(p.positions)[at] : (double)static_cast<const int32_t*>(p.positions)[at];
     };
-    if (p.axes == 1) {
-      pos[0] = position(t);
-#pragma unroll
-      for (int k = 1; k < R; ++k) pos[k] = pos[0];
-    } else {
-#pragma unroll
-      for (int k = 0; k < R; ++k) {
-        const int i = min(pair(k), half_rot - 1);
+    const double pos0 = p.axes == 1 ? position(t) : 0.0;
+    order();                           // the token before: its angles have been read
+    for (int i = threadIdx.x & 63; i < half_rot; i += 64) {
+      double pos = pos0;
+      if (p.axes > 1) {
         int axis = 0;
 #pragma unroll
         for (int a = 0; a + 1 < kHeadMaxAxes; ++a) axis += i >= p.section_end[a] && a + 1 < p.axes ? 1 : 0;
-        pos[k] = position(t * p.axes + axis);
+        pos = position(t * p.axes + axis);
       }
+      float2 cs;
+      rotation(pos, p.freq[i], cs.x, cs.y);
+      shared[i] = cs;
     }
+    order();
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      rotation(pos[k], f[k], c[k], s[k]);
+      const float2 cs = shared[min(pair(k), half_rot - 1)];
+      c[k] = cs.x;
+      s[k] = cs.y;
     }
+  }
+  // Within a wave LDS accesses happen in the order of its instructions: this keeps the
+  // compiler from moving them.
+  static __device__ __forceinline__ void order() {
+    __asm__ volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+    __asm__ volatile("" ::: "memory");
   }
   // rotates the pairs by the angles (kBack: against them); pairs that do not
   // rotate are left alone, infinities and NaN included
@@ -228,6 +246,15 @@ struct Lane {
 #pragma unroll
       for (int k = 0; k < R; ++k)
         if (pair(k) < half_rot) turn(k);
+    } else if constexpr (kMode == kAdjacent) {      // a run rotates or not (rot % 16 == 0)
+      if (pair(0) < half_rot) {
+#pragma unroll
+        for (int k = 0; k < R / 2; ++k) turn(k);
+      }
+      if (pair(R / 2) < half_rot) {
+#pragma unroll
+        for (int k = R / 2; k < R; ++k) turn(k);
+      }
     } else if (l * R < half_rot) {
 #pragma unroll
       for (int k = 0; k < R; ++k) turn(k);
@@ -260,120 +287,177 @@ struct Lane {
 // passes of a wave over the heads of a set, 64 / G heads each
 __host__ __device__ inline int passes(int64_t heads, int G) { return (int)((heads * G + 63) / 64); }
 
-// A wave has one token and `per` passes over its heads, queries first; blockIdx.y
-// says which share of them.
-template <typename T, int kMode, int G, int R>
-__global__ __launch_bounds__(kHB) void head_norm_rotary_kernel(HeadProblem p, int per) {
-  const int lane = threadIdx.x & 63, slot = lane / G;
-  const int64_t t = (int64_t)blockIdx.x * kHW + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (t >= p.T) return;
-  const Lane<kMode, G, R> me{lane % G, p.dim, p.rot / 2, p.adjacent};
-  const int nq = passes(p.set[0].heads, G), n = nq + passes(p.set[1].heads, G);
-  const int first = blockIdx.y * per, end = min(first + per, n);
-  float c[R], s[R];
-  me.angles(p, t, c, s);
-#pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    const HeadSet& hs = p.set[which];
-    const int from = which == 0 ? first : max(first, nq) - nq, to = which == 0 ? min(end, nq) : end - nq;
-    if (from >= to) continue;
-    const T* x = static_cast<const T*>(hs.x) + t * hs.ld_token;
-    T* y = static_cast<T*>(hs.y) + t * hs.ldy_token;
-    // past the last head: that one again, not stored
-    auto head_of = [&](int pass) { return min((int64_t)pass * (64 / G) + slot, hs.heads - 1); };
-    Raw<T, R> next;
-    me.fetch(x + head_of(from) * hs.ld_head, next);
-    float w[2 * R];
-    if (p.norm != kHeadNone) me.load_weight(hs.w, p.w_fp32, w);
-#pragma unroll 1
-    for (int pass = from; pass < to; ++pass) {
-      float v[2 * R];
-      me.unpack(next, v);
-      me.fetch(x + head_of(min(pass + 1, to - 1)) * hs.ld_head, next);
-      if (p.norm != kHeadNone) {
-        me.normalize(v, p.norm, p.eps);
-#pragma unroll
-        for (int k = 0; k < 2 * R; ++k) v[k] *= w[k];
-      }
-      me.template rotate<false>(v, c, s);
-      const int64_t h = (int64_t)pass * (64 / G) + slot;
-      if (h < hs.heads) me.store(y + h * hs.ldy_head, v);
-    }
-  }
+// A weight into LDS as FP32 (null: ones), by the workgroup; a barrier publishes it.
+__device__ __forceinline__ void stage_weight(const void* w, int is_f32, int dim, float* to) {
+  for (int e = threadIdx.x; e < dim; e += kHB)
+    to[e] = w == nullptr ? 1.f : is_f32 ? static_cast<const float*>(w)[e] : __uint_as_float((uint32_t)static_cast<const uint16_t*>(w)[e] << 16);
+}
+// Barrier that waits for LDS alone: the loads from memory stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __asm__ volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));   // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  __asm__ volatile("" ::: "memory");
 }
 
-// How the backward pass divides a set: `cuts` shares of a token's passes, `per` each,
-// and for each share `blocks` workgroups along the tokens.
+// How a set is divided: a token's passes into `cuts` units of `per`, the units of all
+// tokens dealt to the waves of `blocks` workgroups in the order of memory, so that
+// what is in flight lies close together (8192 tokens of 64 + 8 heads of 128, forward 62 us
+// for 66, backward 91 for 100, where each wave had a token of its own).
 struct Shares {
   int per, cuts, blocks;
+};
+// A wave's walk over its units: token, unit of the token, pass.
+struct Walk {
+  int64_t t;
+  int cut, pass, end;
+  int dt, dc;             // a step of all waves, in tokens and units
+  Shares sh;
+  int n;                  // passes of a token
+  __device__ __forceinline__ Walk(const Shares& s, int n_, int block) : sh(s), n(n_) {
+    const uint32_t first = (uint32_t)block * kHW + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t all = (uint32_t)s.blocks * kHW, cuts = (uint32_t)s.cuts;
+    t = first / cuts;
+    cut = (int)(first - (uint32_t)t * cuts);
+    dt = (int)(all / cuts);
+    dc = (int)(all - (uint32_t)dt * cuts);
+    open();
+  }
+  __device__ __forceinline__ void open() {
+    pass = cut * sh.per;
+    end = min(pass + sh.per, n);
+  }
+  __device__ __forceinline__ bool fresh() const { return pass == cut * sh.per; }     // a unit begins
+  __device__ __forceinline__ void next() {
+    if (++pass < end) return;
+    t += dt;
+    cut += dc;
+    if (cut >= sh.cuts) {
+      cut -= sh.cuts;
+      ++t;
+    }
+    open();
+  }
 };
 struct GradGrid {
   Shares set[2];
 };
 
+// Forward.  A wave walks over tokens with its share of their heads, queries and then
+// keys; the heads of its next two passes are in flight, across tokens too.  FP32 results
+// are stored past the caches (5003 x 16 + 16 heads of 80: 27.6 us for 29.5; BF16: no
+// difference).
+template <typename T, int kMode, int G, int R>
+__global__ __launch_bounds__(kHB) void head_norm_rotary_kernel(HeadProblem p, Shares sh) {
+  __shared__ float2 turn[kHW][G * R];
+  __shared__ __attribute__((aligned(16))) float w[2][2 * R * G];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), slot = lane / G;
+  const Lane<kMode, G, R> me{lane % G, p.dim, p.rot / 2, p.adjacent};
+  const int nq = passes(p.set[0].heads, G), n = nq + passes(p.set[1].heads, G);
+  // what pass `pass` of token t is about: its set, and the lane's head of it
+  auto head_of = [&](int pass) { return (int64_t)(pass < nq ? pass : pass - nq) * (64 / G) + slot; };
+  auto fetch = [&](int64_t t, int pass, Raw<T, R>& r) {      // past the last head: that one again, not stored
+    const HeadSet& hs = p.set[pass >= nq];
+    me.fetch(static_cast<const T*>(hs.x) + t * hs.ld_token + min(head_of(pass), hs.heads - 1) * hs.ld_head, r);
+  };
+  Walk at(sh, n, (int)blockIdx.x), ahead = at;      // the pass at hand, the next to ask for
+  Raw<T, R> r0, r1;
+  if (ahead.t < p.T) fetch(ahead.t, ahead.pass, r0);
+  ahead.next();
+  if (ahead.t < p.T) fetch(ahead.t, ahead.pass, r1);
+  ahead.next();
+  if (p.norm != kHeadNone) {
+    stage_weight(p.set[0].w, p.w_fp32, p.dim, w[0]);
+    stage_weight(p.set[1].w, p.w_fp32, p.dim, w[1]);
+    lds_barrier();
+  }
+  float c[R], s[R];
+#pragma unroll 1
+  while (at.t < p.T) {
+    if (at.fresh()) me.angles(p, at.t, turn[wave], c, s);
+    const int which = at.pass >= nq;
+    float v[2 * R];
+    me.unpack(r0, v);
+    r0 = r1;
+    if (ahead.t < p.T) fetch(ahead.t, ahead.pass, r1);
+    ahead.next();
+    if (p.norm != kHeadNone) {
+      me.normalize(v, p.norm, p.eps);
+      float wv[2 * R];
+      me.weight(w[which], wv);
+#pragma unroll
+      for (int k = 0; k < 2 * R; ++k) v[k] *= wv[k];
+    }
+    me.template rotate<false>(v, c, s);
+    const HeadSet& hs = p.set[which];
+    const int64_t h = head_of(at.pass);
+    if (h < hs.heads) me.template store<sizeof(T) == 4>(static_cast<T*>(hs.y) + at.t * hs.ldy_token + h * hs.ldy_head, v);
+    at.next();
+  }
+}
+
 // Backward.  A workgroup has one set, and one share of its heads; its waves walk over
-// tokens, the next heads' loads in flight.  (Both sets in a workgroup would hold twice the
-// sums in registers: 76 us for 71 with 16 elements a lane.)  A lane keeps its elements' sums for the weight, a workgroup's
-// meet in LDS at the end, and the workgroups' sums are added by a second launch, all in
-// a fixed order.
+// tokens, the next heads' loads in flight, across tokens too.  (Both sets in a
+// workgroup would hold twice the sums in registers: 76 us for 71 with 16 elements a
+// lane.)  A lane keeps its elements' sums for the weight, a workgroup's meet in LDS at
+// the end, and the workgroups' sums are added by a second launch, all in a fixed order.
 template <typename T, int kMode, int G, int R>
 __global__ __launch_bounds__(kHB) void head_norm_rotary_backward_kernel(HeadProblem p, GradGrid grid) {
-  const int lane = threadIdx.x & 63, slot = lane / G;
+  __shared__ float2 turn[kHW][G * R];
+  __shared__ __attribute__((aligned(16))) float w[2 * R * G];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), slot = lane / G;
   const Lane<kMode, G, R> me{lane % G, p.dim, p.rot / 2, p.adjacent};
-  const int queries = grid.set[0].cuts * grid.set[0].blocks, which = (int)blockIdx.x >= queries;
+  const int queries = grid.set[0].blocks, which = (int)blockIdx.x >= queries;
   const Shares sh = grid.set[which];
   const HeadSet& hs = p.set[which];
-  const int block = (int)blockIdx.x - which * queries, cut = block / sh.blocks;
-  const int first = cut * sh.per, end = min(first + sh.per, passes(hs.heads, G));
   const float inv_d = 1.0f / (float)p.dim;
   const bool normed = p.norm != kHeadNone;
-  float w[2 * R], dw[2 * R];
-  if (normed) me.load_weight(hs.w, p.w_fp32, w);
+  Raw<T, R> rd, rx;
+  auto fetch = [&](int64_t t, int pass) {      // past the last head: that one again, not used
+    const int64_t h = min((int64_t)pass * (64 / G) + slot, hs.heads - 1);
+    me.fetch(static_cast<const T*>(hs.dy) + t * hs.lddy_token + h * hs.lddy_head, rd);
+    if (normed) me.fetch(static_cast<const T*>(hs.x) + t * hs.ld_token + h * hs.ld_head, rx);
+  };
+  Walk at(sh, passes(hs.heads, G), (int)blockIdx.x - which * queries);
+  if (at.t < p.T) fetch(at.t, at.pass);
+  if (normed) {
+    stage_weight(hs.w, p.w_fp32, p.dim, w);
+    lds_barrier();
+  }
+  float dw[2 * R], c[R], s[R];
 #pragma unroll
   for (int k = 0; k < 2 * R; ++k) dw[k] = 0.f;
 #pragma unroll 1
-  for (int64_t t = (int64_t)(block - cut * sh.blocks) * kHW + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); t < p.T;
-       t += (int64_t)sh.blocks * kHW) {
-    const T* x = static_cast<const T*>(hs.x) + t * hs.ld_token;
-    const T* dy = static_cast<const T*>(hs.dy) + t * hs.lddy_token;
-    T* dx = static_cast<T*>(hs.y) + t * hs.ldy_token;
-    Raw<T, R> rd, rx;
-    auto fetch = [&](int pass) {      // past the last head: that one again, not used
-      const int64_t h = min((int64_t)pass * (64 / G) + slot, hs.heads - 1);
-      me.fetch(dy + h * hs.lddy_head, rd);
-      if (normed) me.fetch(x + h * hs.ld_head, rx);
-    };
-    fetch(first);
-    float c[R], s[R];
-    me.angles(p, t, c, s);
-#pragma unroll 1
-    for (int pass = first; pass < end; ++pass) {
-      const int64_t h = (int64_t)pass * (64 / G) + slot;
-      const bool on = h < hs.heads;
-      float d[2 * R], xh[2 * R];
-      me.unpack(rd, d);
-      me.unpack(rx, xh);
-      fetch(min(pass + 1, end - 1));
-      me.template rotate<true>(d, c, s);
-      if (normed) {
-        const float rstd = me.normalize(xh, p.norm, p.eps);
-        if (on) {
+  while (at.t < p.T) {
+    if (at.fresh()) me.angles(p, at.t, turn[wave], c, s);
+    const int64_t h = (int64_t)at.pass * (64 / G) + slot, now = at.t;
+    const bool on = h < hs.heads;
+    float d[2 * R], xh[2 * R];
+    me.unpack(rd, d);
+    me.unpack(rx, xh);
+    at.next();
+    if (at.t < p.T) fetch(at.t, at.pass);
+    me.template rotate<true>(d, c, s);
+    if (normed) {
+      const float rstd = me.normalize(xh, p.norm, p.eps);
+      if (on) {
 #pragma unroll
-          for (int k = 0; k < 2 * R; ++k) dw[k] = __builtin_fmaf(d[k], xh[k], dw[k]);
-        }
-        float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-        for (int k = 0; k < 2 * R; ++k) {
-          d[k] *= w[k];
-          s1 += d[k];
-          s2 = __builtin_fmaf(d[k], xh[k], s2);
-        }
-        const float c1 = p.norm == kHeadLayer ? lanes_sum<G>(s1) * inv_d : 0.f, c2 = lanes_sum<G>(s2) * inv_d;
-#pragma unroll
-        for (int k = 0; k < 2 * R; ++k) d[k] = rstd * (d[k] - c1 - xh[k] * c2);
+        for (int k = 0; k < 2 * R; ++k) dw[k] = __builtin_fmaf(d[k], xh[k], dw[k]);
       }
-      if (on) me.store(dx + h * hs.ldy_head, d);
+      float wv[2 * R];
+      me.weight(w, wv);
+      float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2 * R; ++k) {
+        d[k] *= wv[k];
+        s1 += d[k];
+        s2 = __builtin_fmaf(d[k], xh[k], s2);
+      }
+      const float c1 = p.norm == kHeadLayer ? lanes_sum<G>(s1) * inv_d : 0.f, c2 = lanes_sum<G>(s2) * inv_d;
+#pragma unroll
+      for (int k = 0; k < 2 * R; ++k) d[k] = rstd * (d[k] - c1 - xh[k] * c2);
     }
+    if (on) me.template store<true>(static_cast<T*>(hs.y) + now * hs.ldy_token + h * hs.ldy_head, d);
   }
   if (!normed) return;
   // the workgroup's share of the weight's gradient: its lane groups in order
@@ -436,15 +520,16 @@ int lanes_of(int64_t dim, int R) {
   return g;
 }
 
-// Passes of a wave over a token's heads in the forward pass: few enough that there
-// are about 16 waves a CU; the shares of a token's heads that gives.
-void split_heads(const HeadProblem& p, int& per, int& cuts) {
+// A set of n passes a token for at most `most` workgroups.
+Shares share_out(int64_t T, int64_t n, int64_t most, int64_t per) {
+  if (n * T <= most * kHW) per = 1;
+  const int64_t cuts = (n + per - 1) / per, blocks = (T * cuts + kHW - 1) / kHW;
+  return Shares{(int)per, (int)cuts, (int)(blocks < most ? blocks : most)};
+}
+// The forward pass
+Shares forward_shares(const HeadProblem& p) {
   const int G = lanes_of(p.dim, run_of(false, p.x_fp32, p.dim));
-  const int64_t n = passes(p.set[0].heads, G) + passes(p.set[1].heads, G);
-  int64_t want = (4096 + p.T - 1) / p.T;
-  if (want > 1024) want = 1024;
-  per = (int)((n + want - 1) / want);
-  cuts = (int)((n + per - 1) / per);
+  return share_out(p.T, passes(p.set[0].heads, G) + passes(p.set[1].heads, G), kForwardBlocks, 2);
 }
 
 // The backward pass: as many workgroups as run at once on 256 CUs, five a CU for BF16 and
@@ -461,13 +546,7 @@ GradGrid divide(int64_t T, int64_t q_heads, int64_t k_heads, int64_t dim, bool x
     int64_t most = all * n[i] / (n[0] + n[1]);
     if (most < 1) most = 1;
     if (most > all - 1 && n[1 - i] > 0) most = all - 1;
-    int64_t cuts = (most * kHW + T - 1) / T;
-    if (cuts > n[i]) cuts = n[i];
-    if (cuts > most) cuts = most;
-    const int64_t per = (n[i] + cuts - 1) / cuts;
-    cuts = (n[i] + per - 1) / per;
-    const int64_t blocks = (T + kHW - 1) / kHW;
-    g.set[i] = Shares{(int)per, (int)cuts, (int)(blocks < most / cuts ? blocks : most / cuts)};
+    g.set[i] = share_out(T, n[i], most, 2);
   }
   return g;
 }
@@ -480,13 +559,11 @@ template <bool kBack, typename T, int kMode, int G, int R>
 void start(const HeadProblem& p, hipStream_t stream) {
   if constexpr (kBack) {
     const GradGrid g = divide(p.T, p.set[0].heads, p.set[1].heads, p.dim, p.x_fp32);
-    const int64_t parts = (int64_t)g.set[0].cuts * g.set[0].blocks + (int64_t)g.set[1].cuts * g.set[1].blocks;
+    const int64_t parts = g.set[0].blocks + g.set[1].blocks;
     hipLaunchKernelGGL((head_norm_rotary_backward_kernel<T, kMode, G, R>), dim3((unsigned)parts), dim3(kHB), 0, stream, p, g);
   } else {
-    int per, cuts;
-    split_heads(p, per, cuts);
-    const dim3 grid((unsigned)((p.T + kHW - 1) / kHW), (unsigned)cuts);
-    hipLaunchKernelGGL((head_norm_rotary_kernel<T, kMode, G, R>), grid, dim3(kHB), 0, stream, p, per);
+    const Shares sh = forward_shares(p);
+    hipLaunchKernelGGL((head_norm_rotary_kernel<T, kMode, G, R>), dim3((unsigned)sh.blocks), dim3(kHB), 0, stream, p, sh);
   }
 }
 template <bool kBack, typename T, int kMode>
@@ -538,7 +615,7 @@ int64_t head_grad_parts(int64_t T, int64_t q_heads, int64_t k_heads, int64_t dim
   int64_t most = 0;
   for (const bool x_fp32 : {false, true}) {
     const GradGrid g = divide(T, q_heads, k_heads, dim, x_fp32);
-    const int64_t n = (int64_t)g.set[0].cuts * g.set[0].blocks + (int64_t)g.set[1].cuts * g.set[1].blocks;
+    const int64_t n = g.set[0].blocks + g.set[1].blocks;
     if (n > most) most = n;
   }
   return most;
@@ -554,7 +631,7 @@ hipError_t launch_head_norm_rotary_backward(const HeadProblem& p, hipStream_t st
   if (p.norm == kHeadNone || (p.set[0].dw == nullptr && p.set[1].dw == nullptr)) return hipSuccess;
   const GradGrid g = divide(p.T, p.set[0].heads, p.set[1].heads, p.dim, p.x_fp32);
   hipLaunchKernelGGL(head_grad_sum_kernel, dim3((unsigned)((p.dim + 15) / 16), 2), dim3(1024), 0, stream, p.partial,
-                     g.set[0].cuts * g.set[0].blocks, g.set[1].cuts * g.set[1].blocks, p.dim, p.set[0].dw, p.set[1].dw);
+                     g.set[0].blocks, g.set[1].blocks, p.dim, p.set[0].dw, p.set[1].dw);
   return hipGetLastError();
 }
 
