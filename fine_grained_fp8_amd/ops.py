@@ -699,7 +699,8 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, sw: torch.Tensor, lora_a: t
 
 def _on_current_device(name, t):
     """Launches go to the current device: a tensor of another one is refused."""
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
+    index = t.get_device()
+    if index >= 0 and index != torch.cuda.current_device():
         raise ValueError(f"{name}: on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
@@ -859,73 +860,81 @@ def quant_act_cols(x: torch.Tensor, *, stream=None):
 
 
 def _check_heads(name, t, dtype, dev, T, heads, dim):
-    """t is [T][heads][dim] (heads None: any number) of this type on this device; its strides."""
-    if t.dim() != 3:
-        raise ValueError(f"{name}: expected [tokens][heads][dim], got shape {tuple(t.shape)}")
-    strides, shape = t.stride(), t.shape
+    """t is [T][heads][dim] (heads None: any number) of this type on this device; its number of heads and strides."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != T or shape[2] != dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name}: expected {(T, 'any' if heads is None else heads, dim)}, got {tuple(shape)}")
     if strides[2] != 1 and dim > 1:
         raise ValueError(f"{name}: the channels have to be contiguous, got strides {strides}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if shape[0] != T or shape[2] != dim or (heads is not None and shape[1] != heads):
-        raise ValueError(f"{name}: expected {(T, 'any' if heads is None else heads, dim)}, got {tuple(shape)}")
     if t.get_device() != dev:
         raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
-    return strides
+    return shape[1], strides
 
 
 def _first_heads(q, k):
-    """(type, device index, T, dim) that the sets share, and the device."""
+    """(type, device index, T, dim) that the sets share."""
     t = q if q is not None else k
     if t is None:
         raise ValueError("q, k: at least one is required")
-    if t.dim() != 3 or t.dtype not in _FLOATS:
-        raise TypeError(f"q, k: expected [tokens][heads][dim] of {_FLOATS}, got {tuple(t.shape)} {t.dtype}")
+    shape = t.shape
+    if len(shape) != 3 or t.dtype not in _FLOATS:
+        raise TypeError(f"q, k: expected [tokens][heads][dim] of {_FLOATS}, got {tuple(shape)} {t.dtype}")
     if not t.is_cuda:
         raise ValueError("q, k: must be device tensors")
     _on_current_device("q, k", t)
-    return t.dtype, t.get_device(), t.shape[0], t.shape[2], t.device
+    return t.dtype, t.get_device(), shape[0], shape[2]
+
+
+def _head_vector(name, t, n, dev, dtypes):
+    if t.dtype not in dtypes or t.shape != (n,) or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name}: a contiguous vector of {n} elements of {dtypes} on cuda:{dev} is required, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+
+
+_POSITION_BYTES = {torch.int64: 8, torch.int32: 4}
 
 
 def _head_arguments(dev, T, dim, wq, wk, norm, eps, positions, freq, sections, adjacent):
     """The arguments between the sets and the workspace or stream."""
-    if norm not in _lib.HEAD_NORM:
+    code = _lib.HEAD_NORM.get(norm, -1)
+    if code < 0:
         raise ValueError(f"norm: {norm!r} not in {list(_lib.HEAD_NORM)}")
     wt = _lib.OUT_BF16
-    for name, w in (("q_weight", wq), ("k_weight", wk)):
-        if w is not None:
-            _check_vec(name, w, dim, _FLOATS)
-            if norm is None or w.get_device() != dev:
-                raise ValueError(f"{name}: on {w.device} (expected cuda:{dev}), or given without a norm")
-            wt = _is_fp32(w)
-    if wq is not None and wk is not None and wq.dtype != wk.dtype:
-        raise TypeError(f"q_weight is {wq.dtype} and k_weight {wk.dtype}: one type is required")
+    if wq is not None or wk is not None:
+        if norm is None:
+            raise ValueError("q_weight, k_weight: without a norm there is no weight")
+        if wq is not None:
+            _head_vector("q_weight", wq, dim, dev, _FLOATS)
+            wt = _is_fp32(wq)
+        if wk is not None:
+            _head_vector("k_weight", wk, dim, dev, _FLOATS if wq is None else (wq.dtype,))
+            wt = _is_fp32(wk)
     if freq is None:
         if positions is not None:
             raise ValueError("positions and freq: both or neither")
-        return wt, _lib.HEAD_NORM[norm], eps, 0, None, 8, 1, None, None, 0
+        return wt, code, eps, 0, None, 8, 1, None, None, 0
     if positions is None:
         raise ValueError("positions and freq: both or neither")
     pairs = freq.numel()
-    _check_vec("freq", freq, pairs, (torch.float64,))
+    _head_vector("freq", freq, pairs, dev, (torch.float64,))
     axes, counts = 1, None
     if sections is not None:
         axes = len(sections)
         counts = (ctypes.c_int64 * axes)(*sections)
-    shape = positions.shape
-    if positions.dtype not in (torch.int64, torch.int32) or not positions.is_contiguous() or \
-            not (shape == (T, axes) or (axes == 1 and shape == (T,))):
-        raise ValueError(f"positions: contiguous int32 or int64 {(T, axes)} required, got {positions.dtype} {tuple(shape)}")
-    if positions.get_device() != dev or freq.get_device() != dev:
-        raise ValueError(f"positions on {positions.device}, freq on {freq.device}: expected cuda:{dev}")
-    return (wt, _lib.HEAD_NORM[norm], eps, 2 * pairs, positions.data_ptr(), 8 if positions.dtype == torch.int64 else 4, axes,
-            counts, freq.data_ptr(), 1 if adjacent else 0)
+    shape, nbytes = positions.shape, _POSITION_BYTES.get(positions.dtype)
+    if nbytes is None or not positions.is_contiguous() or not (shape == (T, axes) or (axes == 1 and shape == (T,))) or \
+            positions.get_device() != dev:
+        raise ValueError(f"positions: contiguous int32 or int64 {(T, axes)} on cuda:{dev} required, got {positions.dtype} "
+                         f"{tuple(shape)} on {positions.device}")
+    return wt, code, eps, 2 * pairs, positions.data_ptr(), nbytes, axes, counts, freq.data_ptr(), 1 if adjacent else 0
 
 
 def _head_output(name, given, like, index, shape, stream):
     """The set's output (a new contiguous tensor unless one is given) and its strides."""
     if given is not None:
-        return given, _check_heads(name, given, like.dtype, index, *shape)
+        return given, _check_heads(name, given, like.dtype, index, *shape)[1]
     if stream is None:      # the shorter call
         made = torch.empty_like(like, memory_format=torch.contiguous_format)
     else:
@@ -950,21 +959,21 @@ def head_norm_rotary(q: torch.Tensor, k, positions=None, freq=None, *, q_weight=
     Returns (q_out, k_out), None for a set that is None.
     """
     lib = _lib.load_library()
-    dtype, dev, T, dim, _ = _first_heads(q, k)
+    dtype, dev, T, dim = _first_heads(q, k)
     args = _head_arguments(dev, T, dim, q_weight, k_weight, norm, eps, positions, freq, sections, adjacent)
-    given = (None, None) if out is None else out
     made, sets = [None, None], [None, None]
     for i, t, w in ((0, q, q_weight), (1, k, k_weight)):
         if t is None:
             continue
-        name = "qk"[i]
-        strides, heads = _check_heads(name, t, dtype, dev, T, None, dim), t.shape[1]
-        o, to = _head_output("out: " + name, given[i], t, dev, (T, heads, dim), stream)
+        heads, strides = _check_heads("qk"[i], t, dtype, dev, T, None, dim)
+        o, to = _head_output("out", None if out is None else out[i], t, dev, (T, heads, dim), stream)
         made[i] = o
-        sets[i] = _lib.Heads(t.data_ptr(), heads, strides[0], strides[1], _ptr(w), o.data_ptr(), to[0], to[1])
+        sets[i] = _lib.Heads(t.data_ptr(), heads, strides[0], strides[1], None if w is None else w.data_ptr(), o.data_ptr(), to[0],
+                             to[1])
     st = lib.fp8_head_norm_rotary(T, dim, _lib.OUT_FP32 if dtype == torch.float32 else _lib.OUT_BF16, sets[0], sets[1], *args,
                                   _stream(stream))
-    _lib.check("fp8_head_norm_rotary", st)
+    if st != 0:
+        _lib.check("fp8_head_norm_rotary", st)
     return made[0], made[1]
 
 
@@ -979,15 +988,14 @@ def head_norm_rotary_backward(dq: torch.Tensor, dk, q, k, positions=None, freq=N
     optional (dq_in, dk_in) tensors.
     """
     lib = _lib.load_library()
-    dtype, dev, T, dim, device = _first_heads(dq, dk)
+    dtype, dev, T, dim = _first_heads(dq, dk)
     args = _head_arguments(dev, T, dim, q_weight, k_weight, norm, eps, positions, freq, sections, adjacent)
-    given = (None, None) if out is None else out
     made, sets, grads, count = [None, None], [None, None], [None, None], [0, 0]
     for i, d, x, w in ((0, dq, q, q_weight), (1, dk, k, k_weight)):
         if d is None:
             continue
         name = "qk"[i]
-        strides, heads = _check_heads("d" + name, d, dtype, dev, T, None, dim), d.shape[1]
+        heads, strides = _check_heads("d" + name, d, dtype, dev, T, None, dim)
         count[i] = heads
         of = strides
         if norm is None:
@@ -995,15 +1003,16 @@ def head_norm_rotary_backward(dq: torch.Tensor, dk, q, k, positions=None, freq=N
         elif x is None:
             raise ValueError(f"{name}: required with a norm")
         else:
-            of = _check_heads(name, x, dtype, dev, T, heads, dim)
-            grads[i] = _empty(dim, torch.float32, device, stream)
-        o, to = _head_output("out: d" + name, given[i], d, dev, (T, heads, dim), stream)
+            of = _check_heads(name, x, dtype, dev, T, heads, dim)[1]
+            grads[i] = _empty(dim, torch.float32, d.device, stream)
+        o, to = _head_output("out", None if out is None else out[i], d, dev, (T, heads, dim), stream)
         made[i] = o
-        sets[i] = _lib.HeadsGrad(x.data_ptr(), heads, of[0], of[1], _ptr(w), d.data_ptr(), strides[0], strides[1], o.data_ptr(),
-                                 to[0], to[1], _ptr(grads[i]))
+        sets[i] = _lib.HeadsGrad(x.data_ptr(), heads, of[0], of[1], None if w is None else w.data_ptr(), d.data_ptr(), strides[0],
+                                 strides[1], o.data_ptr(), to[0], to[1], _ptr(grads[i]))
     nbytes = 0 if norm is None else _heads_workspace(T, count[0], count[1], dim)
-    ws = _workspace(nbytes, device, stream) if nbytes != 0 else None
+    ws = _workspace(nbytes, (dq if dq is not None else dk).device, stream) if nbytes != 0 else None
     st = lib.fp8_head_norm_rotary_backward(T, dim, _lib.OUT_FP32 if dtype == torch.float32 else _lib.OUT_BF16, sets[0], sets[1],
                                            *args, _ptr(ws), nbytes, _stream(stream))
-    _lib.check("fp8_head_norm_rotary_backward", st)
+    if st != 0:
+        _lib.check("fp8_head_norm_rotary_backward", st)
     return made[0], made[1], grads[0], grads[1]

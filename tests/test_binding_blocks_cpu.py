@@ -74,7 +74,10 @@ def test_memory_of_a_call_on_the_current_stream(rec, name):
 def test_tensors_of_another_device_than_the_current_one(monkeypatch):
     """Refused before anything is launched."""
     class Elsewhere:
-        is_cuda, device = True, torch.device("cuda", 1)
+        device = torch.device("cuda", 1)
+
+        def get_device(self):
+            return 1
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     with pytest.raises(ValueError, match="current device"):
         ops._on_current_device("x", Elsewhere())
