@@ -722,46 +722,64 @@ def _heads_workspace(T, heads_q, heads_k, dim):
     return _lib.load_library().fp8_head_norm_rotary_backward_workspace(T, heads_q, heads_k, dim)
 
 
+def _rows(name, t, dtypes, rows, cols, dev):
+    """t has at least [rows][cols] of these types, row-major, on this device; its row stride."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or strides[1] != 1 or shape[0] < rows or shape[1] < cols:
+        raise ValueError(f"{name}: expected row-major, at least {(rows, cols)}, got {tuple(shape)} strides {strides}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
+    return strides[0]
+
+
+def _made(like, shape, dtype, stream):
+    """An uninitialized tensor on like's device (the short call on the current stream)."""
+    return like.new_empty(shape, dtype=dtype) if stream is None else _empty(shape, dtype, like.device, stream)
+
+
 def _gated(A, sA, w13, s13, activation, quant, return_gate_up, out_dtype, out, stream):
     lib = _lib.load_library()
     act = _activation(activation)
     _check_2d("A", A, _CODES)
-    _check_2d("sA", sA, _FP32)
-    _check_2d("s13", s13, _FP32)
     _on_current_device("A", A)
+    dev = A.get_device()
     M, K = A.shape
     rows = w13.shape[0] if w13.dim() == 2 else 1
     if rows % 2 != 0:
         raise ValueError(f"w13: expected [2 I][K], got {tuple(w13.shape)}")
     I = rows // 2
     _check_codes("w13", w13, (rows, K))
-    if sA.shape[0] < K // 128 or sA.shape[1] < M or s13.shape[0] < rows // 128 or s13.shape[1] < K // 128:
-        raise ValueError(f"sA {tuple(sA.shape)}, s13 {tuple(s13.shape)}: expected at least {(K // 128, M)} and "
-                         f"{(rows // 128, K // 128)}")
-    dev = A.device
-    _same_device(dev, sA=sA, w13=w13, s13=s13, out=out)
-    q = s = gate_up = None
+    if w13.get_device() != dev:
+        raise ValueError(f"w13: on {w13.device}, the input is on {A.device}")
+    ld_sa = _rows("sA", sA, _FP32, K // 128, M, dev)
+    ld_s13 = _rows("s13", s13, _FP32, rows // 128, K // 128, dev)
+    q = s = gate_up = ws = None
     ldh = ld_s = h_type = 0
     if quant:
         ld_s = round_up(M, 4)
-        q = _empty((M, I), torch.uint8, dev, stream)
-        s = _empty((I // 128, ld_s), torch.float32, dev, stream)
+        q = _made(A, (M, I), torch.uint8, stream)
+        s = _made(A, (I // 128, ld_s), torch.float32, stream)
     else:
         if out is None:
-            out = _empty((M, I), _float_type(out_dtype), dev, stream)
+            out = _made(A, (M, I), _float_type(out_dtype), stream)
+            ldh = I
         else:
-            _check_2d("out", out, _FLOATS)
+            ldh = _rows("out", out, _FLOATS, M, I, dev)
             if out.shape != (M, I):
                 raise ValueError(f"out: expected {(M, I)}, got {tuple(out.shape)}")
-        ldh, h_type = out.stride(0), _is_fp32(out)
+        h_type = _is_fp32(out)
     if return_gate_up:
-        gate_up = _empty((M, rows), torch.bfloat16, dev, stream)
+        gate_up = _made(A, (M, rows), torch.bfloat16, stream)
     nbytes = _gated_workspace(M, I, K)
-    ws = _workspace(nbytes, dev, stream) if nbytes != 0 else None
+    if nbytes != 0:
+        ws = A.new_empty(max(nbytes, 0), dtype=torch.uint8) if stream is None else _workspace(nbytes, A.device, stream)
     st = lib.fp8_block_gemm_gated(
-        M, I, K, A.data_ptr(), A.stride(0), sA.data_ptr(), sA.stride(0), w13.data_ptr(), s13.data_ptr(), s13.stride(0), act,
+        M, I, K, A.data_ptr(), A.stride(0), sA.data_ptr(), ld_sa, w13.data_ptr(), s13.data_ptr(), ld_s13, act,
         _ptr(out), h_type, ldh, _ptr(gate_up), rows, _ptr(q), I, _ptr(s), ld_s, _ptr(ws), nbytes, _stream(stream))
-    _lib.check("fp8_block_gemm_gated", st)
+    if st != 0:
+        _lib.check("fp8_block_gemm_gated", st)
     return out, q, s, gate_up
 
 
@@ -791,30 +809,30 @@ def block_gemm_gated_quant(A: torch.Tensor, sA: torch.Tensor, w13: torch.Tensor,
 
 
 def _gated_backward(dh, gate_up, activation, stream, d=None, q=None, s=None, qt=None, st=None, ht=None, sht=None):
-    lib = _lib.load_library()
     T, I = dh.shape
-    status = lib.fp8_gated_backward(
-        T, I, _ptr(dh), dh.stride(0), _ptr(gate_up), gate_up.stride(0), _activation(activation), _ptr(d), 2 * I,
-        _ptr(q), 2 * I, _ptr(s), 0 if s is None else s.stride(0), _ptr(qt), round_up(T, 128), _ptr(st), 2 * I,
-        _ptr(ht), _ptr(sht), 0 if sht is None else sht.stride(0), _stream(stream))
-    _lib.check("fp8_gated_backward", status)
+    status = _lib.load_library().fp8_gated_backward(
+        T, I, dh.data_ptr(), dh.stride(0), gate_up.data_ptr(), gate_up.stride(0), _activation(activation), _ptr(d), 2 * I,
+        _ptr(q), 2 * I, _ptr(s), round_up(T, 4), _ptr(qt), round_up(T, 128), _ptr(st), 2 * I, _ptr(ht), _ptr(sht), I,
+        _stream(stream))
+    if status != 0:
+        _lib.check("fp8_gated_backward", status)
 
 
 def _check_gated_backward(dh, gate_up):
     _check_2d("dh", dh, (torch.bfloat16,))
-    _check_2d("gate_up", gate_up, (torch.bfloat16,))
-    if gate_up.shape != (dh.shape[0], 2 * dh.shape[1]):
-        raise ValueError(f"gate_up: expected {(dh.shape[0], 2 * dh.shape[1])}, got {tuple(gate_up.shape)}")
     _on_current_device("dh", dh)
-    _same_device(dh.device, gate_up=gate_up)
-    return dh.shape
+    T, I = dh.shape
+    _rows("gate_up", gate_up, (torch.bfloat16,), T, 2 * I, dh.get_device())
+    if gate_up.shape != (T, 2 * I):
+        raise ValueError(f"gate_up: expected {(T, 2 * I)}, got {tuple(gate_up.shape)}")
+    return T, I
 
 
 def gated_backward(dh: torch.Tensor, gate_up: torch.Tensor, *, activation: str = "silu", stream=None):
     """Gradient of h = act(a) * u for dh [T][I] bfloat16 and gate_up = [a | u]
     [T][2 I] bfloat16 (I a multiple of 128): [da | du] [T][2 I] bfloat16."""
     T, I = _check_gated_backward(dh, gate_up)
-    d = _empty((T, 2 * I), torch.bfloat16, dh.device, stream)
+    d = _made(dh, (T, 2 * I), torch.bfloat16, stream)
     _gated_backward(dh, gate_up, activation, stream, d=d)
     return d
 
@@ -829,15 +847,15 @@ def gated_backward_quant(dh: torch.Tensor, gate_up: torch.Tensor, *, activation:
     other operand alike).  return_h appends (ht [I][Tp], sht [Tp/128][I]): h's column
     tiles, operand-tiled, for the weight gradient of the down projection."""
     T, I = _check_gated_backward(dh, gate_up)
-    Tp, dev = round_up(T, 128), dh.device
-    q = _empty((T, 2 * I), torch.uint8, dev, stream)
-    s = _empty((2 * I // 128, round_up(T, 4)), torch.float32, dev, stream)
-    qt = _empty((2 * I, Tp), torch.uint8, dev, stream)
-    st = _empty((Tp // 128, 2 * I), torch.float32, dev, stream)
+    Tp = round_up(T, 128)
+    q = _made(dh, (T, 2 * I), torch.uint8, stream)
+    s = _made(dh, (2 * I // 128, round_up(T, 4)), torch.float32, stream)
+    qt = _made(dh, (2 * I, Tp), torch.uint8, stream)
+    st = _made(dh, (Tp // 128, 2 * I), torch.float32, stream)
     ht = sht = None
     if return_h:
-        ht = _empty((I, Tp), torch.uint8, dev, stream)
-        sht = _empty((Tp // 128, I), torch.float32, dev, stream)
+        ht = _made(dh, (I, Tp), torch.uint8, stream)
+        sht = _made(dh, (Tp // 128, I), torch.float32, stream)
     _gated_backward(dh, gate_up, activation, stream, None, q, s, qt, st, ht, sht)
     return (q, s, qt, st, ht, sht) if return_h else (q, s, qt, st)
 
@@ -852,10 +870,11 @@ def quant_act_cols(x: torch.Tensor, *, stream=None):
     _on_current_device("x", x)
     rows, cols = x.shape
     Tp = round_up(rows, 128)
-    q = _empty((cols, Tp), torch.uint8, x.device, stream)
-    s = _empty((Tp // 128, cols), torch.float32, x.device, stream)
-    st = lib.fp8_quant_act_cols(_ptr(x), rows, cols, x.stride(0), _ptr(q), _ptr(s), s.stride(0), _stream(stream))
-    _lib.check("fp8_quant_act_cols", st)
+    q = _made(x, (cols, Tp), torch.uint8, stream)
+    s = _made(x, (Tp // 128, cols), torch.float32, stream)
+    st = lib.fp8_quant_act_cols(x.data_ptr(), rows, cols, x.stride(0), q.data_ptr(), s.data_ptr(), cols, _stream(stream))
+    if st != 0:
+        _lib.check("fp8_quant_act_cols", st)
     return q, s
 
 
