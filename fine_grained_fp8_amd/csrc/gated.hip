@@ -541,11 +541,13 @@ __device__ __forceinline__ float quotient(float y, const ScaleInverse& i) { retu
 // Bound by memory with the vector unit close behind: 4096 x 18432, 755 MB, 170 us (4.4
 // TB/s; BF16 gradients alone 140).  The registers decide: at most 128 let two workgroups
 // of 512 lanes share a CU (left to the compiler, 131: one, 222 us); with h three
-// sets of values need 1024 lanes of two rows (242 us; four rows: 342 with spills).
-template <bool kH, int kGR, int kWavesPerSimd>
+// sets of values need 1024 lanes of two rows (242 us; four rows: 342 with spills; four
+// rows with gate and up asked for again, for h alone, after da and du: 243).
+// kOne: one of the sets, which blockIdx.y names.
+template <bool kH, int kGR, int kWavesPerSimd, bool kOne = false>
 __global__ __launch_bounds__(2048 / kGR, kWavesPerSimd) void gated_backward_kernel(GatedGradProblem p) {
   constexpr int kGW = 32 / kGR, kGB = kGW * 64;              // waves and threads: kGR rows a lane
-  constexpr int kSets = kH ? 3 : 2;                          // da, du, h
+  constexpr int kSets = kOne ? 1 : kH ? 3 : 2;               // da, du, h
   __shared__ uint32_t most[kSets][kGW][128];
   __shared__ __attribute__((aligned(16))) float inv[kSets][2][128];
   __shared__ __attribute__((aligned(16))) uint8_t codes[kSets][128 * 128];
@@ -553,6 +555,7 @@ __global__ __launch_bounds__(2048 / kGR, kWavesPerSimd) void gated_backward_kern
   const int sub = lane >> 4, l16 = lane & 15;
   const int64_t ncb = p.I / 128, nrb = (p.T + 127) / 128;
   const int64_t rb = blockIdx.x / ncb, cb = blockIdx.x % ncb;
+  const int first = kOne ? blockIdx.y : 0;                   // the workgroup's first set
   const int64_t r0 = rb * 128 + wave * 4 * kGR + sub * kGR, c0 = cb * 128 + l16 * 8;
 
   float y[kSets][kGR][8];
@@ -578,21 +581,28 @@ __global__ __launch_bounds__(2048 / kGR, kWavesPerSimd) void gated_backward_kern
         const float z = logistic(p.gelu ? gelu_argument(a) : a);
         const float f = a * z;                               // act(a)
         const float slope = p.gelu ? gelu_argument_slope(a) : 1.0f;
-        y[0][i][k] = d * b * __builtin_fmaf(f * (1.0f - z), slope, z);
-        y[1][i][k] = d * f;
-        if constexpr (kH) y[2][i][k] = f * b;
+        const float da = d * b * __builtin_fmaf(f * (1.0f - z), slope, z), du = d * f, h = f * b;
+        if constexpr (kOne) {
+          y[0][i][k] = first == 0 ? da : first == 1 ? du : h;
+        } else {
+          y[0][i][k] = da;
+          y[1][i][k] = du;
+          if constexpr (kH) y[2][i][k] = h;
+        }
       }
   }
 
   // row tiles, from registers
 #pragma unroll
-  for (int m = 0; m < 2; ++m) {
+  for (int n = 0; n < kSets; ++n) {
+    const int m = first + n;
+    if (m == 2) break;                                       // h has none
     const int64_t col = m * p.I + c0;
     if (p.d != nullptr) {
 #pragma unroll
       for (int i = 0; i < kGR; ++i)
         if (r0 + i < p.T) {
-          const float* v = y[m][i];
+          const float* v = y[n][i];
           __builtin_nontemporal_store(gv4i{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])},
                                       reinterpret_cast<gv4i*>(p.d + (r0 + i) * p.ld_d + col));
         }
@@ -602,9 +612,9 @@ __global__ __launch_bounds__(2048 / kGR, kWavesPerSimd) void gated_backward_kern
       for (int i = 0; i < kGR; ++i) {
         uint32_t t = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) t = max(t, __float_as_uint(y[m][i][k]) & 0x7FFFFFFFu);
+        for (int k = 0; k < 8; ++k) t = max(t, __float_as_uint(y[n][i][k]) & 0x7FFFFFFFu);
         float s;
-        const uint2 q = quant8_f32(y[m][i], row16_max_u32(t), s);
+        const uint2 q = quant8_f32(y[n][i], row16_max_u32(t), s);
         if (r0 + i < p.T) {
           __builtin_nontemporal_store(gv2i{(int)q.x, (int)q.y}, reinterpret_cast<gv2i*>(p.q + (r0 + i) * p.ldq + col));
           if (l16 == 0) p.s[(m * ncb + cb) * p.ld_s + r0 + i] = s;
@@ -612,7 +622,7 @@ __global__ __launch_bounds__(2048 / kGR, kWavesPerSimd) void gated_backward_kern
       }
     }
   }
-  if (p.qt == nullptr && !kH) return;
+  if (p.qt == nullptr && (!kH || (kOne && first < 2))) return;
 
   // column tiles: their maxima over the waves
 #pragma unroll
@@ -631,14 +641,14 @@ __global__ __launch_bounds__(2048 / kGR, kWavesPerSimd) void gated_backward_kern
   }
   __syncthreads();
   if (threadIdx.x < kSets * 128) {
-    const int m = threadIdx.x >> 7, c = threadIdx.x & 127;
-    uint32_t t = most[m][0][c];
+    const int n = threadIdx.x >> 7, m = first + n, c = threadIdx.x & 127;
+    uint32_t t = most[n][0][c];
 #pragma unroll
-    for (int w = 1; w < kGW; ++w) t = max(t, most[m][w][c]);
+    for (int w = 1; w < kGW; ++w) t = max(t, most[n][w][c]);
     ScaleInverse v;
     const float s = tile_scale_f32(t, v);
-    inv[m][0][c] = v.r;
-    inv[m][1][c] = v.l;
+    inv[n][0][c] = v.r;
+    inv[n][1][c] = v.l;
     if (m == 2) p.hst[rb * p.ld_hst + cb * 128 + c] = s;
     else if (p.qt != nullptr) p.st[rb * p.ld_st + m * p.I + cb * 128 + c] = s;
   }
@@ -679,21 +689,22 @@ __global__ __launch_bounds__(2048 / kGR, kWavesPerSimd) void gated_backward_kern
   }
   __syncthreads();
 #pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    if (p.qt == nullptr) break;
+  for (int n = 0; n < kSets; ++n) {
+    const int m = first + n;
+    if (p.qt == nullptr || m == 2) break;
 #pragma unroll
     for (int i = 0; i < 1024 / kGB; ++i) {
       const int at = i * kGB + threadIdx.x, c = at >> 3, ch = at & 7;
-      const gv4i v = *reinterpret_cast<const gv4i*>(&codes[m][c * 128 + ((ch ^ ((c >> 3) & 7)) << 4)]);
+      const gv4i v = *reinterpret_cast<const gv4i*>(&codes[n][c * 128 + ((ch ^ ((c >> 3) & 7)) << 4)]);
       __builtin_nontemporal_store(v, reinterpret_cast<gv4i*>(p.qt + (m * p.I + cb * 128 + c) * p.ldqt + rb * 128 + ch * 16));
     }
   }
-  if constexpr (kH) {
+  if (kH && (!kOne || first == 2)) {
     // operand tiles: 16 columns x 128 tokens are 2 KB, lane 16 g + c of half h: tokens 64 h + 16 g ..
 #pragma unroll
     for (int i = 0; i < 1024 / kGB; ++i) {
       const int at = i * kGB + threadIdx.x, c = (at >> 7) * 16 + (at & 15), ch = (at >> 4) & 7;
-      const gv4i v = *reinterpret_cast<const gv4i*>(&codes[2][c * 128 + ((ch ^ ((c >> 3) & 7)) << 4)]);
+      const gv4i v = *reinterpret_cast<const gv4i*>(&codes[kSets - 1][c * 128 + ((ch ^ ((c >> 3) & 7)) << 4)]);
       uint8_t* tile = p.ht + ((cb * 8 + (at >> 7)) * nrb + rb) * 2048;
       __builtin_nontemporal_store(v, reinterpret_cast<gv4i*>(tile + (at & 127) * 16));
     }
@@ -744,7 +755,11 @@ hipError_t launch_gated_few(const GatedFewProblem& p, hipStream_t stream) {
 
 hipError_t launch_gated_backward(const GatedGradProblem& p, hipStream_t stream) {
   const dim3 grid((unsigned)((p.T + 127) / 128 * (p.I / 128)));
-  if (p.ht != nullptr) hipLaunchKernelGGL((gated_backward_kernel<true, 2, 4>), grid, dim3(1024), 0, stream, p);
+  // few blocks: a workgroup for each of da, du and h, which reads what it needs by itself
+  // (1333 x 1408, 121 blocks: 12.0 to 10.2 us, with h 13.0 to 12.5; 100 x 512, 4: 9.8 to 7.3;
+  // 2048 x 1408, 176: 12.7 to 13.1, with h 13.4 to 16.4)
+  if (grid.x <= 128) hipLaunchKernelGGL((gated_backward_kernel<true, 2, 4, true>), dim3(grid.x, p.ht != nullptr ? 3 : 2), dim3(1024), 0, stream, p);
+  else if (p.ht != nullptr) hipLaunchKernelGGL((gated_backward_kernel<true, 2, 4>), grid, dim3(1024), 0, stream, p);
   else hipLaunchKernelGGL((gated_backward_kernel<false, 4, 4>), grid, dim3(512), 0, stream, p);
   return hipGetLastError();
 }

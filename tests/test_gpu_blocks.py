@@ -225,7 +225,7 @@ def padded_t(a):
 
 
 @pytest.mark.parametrize("kind", ["silu", "gelu"])
-@pytest.mark.parametrize("T,I", [(1, 128), (3, 256), (127, 128), (128, 384), (129, 128), (300, 640), (1000, 1408)])
+@pytest.mark.parametrize("T,I", [(1, 128), (3, 256), (127, 128), (128, 384), (129, 128), (300, 640), (1000, 1408), (1501, 1408)])
 def test_gated_backward(gpu_lib, T, I, kind):
     dh, gu = rand((T, I), 21, torch.bfloat16, std=1e-3), rand((T, 2 * I), 22, torch.bfloat16, std=2.0)
     gu[0, 0], gu[0, 1], gu[0, 2] = -30.0, 60.0, 0.0
@@ -257,8 +257,9 @@ def test_gated_backward_against_differences(gpu_lib):
         assert (np.abs(d - want) <= half_step(torch.bfloat16) * np.abs(want) + 1e-8).all()
 
 
-def test_gated_backward_strides_nonfinite_and_zero(gpu_lib):
-    T, I = 150, 256
+@pytest.mark.parametrize("T", [150, 8300])       # a set of values and all of them to a workgroup
+def test_gated_backward_strides_nonfinite_and_zero(gpu_lib, T):
+    I = 256
     big_dh, big_gu = rand((T + 1, I + 8), 31, torch.bfloat16), rand((T + 1, 2 * I + 24), 32, torch.bfloat16)
     dh, gu = big_dh[:T, 8:], big_gu[:T, 16:16 + 2 * I]
     want = gpu_lib.gated_backward_quant(dh.contiguous(), gu.contiguous(), return_h=True)
