@@ -6,6 +6,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "blocks.hpp"
 #include "host_checks.hpp"
 
@@ -142,7 +144,7 @@ extern "C" {
 
 int64_t fp8_block_gemm_gated_workspace(int64_t M, int64_t I, int64_t K) {
   if (gated_shape(M, I, K) != FP8_OK) return -1;
-  const int64_t cuts = fp8bs::gated_few_cuts(M, I, K);
+  const int64_t cuts = std::max(fp8bs::gated_few_cuts(M, I, K, false), fp8bs::gated_few_cuts(M, I, K, true));   // one size for both
   return (cuts > 1 ? 2 * cuts : cuts) * M * I * 4;
 }
 
@@ -189,7 +191,7 @@ fp8_status fp8_block_gemm_gated(int64_t M, int64_t I, int64_t K, const uint8_t* 
   ge.gate_up = static_cast<uint16_t*>(gate_up);
   ge.ld_gu = ld_gu;
   ge.q = q; ge.ldq = ldq; ge.s = scales; ge.ld_s = ld_s;
-  if (const int cuts = fp8bs::gated_few_cuts(M, I, K); cuts > 0) {
+  if (const int cuts = fp8bs::gated_few_cuts(M, I, K, q != nullptr || e == 4); cuts > 0) {
     fp8bs::GatedFewProblem p{};
     p.M = static_cast<int>(M); p.N = I; p.K = K;
     p.A = A; p.lda = lda; p.sA = sA; p.ld_sa = ld_sa;

@@ -15,8 +15,9 @@ namespace fp8bs {
 // ---- the gated product for few tokens ----
 constexpr int kGatedExactTokens = 64;    // up to so many: FP32 values and codes from exact products
 constexpr int kGatedMaxCuts = 8;
-// Workgroups that share the K blocks of a tile of channels; 0: the block GEMM is faster
-int gated_few_cuts(int64_t M, int64_t N, int64_t K);
+// Workgroups that share the K blocks of a tile of channels, for FP32 results and codes
+// or for BF16 results; 0: the block GEMM is faster
+int gated_few_cuts(int64_t M, int64_t N, int64_t K, bool fp32);
 struct GatedFewProblem {
   int M;
   int64_t N, K;
@@ -32,7 +33,7 @@ struct GatedFewProblem {
   int out_fp32;
   GatedEpilogue gated;
   // workspace
-  int cuts;               // gated_few_cuts(M, N, K)
+  int cuts;               // gated_few_cuts of the result
   float* parts;           // [cuts][M][2 N] if cuts > 1; otherwise [M][N], h of a call for codes
 };
 hipError_t launch_gated_few(const GatedFewProblem& p, hipStream_t stream);

@@ -5,6 +5,7 @@
 //   a = X W1^T, u = X W3^T,  h = act(a) u,  act(a) = a logistic(v(a))
 //   da = dh u act'(a),  du = dh act(a)
 //   act'(a) = z + a z (1 - z) v'(a),  z = logistic(v(a))
+#include <algorithm>
 #include <atomic>
 
 #include "blocks.hpp"
@@ -722,12 +723,17 @@ __global__ __launch_bounds__(2048 / kGR, kWavesPerSimd) void gated_backward_kern
 // K is cut so that every CU has a workgroup; a cut adds partial sums and the
 // finishing launch, about what 6 to 8 blocks of K take: 48 tokens, 7168 x 2048, with 1 / 2
 // / 4 / 8 cuts 26 / 18 / 15 / 14; 256 tokens 29 / 24 / 24 / 30; 300 tokens, 2048 x 1408 11 / 14 / 18.
-int gated_few_cuts(int64_t M, int64_t N, int64_t K) {
+// Codes of tiles that no workgroup has whole take that launch anyway, and cuts of four
+// blocks pay: 48 tokens, 2048 x 1408, 1 / 2 / 4 / 8 cuts 14.9 / 11.4 / 10.5 / 12; 64 tokens, 1024 x 512,
+// 1 / 2 / 4 11.4 / 9.6 / 9.4; 128 tokens, 2048 x 1408 13.4 / 11.8 / 11.9; 300 tokens 13.7 / 14.1 / 18.
+// FP32 results follow them, so that the codes are those of that result (64 tokens,
+// 2048 x 1408: 10.5 for 10.9; 17 tokens, 1024 x 1024 7.6 for 6.3).
+int gated_few_cuts(int64_t M, int64_t N, int64_t K, bool fp32) {
   const int64_t kb = K / 128;
   if (M <= 16) return (int)((kb + kMaxLds / kRowBlockLds - 1) / (kMaxLds / kRowBlockLds));
   if (M > 64 && (M + 127) / 128 * (N / 128) >= 128) return 0;
-  const int64_t groups = (M + 63) / 64 * (N / 64), most = (kb - 8) / 6 < kGatedMaxCuts ? (kb - 8) / 6 : kGatedMaxCuts;
-  const int64_t c = 256 / groups < most ? 256 / groups : most;
+  const int64_t groups = (M + 63) / 64 * (N / 64), worth = fp32 ? kb / 4 : (kb - 8) / 6;
+  const int64_t c = std::min({256 / groups, worth, (int64_t)kGatedMaxCuts});
   return (int)(c > 1 ? c : 1);
 }
 
