@@ -225,8 +225,12 @@ __global__ __launch_bounds__(256) void gated_few_kernel(GatedFewProblem p) {
   const int kb_n = (int)(p.K / 128), tiles = (int)(p.N / 16);
   // workgroups of the same tiles follow each other: the token blocks, and for each the cuts
   const int blocks = (p.M + NT * 16 - 1) / (NT * 16);
-  const int cut = blockIdx.x % p.cuts, block = blockIdx.x / p.cuts % blocks;
-  const int t0 = (blockIdx.x / p.cuts / blocks * 4 + wave) * RT;                     // the wave's first tile
+  // on one XCD (workgroup i starts on XCD i % 8), whose L2 then has their weights once (700
+  // tokens, 2048 x 1408: 13.1 to 10.8 us; 1333: 17.5 to 16.4; 512, 7168 x 2048: 39 to 33)
+  const int xcd = blockIdx.x & 7, each = gridDim.x >> 3;
+  const int id = blocks == 1 ? blockIdx.x : xcd * each + min(xcd, (int)(gridDim.x & 7)) + (blockIdx.x >> 3);
+  const int cut = id % p.cuts, block = id / p.cuts % blocks;
+  const int t0 = (id / p.cuts / blocks * 4 + wave) * RT;                             // the wave's first tile
   const int m0 = block * NT * 16, M = min(p.M - m0, NT * 16);
   const int kb0 = (int)((int64_t)kb_n * cut / p.cuts), n = (int)((int64_t)kb_n * (cut + 1) / p.cuts) - kb0;
   // buffers end behind the last token and the last scale: what lies past them reads as zero
@@ -499,8 +503,8 @@ bool exact_products(const GatedFewProblem& p) {
   return p.M <= kGatedExactTokens && (p.gated.q != nullptr || p.out_fp32);
 }
 // 64 or 128 channels a workgroup: 128 where 64 give more workgroups than CUs (64 tokens,
-// 7168 x 18432: 58 us for 67; 1333 tokens, 2048 x 1408: 17.4 for 18.4; 512 tokens, 7168 x
-// 2048, 256 workgroups: 49 for 35)
+// 7168 x 18432: 58 us for 67; 1333 tokens, 2048 x 1408: 16.4 for 16.2, its codes 16.4 for 20.5;
+// 512 tokens, 7168 x 2048, 256 workgroups: 47 for 32)
 bool whole_tiles(const GatedFewProblem& p) {
   return p.M > 16 && !exact_products(p) && (p.M + 63) / 64 * (p.N / 64) > 256;
 }
@@ -716,10 +720,10 @@ __global__ __launch_bounds__(2048 / kGR, kWavesPerSimd) void gated_backward_kern
 
 // Which kernel.  The block GEMM's tiles are 128 tokens x 128 channels, one a CU: with
 // few of them most CUs idle, and workgroups of up to 64 tokens and 64 or 128 channels are
-// faster.  Measured, us, GEMM / these: 128 tokens, 7168 x 2048 (16 tiles) 55 / 17; 300, 2048 x
-// 1408 (33) 19 / 11; 512, 7168 x 2048 (64) 53 / 35; 1333, 2048 x 1408 (121) 20 / 17; 1024, 7168 x
-// 2048 (128) 52 / 50; 256, 2048 x 8192 (128) 21 / 24; 65, 7168 x 18432 (144) 66 / 86; 512, 7168 x
-// 7168 (224) 62 / 113.
+// faster.  Measured, us, GEMM / these: 128 tokens, 7168 x 2048 (16 tiles) 55 / 16; 300, 2048 x
+// 1408 (33) 19 / 11; 512, 7168 x 2048 (64) 53 / 33; 1333, 2048 x 1408 (121) 20 / 16; 1024, 7168 x
+// 2048 (128) 52 / 48; 256, 2048 x 8192 (128) 21 / 18; 1500, 2048 x 1408 (132) 21 / 21; 65, 7168 x
+// 18432 (144) 65 / 90; 2000, 2048 x 1408 (176) 19.5 / 22; 512, 7168 x 7168 (224) 62 / 75.
 // K is cut so that every CU has a workgroup; a cut adds partial sums and the
 // finishing launch, about what 6 to 8 blocks of K take: 48 tokens, 7168 x 2048, with 1 / 2
 // / 4 / 8 cuts 26 / 18 / 15 / 14; 256 tokens 29 / 24 / 24 / 30; 300 tokens, 2048 x 1408 11 / 14 / 18.
@@ -731,7 +735,7 @@ __global__ __launch_bounds__(2048 / kGR, kWavesPerSimd) void gated_backward_kern
 int gated_few_cuts(int64_t M, int64_t N, int64_t K, bool fp32) {
   const int64_t kb = K / 128;
   if (M <= 16) return (int)((kb + kMaxLds / kRowBlockLds - 1) / (kMaxLds / kRowBlockLds));
-  if (M > 64 && (M + 127) / 128 * (N / 128) >= 128) return 0;
+  if (M > 64 && (M + 127) / 128 * (N / 128) > 128) return 0;
   const int64_t groups = (M + 63) / 64 * (N / 64), worth = fp32 ? kb / 4 : (kb - 8) / 6;
   const int64_t c = std::min({256 / groups, worth, (int64_t)kGatedMaxCuts});
   return (int)(c > 1 ? c : 1);
