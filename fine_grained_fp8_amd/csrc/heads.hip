@@ -508,10 +508,10 @@ __global__ __launch_bounds__(1024) void head_grad_sum_kernel(const float* __rest
 
 // A lane has 2 R elements.  With 8 instead of 16 the backward pass's sums, weights and
 // heads in flight take about 100 registers instead of 160 - 190 (8192 tokens of 32 + 8
-// heads of 128, BF16: 60.5 us for 70.8; 5003 tokens of 16 + 16 heads of 80, FP32: 35.5 for
-// 46.7), and FP32 heads are still moved in 16-byte pieces (their forward pass 20.6 us for
-// 28.0).  BF16 forward keeps 16: both reach memory's rate (8192 tokens of 64 + 8 heads of
-// 128: 57 us, 302 MB).  Heads over 512 would take more than a wave with 8.
+// heads of 128, BF16: 56 us for 62; 5003 tokens of 16 + 16 heads of 80, FP32: 39 for 46),
+// and FP32 heads are still moved in 16-byte pieces (their forward pass 26 us for 31).
+// BF16 forward keeps 16, pieces of 16 bytes.  Heads over 512 would take more than a wave
+// with 8.
 int run_of(bool back, bool x_fp32, int64_t dim) { return (back || x_fp32) && dim <= 512 ? 4 : 8; }
 // lanes of a head
 int lanes_of(int64_t dim, int R) {
@@ -532,12 +532,12 @@ Shares forward_shares(const HeadProblem& p) {
   return share_out(p.T, passes(p.set[0].heads, G) + passes(p.set[1].heads, G), kForwardBlocks, 2);
 }
 
-// The backward pass: as many workgroups as run at once on 256 CUs, five a CU for BF16 and
-// four for FP32 by their registers, dealt to the sets by their heads.  Measured with 768 /
-// 1024 / 1280 / 2048, us: BF16, 8192 tokens of 32 + 8 heads of 128 70 / 61 / 53 / 55; FP32, 5003
-// tokens of 16 + 16 heads of 80 39 / 36 / 42 / 37.
-GradGrid divide(int64_t T, int64_t q_heads, int64_t k_heads, int64_t dim, bool x_fp32) {
-  const int64_t all = x_fp32 ? 1024 : kMaxGradParts;
+// The backward pass: as many workgroups as run at once on 256 CUs, five a CU by their
+// registers, dealt to the sets by their heads.  Measured with 768 / 1024 / 1280 / 2048, us:
+// BF16, 8192 tokens of 32 + 8 heads of 128 60 / 58 / 54 / 60; 20000 tokens of 16 + 4 heads of 64
+// 52 / 47 / 44 / 49; FP32, 5003 tokens of 16 + 16 heads of 80 39.4 / 39.3 / 38.5 / 38.7.
+GradGrid divide(int64_t T, int64_t q_heads, int64_t k_heads, int64_t dim) {
+  constexpr int64_t all = kMaxGradParts;
   const int G = lanes_of(dim, run_of(true, true, dim));
   const int64_t n[2] = {passes(q_heads, G), passes(k_heads, G)};
   GradGrid g{};
@@ -558,7 +558,7 @@ bool aligned_heads(const void* p, int64_t ld_token, int64_t ld_head, int64_t esz
 template <bool kBack, typename T, int kMode, int G, int R>
 void start(const HeadProblem& p, hipStream_t stream) {
   if constexpr (kBack) {
-    const GradGrid g = divide(p.T, p.set[0].heads, p.set[1].heads, p.dim, p.x_fp32);
+    const GradGrid g = divide(p.T, p.set[0].heads, p.set[1].heads, p.dim);
     const int64_t parts = g.set[0].blocks + g.set[1].blocks;
     hipLaunchKernelGGL((head_norm_rotary_backward_kernel<T, kMode, G, R>), dim3((unsigned)parts), dim3(kHB), 0, stream, p, g);
   } else {
@@ -612,13 +612,8 @@ hipError_t launch_head_norm_rotary(const HeadProblem& p, hipStream_t stream) {
 }
 
 int64_t head_grad_parts(int64_t T, int64_t q_heads, int64_t k_heads, int64_t dim) {
-  int64_t most = 0;
-  for (const bool x_fp32 : {false, true}) {
-    const GradGrid g = divide(T, q_heads, k_heads, dim, x_fp32);
-    const int64_t n = g.set[0].blocks + g.set[1].blocks;
-    if (n > most) most = n;
-  }
-  return most;
+  const GradGrid g = divide(T, q_heads, k_heads, dim);
+  return g.set[0].blocks + g.set[1].blocks;
 }
 
 hipError_t launch_head_norm_rotary_backward(const HeadProblem& p, hipStream_t stream) {
@@ -629,7 +624,7 @@ hipError_t launch_head_norm_rotary_backward(const HeadProblem& p, hipStream_t st
     if (st != hipSuccess) return st;
   }
   if (p.norm == kHeadNone || (p.set[0].dw == nullptr && p.set[1].dw == nullptr)) return hipSuccess;
-  const GradGrid g = divide(p.T, p.set[0].heads, p.set[1].heads, p.dim, p.x_fp32);
+  const GradGrid g = divide(p.T, p.set[0].heads, p.set[1].heads, p.dim);
   hipLaunchKernelGGL(head_grad_sum_kernel, dim3((unsigned)((p.dim + 15) / 16), 2), dim3(1024), 0, stream, p.partial,
                      g.set[0].blocks, g.set[1].blocks, p.dim, p.set[0].dw, p.set[1].dw);
   return hipGetLastError();
