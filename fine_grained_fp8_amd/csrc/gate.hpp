@@ -22,6 +22,7 @@ __device__ __forceinline__ float logistic(float v) {
 
 constexpr float kGeluA = 1.59576912f, kGeluB = 0.0713548163f;   // 2 sqrt(2/pi), and 0.044715 times it
 __device__ __forceinline__ float gelu_argument(float a) { return a * __builtin_fmaf(kGeluB, a * a, kGeluA); }
-__device__ __forceinline__ float gelu_argument_slope(float a) { return __builtin_fmaf(3.0f * kGeluB, a * a, kGeluA); }
+// finite for every finite a (it meets a factor that is 0 far out)
+__device__ __forceinline__ float gelu_argument_slope(float a) { return __builtin_fmaf(3.0f * kGeluB, fminf(a * a, 1e30f), kGeluA); }
 
 }  // namespace fp8bs

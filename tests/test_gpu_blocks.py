@@ -242,6 +242,22 @@ def test_gated_backward(gpu_lib, T, I, kind):
     assert torch.equal(qt, without[2]) and torch.equal(st, without[3])
 
 
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_gated_backward_of_far_gates(gpu_lib, kind):
+    """act'(a) is 1 or vanishes, without a NaN, up to the largest finite gates."""
+    far = torch.tensor([200.0, 1e10, 4e19, 1e20, 1e30, 3e38], dtype=torch.bfloat16, device="cuda")
+    for T in (2, 16500):                    # a set of values and all of them to a workgroup
+        dh = torch.full((T, 128), 2.0 ** -4, dtype=torch.bfloat16, device="cuda")
+        gu = torch.full((T, 256), 2.0, dtype=torch.bfloat16, device="cuda")
+        gu[:, :6], gu[:, 6:12] = far, -far
+        d = gpu_lib.gated_backward(dh, gu, activation=kind)
+        q, s, _, _, ht, sht = gpu_lib.gated_backward_quant(dh, gu, activation=kind, return_h=True)
+        assert d.isfinite().all() and s[:, :T].isfinite().all()
+        assert (d[:, :6] == 2.0 ** -3).all() and (d[:, 6:12] == 0).all()
+        assert torch.equal(d[:, 128:134], (far.float() * 2.0 ** -4).bfloat16().expand(T, 6)) and (d[:, 134:140] == 0).all()
+        assert ((q[:, 6:12] & 0x7F) == 0).all() and not ((q & 0x7F) == 0x7F).any()
+
+
 def test_gated_backward_against_differences(gpu_lib):
     g = np.random.default_rng(3)
     bf = lambda x: torch.from_numpy(x).bfloat16()
