@@ -14,8 +14,12 @@
 namespace {
 
 constexpr int64_t kMaxLd = int64_t{1} << 28;
-constexpr int64_t kMaxBlocks = int64_t{1} << 22;   // a launch holds less than 2^32 threads, here 512 a workgroup
+constexpr int64_t kMaxBlocks = int64_t{1} << 22;   // a launch holds less than 2^32 threads, here up to 1024 a workgroup
 constexpr int64_t kMaxTokens = int64_t{1} << 31;
+
+// Rows at a stride that would end past 2^45 elements: more than any memory, and byte
+// offsets stay far from 2^63.
+bool too_far(int64_t rows, int64_t ld) { return ld > (int64_t{1} << 45) / (rows > 1 ? rows : 1); }
 
 bool aligned_to(const void* p, int64_t bytes) { return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(bytes - 1)) == 0; }
 int64_t up128(int64_t n) { return (n + 127) / 128 * 128; }
@@ -233,9 +237,8 @@ fp8_status fp8_gated_backward(int64_t T, int64_t I, const void* dh, int64_t ld_d
   if (ld_dh < I || ld_gu < 2 * I || (d && ld_d < 2 * I) || (q && (ldq < 2 * I || ld_s < T)) ||
       (qt && (ldqt < Tp || ld_st < 2 * I)) || (ht && ld_sht < I))
     return FP8_ERR_LD;
-  constexpr int64_t kMost = int64_t{1} << 40;
-  if (ld_dh > kMost || ld_gu > kMost || (d && ld_d > kMost) || (q && (ldq > kMost || ld_s > kMost)) ||
-      (qt && (ldqt > kMost || ld_st > kMost)) || (ht && ld_sht > kMost))
+  if (too_far(T, ld_dh) || too_far(T, ld_gu) || (d && too_far(T, ld_d)) || (q && (too_far(T, ldq) || too_far(2 * I / 128, ld_s))) ||
+      (qt && (too_far(2 * I, ldqt) || too_far(Tp / 128, ld_st))) || (ht && too_far(Tp / 128, ld_sht)))
     return FP8_ERR_UNSUPPORTED;
   if (!aligned16(dh) || ld_dh % 8 != 0 || !aligned16(gate_up) || ld_gu % 8 != 0 || !aligned16(d) || (d && ld_d % 8 != 0) ||
       !aligned16(q) || (q && ldq % 16 != 0) || !aligned16(qt) || (qt && ldqt % 16 != 0) || !aligned16(ht) ||
@@ -268,7 +271,7 @@ fp8_status fp8_quant_act_cols(const void* x, int64_t rows, int64_t cols, int64_t
   if (rows == 0 || cols == 0) return FP8_OK;
   if (!x || !q || !scales) return FP8_ERR_NULL;
   if (ldx < cols || ld_s < cols) return FP8_ERR_LD;
-  if (ldx > int64_t{1} << 40 || ld_s > int64_t{1} << 40) return FP8_ERR_UNSUPPORTED;
+  if (too_far(rows, ldx) || too_far(up128(rows) / 128, ld_s)) return FP8_ERR_UNSUPPORTED;
   if (!aligned16(x) || ldx % 8 != 0 || !aligned16(q) || !aligned4(scales)) return FP8_ERR_ALIGN;
   const Range in[1] = {span(x, rows, cols * 2, ldx * 2)};
   const Range out[2] = {span(q, 1, cols * up128(rows), 0), span(scales, up128(rows) / 128, cols * 4, ld_s * 4)};
@@ -291,7 +294,6 @@ fp8_status fp8_head_norm_rotary(int64_t tokens, int64_t dim, fp8_out_dtype x_dty
   if (st != FP8_OK) return st;
   if (tokens == 0) return FP8_OK;
   const int64_t e = x_dtype == FP8_OUT_FP32 ? 4 : 2, we = w_dtype == FP8_OUT_FP32 ? 4 : 2;
-  constexpr int64_t kMost = int64_t{1} << 40;
   Placed x[2]{}, y[2]{};
   Range w[2]{};
   for (int i = 0; i < 2; ++i) {
@@ -299,7 +301,8 @@ fp8_status fp8_head_norm_rotary(int64_t tokens, int64_t dim, fp8_out_dtype x_dty
     if (h.heads == 0) continue;
     if (!h.x || !h.y) return FP8_ERR_NULL;
     if (h.weight && norm == FP8_HEAD_NONE) return FP8_ERR_UNSUPPORTED;
-    if (h.ld_token > kMost || h.ld_head > kMost || h.ldy_token > kMost || h.ldy_head > kMost) return FP8_ERR_UNSUPPORTED;
+    if (too_far(tokens, h.ld_token) || too_far(h.heads, h.ld_head) || too_far(tokens, h.ldy_token) || too_far(h.heads, h.ldy_head))
+      return FP8_ERR_UNSUPPORTED;
     if (!heads_nested(tokens, h.heads, dim, h.ld_token, h.ld_head) || !heads_nested(tokens, h.heads, dim, h.ldy_token, h.ldy_head))
       return FP8_ERR_LD;
     if (!aligned_to(h.x, e) || !aligned_to(h.y, e) || !aligned_to(h.weight, we)) return FP8_ERR_ALIGN;
@@ -349,7 +352,6 @@ fp8_status fp8_head_norm_rotary_backward(int64_t tokens, int64_t dim, fp8_out_dt
   if (workspace_bytes < need) return FP8_ERR_SHAPE;
   if (need > 0 && !aligned16(workspace)) return FP8_ERR_ALIGN;
   const int64_t e = x_dtype == FP8_OUT_FP32 ? 4 : 2, we = w_dtype == FP8_OUT_FP32 ? 4 : 2;
-  constexpr int64_t kMost = int64_t{1} << 40;
   Placed in[2][2]{}, dx[2]{};
   Range w[2]{}, dw[2]{};
   for (int i = 0; i < 2; ++i) {
@@ -357,8 +359,8 @@ fp8_status fp8_head_norm_rotary_backward(int64_t tokens, int64_t dim, fp8_out_dt
     if (h.heads == 0) continue;
     if (tokens > 0) {
       if ((normed && !h.x) || !h.dy || !h.dx) return FP8_ERR_NULL;
-      if ((normed && (h.ld_token > kMost || h.ld_head > kMost)) || h.lddy_token > kMost || h.lddy_head > kMost ||
-          h.lddx_token > kMost || h.lddx_head > kMost)
+      if ((normed && (too_far(tokens, h.ld_token) || too_far(h.heads, h.ld_head))) || too_far(tokens, h.lddy_token) ||
+          too_far(h.heads, h.lddy_head) || too_far(tokens, h.lddx_token) || too_far(h.heads, h.lddx_head))
         return FP8_ERR_UNSUPPORTED;
       if ((normed && !heads_nested(tokens, h.heads, dim, h.ld_token, h.ld_head)) ||
           !heads_nested(tokens, h.heads, dim, h.lddy_token, h.lddy_head) ||

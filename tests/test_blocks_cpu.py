@@ -105,6 +105,8 @@ def test_gated_backward_validation(lib):
                  ("ld_sht", 255)):
         assert back(lib, **{k: v}) == LD, k
         assert back(lib, **{k: 1 << 60}) == UNSUP, k
+    for k in ("ld_dh", "ld_gu", "ld_d", "ldq", "ldqt"):      # no overflow on the way
+        assert back(lib, **{**dict(T=1 << 28, I=128, ldqt=1 << 28, ld_s=1 << 28), k: 1 << 40}) == UNSUP, k
     for k, v in (("ld_dh", 260), ("ld_gu", 516), ("ld_d", 516), ("ldq", 520), ("ldqt", 264)):
         assert back(lib, **{k: v}) == ALIGN, k
     for k in ("dh", "gu", "d", "q", "qt", "ht"):
@@ -132,6 +134,7 @@ def test_quant_act_cols_validation(lib):
         assert cols(lib, **{k: 248}) == LD and cols(lib, **{k: 1 << 60}) == UNSUP
     for k, v in (("x", P[0] + 2), ("q", P[1] + 8), ("s", P[2] + 2), ("ldx", 260)):
         assert cols(lib, **{k: v}) == ALIGN
+    assert cols(lib, rows=1 << 28, cols=128, ldx=1 << 40) == UNSUP      # no overflow on the way
     assert cols(lib, q=P[0]) == ALIAS and cols(lib, s=P[0]) == ALIAS and cols(lib, s=P[1] + 256) == ALIAS
     assert cols(lib, s=P[1] + 256 * 256 - 4) == ALIAS    # the padded columns of codes count
 
@@ -168,6 +171,10 @@ def test_head_norm_rotary_validation(lib):
     for c in (dict(xt=2), dict(wt=2), dict(norm=3), dict(dim=1026), dict(T=1 << 40), dict(axes=0), dict(axes=5, sections=[32, 0, 0, 0, 0]),
               dict(pbytes=2), dict(norm=0)):      # norm 0 with weights
         assert heads(lib, **c) == UNSUP, c
+    for n in ("ld_token", "ldy_token"):                       # no overflow on the way
+        assert heads(lib, T=1 << 25, q={n: 1 << 40}) == UNSUP, n
+    assert heads(lib, q=dict(heads=1 << 20, ld_head=1 << 40)) == UNSUP
+    assert heads(lib, T=1, q=dict(ld_token=1 << 44)) in PASSED
     assert heads(lib, norm=0, q=dict(weight=None), k=dict(weight=None)) in PASSED
     assert heads(lib, q=dict(heads=1 << 30)) == UNSUP and heads(lib, q=dict(ld_token=1 << 60)) == UNSUP
     for c in (dict(pos=None), dict(freq=None), dict(axes=2), dict(q=dict(x=None)), dict(k=dict(y=None))):
@@ -230,6 +237,8 @@ def test_head_norm_rotary_backward_validation(lib):
         assert hback(lib, q={n: 1 << 60}) == UNSUP, n
     for n in ("x", "dy", "dx", "weight", "dweight"):
         assert hback(lib, q={n: P[12] + 2}) == ALIGN, n
+    for n in ("ld_token", "lddy_token", "lddx_token"):
+        assert hback(lib, T=1 << 25, q={n: 1 << 40}) == UNSUP, n
     assert hback(lib, ws=P[11] + 8) == ALIGN
     for c in (dict(q=dict(dx=P[0])), dict(q=dict(dx=P[6])), dict(q=dict(dx=P[7])), dict(k=dict(dx=P[10])), dict(q=dict(dweight=P[9])),
               dict(k=dict(dweight=P[4] + 4)), dict(q=dict(dweight=P[1])), dict(ws=P[0]), dict(ws=P[1]), dict(ws=P[3]), dict(ws=P[8]),
