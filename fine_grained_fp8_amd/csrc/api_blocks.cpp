@@ -345,7 +345,7 @@ fp8_status fp8_head_norm_rotary_backward(int64_t tokens, int64_t dim, fp8_out_dt
   if (st != FP8_OK) return st;
   const bool normed = norm != FP8_HEAD_NONE;
   for (const fp8_heads_grad* h : sets)
-    if (h->heads > 0 && !normed && (h->weight || h->dweight)) return FP8_ERR_UNSUPPORTED;
+    if (!normed && ((h->heads > 0 && h->weight) || h->dweight)) return FP8_ERR_UNSUPPORTED;
   if (tokens == 0 && !sets[0]->dweight && !sets[1]->dweight) return FP8_OK;
   const int64_t need = normed ? fp8_head_norm_rotary_backward_workspace(tokens, sets[0]->heads, sets[1]->heads, dim) : 0;
   if (need > 0 && !workspace) return FP8_ERR_NULL;
@@ -356,7 +356,12 @@ fp8_status fp8_head_norm_rotary_backward(int64_t tokens, int64_t dim, fp8_out_dt
   Range w[2]{}, dw[2]{};
   for (int i = 0; i < 2; ++i) {
     const fp8_heads_grad& h = *sets[i];
-    if (h.heads == 0) continue;
+    if (h.heads == 0) {                       // no heads, but a gradient of zeros may be asked for
+      if (!aligned4(h.dweight)) return FP8_ERR_ALIGN;
+      dw[i] = span(h.dweight, h.dweight ? 1 : 0, dim * 4, 0);
+      p.set[i].dw = h.dweight;
+      continue;
+    }
     if (tokens > 0) {
       if ((normed && !h.x) || !h.dy || !h.dx) return FP8_ERR_NULL;
       if ((normed && (too_far(tokens, h.ld_token) || too_far(h.heads, h.ld_head))) || too_far(tokens, h.lddy_token) ||

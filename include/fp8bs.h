@@ -660,8 +660,8 @@ fp8_status fp8_head_norm_rotary(int64_t tokens, int64_t dim, fp8_out_dtype x_dty
  * statistics are formed anew).
  *  x, weight  as in the forward pass (x is not read with FP8_HEAD_NONE and may be NULL)
  *  dy, dx     of x_dtype, [tokens][heads][dim] at strides as x's
- *  dweight    optional FP32 [dim]: the sum over tokens and heads (tokens == 0 writes
- *             zeros); none with FP8_HEAD_NONE.  Fixed order: results repeat bit for bit.
+ *  dweight    optional FP32 [dim]: the sum over tokens and heads (tokens == 0 or heads == 0
+ *             writes zeros); none with FP8_HEAD_NONE.  Fixed order: results repeat bit for bit.
  */
 typedef struct {
   const void* x;

@@ -229,6 +229,10 @@ def test_head_norm_rotary_backward_validation(lib):
     assert hback(lib, norm=0, q=no, k=no, ws=None, bytes=0) in PASSED
     assert hback(lib, norm=0, q=no) == UNSUP and hback(lib, norm=0, q=no, k=dict(no, dweight=P[8])) == UNSUP
     assert hback(lib, T=0, q=dict(dweight=None), k=dict(dweight=None), ws=None) == OK
+    empty = dict(heads=0, x=None, dy=None, dx=None, weight=None)     # its dweight is written all the same
+    assert hback(lib, k=empty) in PASSED and hback(lib, k=dict(empty, dweight=None)) in PASSED
+    assert hback(lib, norm=0, q=no, k=empty) == UNSUP and hback(lib, k=dict(empty, dweight=P[8] + 2)) == ALIGN
+    assert hback(lib, k=dict(empty, dweight=P[0])) == ALIAS and hback(lib, k=dict(empty, dweight=P[4])) == ALIAS
     for c in (dict(ws=None), dict(q=dict(x=None)), dict(q=dict(dy=None)), dict(k=dict(dx=None)), dict(pos=None)):
         assert hback(lib, **c) == NULL, c
     assert hback(lib, bytes=100) == SHAPE and hback(lib, dim=62, rot=64) == SHAPE

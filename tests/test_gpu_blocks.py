@@ -550,6 +550,22 @@ def test_heads_empty(gpu_lib):
     assert dq.shape == (0, 4, 64) and dk is None and wk is None and (wq == 0).all()
 
 
+def test_a_set_without_heads(gpu_lib):
+    """It has results without heads and a gradient of zeros; the other set is as alone."""
+    T = 300
+    none = torch.empty(T, 0, 64, device="cuda")
+    k, dk = rand((T, 3, 64), 91, torch.float32), rand((T, 3, 64), 92, torch.float32)
+    w = rand((64,), 93, torch.float32)
+    rotary = torch.arange(T, device="cuda"), dev(0.9 ** np.arange(32))
+    y, yk = gpu_lib.head_norm_rotary(none, k, *rotary, q_weight=w, k_weight=w)
+    assert y.shape == (T, 0, 64) and torch.equal(yk, gpu_lib.head_norm_rotary(None, k, *rotary, k_weight=w)[1])
+    alone = gpu_lib.head_norm_rotary_backward(None, dk, None, k, *rotary, k_weight=w)
+    torch.full((4096,), float("nan"), device="cuda")           # what the next allocation holds
+    dq, dx, dwq, dwk = gpu_lib.head_norm_rotary_backward(none, dk, none, k, *rotary, q_weight=w, k_weight=w)
+    assert dq.shape == (T, 0, 64) and dwq.shape == (64,) and (dwq == 0).all()
+    assert torch.equal(dx, alone[1]) and torch.equal(dwk, alone[3])
+
+
 def test_rows_past_32_bit_offsets(gpu_lib):
     """Heads and gates whose elements lie more than 2^31 (2^32 bytes) into their arrays."""
     T, H, D = 70000, 256, 128                     # 2.3e9 elements
