@@ -11,6 +11,10 @@ request or their prompts; the expert layer takes up to 64 tokens at a time.
 train_step(): layer norm with the fused 1x128 quantization into the FP8 Fprop
 product, and back: Dgrad and Wgrad on FP8 codes, then the norm's gradients.
 
+dense_step(): the block's parts with dense weights, forward and backward, for any
+number of tokens: layer norm with codes, the query/key/value projection, the head
+norms with the rotation, and a gated feed-forward block on FP8 codes throughout.
+
 Random weights; needs an MI355X and the built library.
 """
 import argparse
@@ -70,6 +74,66 @@ def train_step(x, norm, w_bf16, dy):
     return y, dx, dw, dnorm_w, dnorm_b
 
 
+class Dense:
+    """Weights of a dense block in both orientations' codes."""
+
+    def __init__(self, hidden, inner, heads=8, kv_heads=2, dim=64, base=10000.0):
+        self.heads, self.kv_heads, self.dim, self.inner = heads, kv_heads, dim, inner
+        self.norm = torch.ones(hidden, device="cuda"), torch.zeros(hidden, device="cuda")
+        self.q_weight, self.k_weight = torch.ones(dim, device="cuda"), torch.ones(dim, device="cuda")
+        self.freq = base ** (-torch.arange(dim // 2, device="cuda", dtype=torch.float64) / (dim // 2))
+        std = hidden ** -0.5
+        self.weights = {"qkv": std * torch.randn((heads + 2 * kv_heads) * dim, hidden, device="cuda"),
+                        "w13": std * torch.randn(2 * inner, hidden, device="cuda"),
+                        "w2": inner ** -0.5 * torch.randn(hidden, inner, device="cuda")}
+        self.weights = {name: w.bfloat16() for name, w in self.weights.items()}
+        self.codes = {name: fp8.quant_weight_128x128(w, transposed=True, tiled=True) for name, w in self.weights.items()}
+
+    def split(self, qkv):
+        """[tokens][channels] -> queries, keys, values [tokens][heads][dim], in place."""
+        t = qkv.view(qkv.shape[0], -1, self.dim)
+        return t[:, :self.heads], t[:, self.heads:-self.kv_heads], t[:, -self.kv_heads:]
+
+
+def dense_step(block, x, positions, dq, dk, dv, dy):
+    """q, k, v = the rotated heads of norm(x), y = W2 (act(W1 n) * (W3 n)) of the same
+    n = norm(x), and the gradients for given ones of q, k, v and y: dn, and those
+    of the weights."""
+    rows = x.shape[0]
+    codes, s, n = fp8.layer_norm_quant(x, *block.norm, return_y=True)
+    w, sw, wt = block.codes["qkv"]
+    qkv = fp8.block_gemm("fprop_tiled", codes, s, w, sw)
+    heads = block.split(qkv)
+    rotary = dict(positions=positions, freq=block.freq, q_weight=block.q_weight, k_weight=block.k_weight)
+    q, k = fp8.head_norm_rotary(heads[0], heads[1], **rotary)
+    w13, s13, w13t = block.codes["w13"]
+    w2, s2, w2t = block.codes["w2"]
+    hq, hs, gate_up = fp8.block_gemm_gated_quant(codes, s, w13, s13, return_gate_up=True)
+    y = fp8.block_gemm("fprop_tiled", hq, hs, w2, s2)
+
+    nt, nst = fp8.quant_act_cols(n)
+    # the feed-forward block
+    dyq, dys, _ = fp8.quant_act_1x128(dy)
+    dh = fp8.block_gemm("dgrad_t_tiled", dyq, dys, w2t, s2)
+    dgu, dgus, dgut, dgust, ht, hst = fp8.gated_backward_quant(dh, gate_up, return_h=True)
+    dn_ff = fp8.block_gemm("dgrad_t_tiled", dgu, dgus, w13t, s13)
+    dw13 = fp8.block_gemm("wgrad_tiled", dgut, dgust, nt, nst, out_dtype=torch.float32)
+    padded = torch.zeros((rows + 127) // 128 * 128, dy.shape[1], dtype=dy.dtype, device=dy.device)
+    padded[:rows] = dy
+    dyt, dyst, _ = fp8.quant_act_1x128(padded, "col")
+    dw2 = fp8.block_gemm("wgrad_tiled", dyt, dyst, ht, hst, out_dtype=torch.float32)
+    # the heads: their gradients beside dv in the projection's rows
+    dqkv = torch.zeros(padded.shape[0], qkv.shape[1], dtype=x.dtype, device=x.device)
+    into = block.split(dqkv[:rows])
+    _, _, dq_weight, dk_weight = fp8.head_norm_rotary_backward(dq, dk, heads[0], heads[1], **rotary, out=into[:2])
+    into[2].copy_(dv)
+    dp, dps, dpt, dpst = fp8.quant_act_dual(dqkv)
+    dn_heads = fp8.block_gemm("dgrad_t_tiled", dp, dps, wt, sw)[:rows]
+    dqkv_w = fp8.block_gemm("wgrad_tiled", dpt, dpst, nt, nst, out_dtype=torch.float32)
+    return (q, k, heads[2], y), {"n": dn_ff + dn_heads, "qkv": dqkv_w, "w13": dw13, "w2": dw2, "q_weight": dq_weight,
+                                 "k_weight": dk_weight}
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--hidden", type=int, default=7168)
@@ -95,6 +159,13 @@ def main():
     out = train_step(x, block.norm1, w, dy)
     torch.cuda.synchronize()
     print("train step: " + ", ".join(f"{n} {tuple(t.shape)}" for n, t in zip(("y", "dx", "dw", "dnorm_w", "dnorm_b"), out)))
+    rows = 1000
+    dense = Dense(args.hidden, args.inner)
+    x, dy = torch.randn(2, rows, args.hidden, device="cuda").bfloat16()
+    dq, dk, dv = (torch.randn(rows, h, dense.dim, device="cuda").bfloat16() for h in (8, 2, 2))
+    _, grads = dense_step(dense, x, torch.arange(rows, device="cuda"), dq, dk, dv, dy)
+    torch.cuda.synchronize()
+    print("dense step: " + ", ".join(f"{n} {tuple(t.shape)}" for n, t in grads.items()))
 
 
 if __name__ == "__main__":

@@ -313,6 +313,46 @@ def test_quant_act_cols(gpu_lib, rows, cols):
     assert np.array_equal(s.t().cpu().numpy(), sw)
 
 
+def test_the_dense_example_and_its_gradients(gpu_lib):
+    """Norm, projection, heads and feed-forward block as the example joins them, ragged
+    tokens, against the unquantized computation in FP64 and its gradients there."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import decoder_block as ex
+    torch.manual_seed(3)
+    T, H = 333, 256
+    b = ex.Dense(H, 384, heads=8, kv_heads=2, dim=64)
+    b.q_weight += 0.3 * torch.randn(64, device="cuda")
+    b.k_weight += 0.3 * torch.randn(64, device="cuda")
+    x = rand((T, H), 61, torch.bfloat16)
+    dq, dk, dv = (rand((T, h, 64), 62 + h, torch.bfloat16, std=0.1) for h in (8, 2, 2))
+    dy = rand((T, H), 66, torch.bfloat16, std=0.1)
+    pos = torch.arange(T, device="cuda") + 5000
+    outs, grads = ex.dense_step(b, x, pos, dq, dk, dv, dy)
+
+    leaf = lambda t: t.detach().double().cpu().requires_grad_()
+    n = leaf(torch.nn.functional.layer_norm(x.double(), (H,), eps=1e-5))
+    w = {k: leaf(v) for k, v in b.weights.items()}
+    qw, kw = leaf(b.q_weight), leaf(b.k_weight)
+    t = (n @ w["qkv"].T).view(T, 12, 64)
+    turn = pos.cpu().double()[:, None, None] * b.freq.cpu()
+    c, s = turn.cos(), turn.sin()
+
+    def rotated(h, weight):
+        h = h / (h.square().mean(-1, keepdim=True) + 1e-6).sqrt() * weight
+        return torch.cat([h[..., :32] * c - h[..., 32:] * s, h[..., 32:] * c + h[..., :32] * s], -1)
+    gu = n @ w["w13"].T
+    want = rotated(t[:, :8], qw), rotated(t[:, 8:10], kw), t[:, 10:], torch.nn.functional.silu(gu[:, :384]) * gu[:, 384:] @ w["w2"].T
+    torch.autograd.backward(want, [g.double().cpu() for g in (dq, dk, dv, dy)])
+    # E4M3 rounds each operand by at most 2^-4; two to four quantized products follow each other
+    bound = 4 * 2.0 ** -4
+    names = dict(n=n, **w, q_weight=qw, k_weight=kw)
+    for got, ref in [*zip(outs, want), *((grads[k], v.grad) for k, v in names.items())]:
+        ref = ref.detach().numpy()
+        assert np.linalg.norm(host(got) - ref) <= bound * np.linalg.norm(ref)
+
+
 def test_a_whole_feed_forward_block_and_its_gradients(gpu_lib):
     """x -> codes -> gated product -> down product, and back, ragged tokens: the
     operators together, on the codes that they hand to each other."""
