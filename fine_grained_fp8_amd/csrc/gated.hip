@@ -735,12 +735,17 @@ __global__ __launch_bounds__(2048 / kGR, kWavesPerSimd) void gated_backward_kern
 
 }  // namespace
 
-// Which kernel.  The block GEMM's tiles are 128 tokens x 128 channels, one a CU: with
-// few of them most CUs idle, and workgroups of up to 64 tokens and 64 or 128 channels are
-// faster.  Measured, us, GEMM / these: 128 tokens, 7168 x 2048 (16 tiles) 55 / 16; 300, 2048 x
-// 1408 (33) 19 / 11; 512, 7168 x 2048 (64) 53 / 33; 1333, 2048 x 1408 (121) 20 / 16; 1024, 7168 x
-// 2048 (128) 52 / 48; 256, 2048 x 8192 (128) 21 / 18; 1500, 2048 x 1408 (132) 21 / 21; 65, 7168 x
-// 18432 (144) 65 / 90; 2000, 2048 x 1408 (176) 19.5 / 22; 512, 7168 x 7168 (224) 62 / 75.
+// Which kernel.  The block GEMM's tiles are 128 tokens x 128 channels, one a CU; with
+// few of them most CUs idle, and just above 256 the second round is a short one.  There
+// workgroups of up to 64 tokens and 64 or 128 channels are faster: while those of 128
+// channels are one round of the CUs, and up to 640 of them where the GEMM takes two.
+// Measured, us, GEMM / these (tiles; workgroups of 128): 128 tokens, 7168 x 2048 (16; 32) 55 / 16;
+// 300, 2048 x 1408 (33; 55) 19 / 10; 1333, 2048 x 1408 (121; 231) 20 / 15; 1024, 7168 x 2048
+// (128; 256) 53 / 39; 300, 7168 x 6400 (150; 250) 55 / 39; 450, 7168 x 4608 (144; 288) 52 / 57;
+// 65, 7168 x 18432 (144; 288) 64 / 83; 1333, 2048 x 2048 (176; 336) 20 / 21; 512, 7168 x 7168
+// (224; 448) 59 / 67; 2700, 2048 x 1408 (242; 473) 22 / 25; 700, 7168 x 5632 (264; 484) 89 / 68;
+// 192, 7168 x 18432 (288; 432) 107 / 82; 1333, 2048 x 3840 (330; 630) 40 / 33; 640, 2048 x 8192
+// (320; 640) 38 / 38; 4096, 2048 x 1408 (352; 704) 36 / 34; 800, 2048 x 8192 (448; 832) 38 / 44.
 // K is cut so that every CU has a workgroup; a cut adds partial sums and the
 // finishing launch, about what 6 to 8 blocks of K take: 48 tokens, 7168 x 2048, with 1 / 2
 // / 4 / 8 cuts 26 / 18 / 15 / 14; 256 tokens 29 / 24 / 24 / 30; 300 tokens, 2048 x 1408 11 / 14 / 18.
@@ -752,7 +757,8 @@ __global__ __launch_bounds__(2048 / kGR, kWavesPerSimd) void gated_backward_kern
 int gated_few_cuts(int64_t M, int64_t N, int64_t K, bool fp32) {
   const int64_t kb = K / 128;
   if (M <= 16) return (int)((kb + kMaxLds / kRowBlockLds - 1) / (kMaxLds / kRowBlockLds));
-  if (M > 64 && (M + 127) / 128 * (N / 128) > 128) return 0;
+  const int64_t tiles = (M + 127) / 128 * (N / 128), wide = (M + 63) / 64 * (N / 128);
+  if (M > 64 && wide > 256 && (tiles <= 256 || wide > 640)) return 0;
   const int64_t groups = (M + 63) / 64 * (N / 64), worth = fp32 ? kb / 4 : (kb - 8) / 6;
   const int64_t c = std::min({256 / groups, worth, (int64_t)kGatedMaxCuts});
   return (int)(c > 1 ? c : 1);

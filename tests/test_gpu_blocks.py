@@ -97,7 +97,8 @@ GATED = [  # M, K, I, kind
     (17, 2048, 128, "silu"), (31, 640, 512, "gelu"), (33, 256, 4224, "silu"), (48, 1024, 256, "silu"), (49, 512, 8320, "gelu"),
     (64, 128, 384, "silu"), (64, 896, 2176, "gelu"), (5, 16384, 128, "silu"), (33, 4096, 256, "gelu"), (40, 384, 16384, "silu"),
     (65, 4096, 128, "gelu"), (200, 8192, 256, "silu"), (1000, 256, 1920, "gelu"), (65, 128, 128, "silu"), (90, 256, 16384, "silu"), (100, 384, 256, "gelu"), (128, 512, 128, "silu"), (129, 1024, 384, "silu"), (300, 640, 1408, "gelu"),
-    (1333, 256, 512, "silu"),
+    (1333, 256, 512, "silu"), (700, 2560, 512, "gelu"), (333, 2944, 256, "silu"),
+    (450, 256, 4608, "silu"), (129, 384, 11264, "gelu"), (2300, 640, 1408, "gelu"), (1111, 128, 3840, "silu"),
 ]
 
 
@@ -125,8 +126,8 @@ def test_block_gemm_gated(gpu_lib, case):
 
 
 def test_gated_split_tail_and_wide_few(gpu_lib):
-    """272 tiles (16 of them cut along K on 256 CUs), and a few tokens at a wide output."""
-    for M, K, I in ((2100, 1024, 2048), (700, 1024, 2560), (3, 7168, 2048), (20, 1024, 18432), (7, 1024, 18432)):
+    """352 tiles (96 of them cut along K on 256 CUs), and a few tokens at a wide output."""
+    for M, K, I in ((2700, 1024, 2048), (2100, 1024, 2048), (700, 1024, 2560), (3, 7168, 2048), (20, 1024, 18432), (7, 1024, 18432)):
         g = Gated(M, K, I, "silu", seed=5)
         rows = np.unique(np.concatenate([np.arange(0, M, 97), [M - 1]]))
         y = gpu_lib.block_gemm_gated(*g.args, out_dtype=torch.float32)
@@ -142,16 +143,17 @@ def test_gated_split_tail_and_wide_few(gpu_lib):
 
 def test_gated_equals_the_plain_products(gpu_lib):
     """More than 64 tokens: a and u are the block GEMM's own sums."""
-    g = Gated(200, 512, 384, "silu", seed=9)
-    A, sA, w, sw = g.args
-    _, kept = gpu_lib.block_gemm_gated(A, sA, w, sw, return_gate_up=True)
-    assert torch.equal(kept, gpu_lib.block_gemm("fprop_tiled", A, sA, w, sw))
+    for M, I in ((200, 384), (450, 4608)):
+        g = Gated(M, 512, I, "silu", seed=9)
+        A, sA, w, sw = g.args
+        _, kept = gpu_lib.block_gemm_gated(A, sA, w, sw, return_gate_up=True)
+        assert torch.equal(kept, gpu_lib.block_gemm("fprop_tiled", A, sA, w, sw))
 
 
-@pytest.mark.parametrize("M", [9, 50, 150])
-def test_gated_strides_and_rows_behind(gpu_lib, M):
+@pytest.mark.parametrize("M,I", [(9, 384), (50, 384), (150, 384), (450, 4608)])
+def test_gated_strides_and_rows_behind(gpu_lib, M, I):
     """Operands and outputs inside larger arrays: nothing else is written."""
-    K, I = 256, 384
+    K = 256
     g = Gated(M, K, I, "silu", seed=11)
     A, sA, w, sw = g.args
     bigA = torch.full((M + 3, K + 48), 0x7F, dtype=torch.uint8, device="cuda")
@@ -167,10 +169,10 @@ def test_gated_strides_and_rows_behind(gpu_lib, M):
     assert (out[M:] == 7).all() and (out[:, :8] == 7).all() and (out[:, 8 + I:] == 7).all()
 
 
-@pytest.mark.parametrize("M", [5, 40, 130])
+@pytest.mark.parametrize("M,I", [(5, 256), (40, 256), (130, 256), (450, 4608)])
 @pytest.mark.parametrize("kind", ["silu", "gelu"])
-def test_gated_nonfinite_tokens_stay_apart(gpu_lib, M, kind):
-    g = Gated(M, 256, 256, kind, seed=13)
+def test_gated_nonfinite_tokens_stay_apart(gpu_lib, M, I, kind):
+    g = Gated(M, 256, I, kind, seed=13)
     A, sA, w, sw = g.args
     clean = gpu_lib.block_gemm_gated(A, sA, w, sw, activation=kind)
     qc, sc = gpu_lib.block_gemm_gated_quant(A, sA, w, sw, activation=kind)
@@ -188,7 +190,7 @@ def test_gated_nonfinite_tokens_stay_apart(gpu_lib, M, kind):
 def test_gated_far_gates(gpu_lib):
     """Gates far on both sides: act(a) is a, or vanishes without a NaN."""
     K = 128
-    for M in (4, 100):
+    for M in (4, 100, 42000):
         A = torch.full((M, K), 0x7E, dtype=torch.uint8, device="cuda")        # 448
         sA = torch.ones(1, (M + 3) // 4 * 4, device="cuda")
         w = np.full((512, K), 0x7E, np.uint8)
@@ -647,6 +649,8 @@ def block_calls(gpu_lib, seed=101):
         dq, dk = rand((M, 8, 128), seed + 5, torch.bfloat16), rand((M, 2, 128), seed + 6, torch.bfloat16)
         calls.append(([dq, dk, q, pos], lambda dq, dk, q, pos, k=k, freq=freq:
                       gpu_lib.head_norm_rotary_backward(dq, dk, q, k, pos, freq)))
+    A, sA, w, sw = Gated(450, 256, 4608, "silu", seed=seed).args           # the block GEMM's kernel
+    calls.append(([A], lambda A: gpu_lib.block_gemm_gated(A, sA, w, sw, return_gate_up=True)))
     return calls
 
 
@@ -680,7 +684,7 @@ def test_blocks_replay_from_graphs(gpu_lib):
 def test_two_graphs_of_the_gated_product_at_once(gpu_lib):
     """Two captures of a product whose tail is cut along K when it runs eagerly,
     replayed on two streams at once."""
-    g = [Gated(2100, 512, 2048, "silu", seed=s) for s in (111, 112)]
+    g = [Gated(2700, 512, 2048, "silu", seed=s) for s in (111, 112)]
     want = [gpu_lib.block_gemm_gated(*x.args, out_dtype=torch.float32) for x in g]
     graphs, outs = [], []
     for x in g:
