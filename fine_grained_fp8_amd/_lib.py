@@ -87,7 +87,7 @@ SIGNATURES = {
     "fp8_adapter_linear_workspace": (_I64, [_I64, _I64, _I64, _I32, _I32]),
     "fp8_block_gemm_gated": (ctypes.c_int, [_I64, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _I64, ctypes.c_int, _P,
                                             ctypes.c_int, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P]),
-    "fp8_block_gemm_gated_workspace": (_I64, [_I64, _I64, _I64]),
+    "fp8_block_gemm_gated_workspace": (_I64, [_I64, _I64, _I64, ctypes.c_int, _I32]),
     "fp8_gated_backward": (ctypes.c_int, [_I64, _I64, _P, _I64, _P, _I64, ctypes.c_int, _P, _I64, _P, _I64, _P, _I64,
                                           _P, _I64, _P, _I64, _P, _P, _I64, _P]),
     "fp8_quant_act_cols": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _I64, _P]),

@@ -6,8 +6,6 @@
 
 #include <hip/hip_runtime.h>
 
-#include <algorithm>
-
 #include "blocks.hpp"
 #include "host_checks.hpp"
 
@@ -146,10 +144,9 @@ fp8_status head_common(const HeadArgs& a, int64_t heads_q, int64_t heads_k, fp8b
 
 extern "C" {
 
-int64_t fp8_block_gemm_gated_workspace(int64_t M, int64_t I, int64_t K) {
-  if (gated_shape(M, I, K) != FP8_OK) return -1;
-  const int64_t cuts = std::max(fp8bs::gated_few_cuts(M, I, K, false), fp8bs::gated_few_cuts(M, I, K, true));   // one size for both
-  return (cuts > 1 ? 2 * cuts : cuts) * M * I * 4;
+int64_t fp8_block_gemm_gated_workspace(int64_t M, int64_t I, int64_t K, fp8_out_dtype h_dtype, int32_t codes) {
+  if (gated_shape(M, I, K) != FP8_OK || (h_dtype != FP8_OUT_BF16 && h_dtype != FP8_OUT_FP32)) return -1;
+  return fp8bs::gated_few_parts(M, I, K, codes != 0 || h_dtype == FP8_OUT_FP32, codes != 0) * M * I * 4;
 }
 
 fp8_status fp8_block_gemm_gated(int64_t M, int64_t I, int64_t K, const uint8_t* A, int64_t lda, const float* sA,
@@ -172,7 +169,7 @@ fp8_status fp8_block_gemm_gated(int64_t M, int64_t I, int64_t K, const uint8_t* 
     return FP8_ERR_UNSUPPORTED;
   // the scale tables are read through 32-bit byte offsets
   if ((K / 128) * ld_sa * 4 >= (int64_t{1} << 31) || (2 * I / 128) * ld_s13 * 4 >= (int64_t{1} << 31)) return FP8_ERR_UNSUPPORTED;
-  const int64_t need = fp8_block_gemm_gated_workspace(M, I, K);
+  const int64_t need = fp8_block_gemm_gated_workspace(M, I, K, h_dtype, q != nullptr);
   if (need > 0 && !workspace) return FP8_ERR_NULL;
   if (workspace_bytes < need) return FP8_ERR_SHAPE;
   const int64_t e = h_dtype == FP8_OUT_FP32 ? 4 : 2;

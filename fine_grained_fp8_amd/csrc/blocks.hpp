@@ -18,6 +18,7 @@ constexpr int kGatedMaxCuts = 8;
 // Workgroups that share the K blocks of a tile of channels, for FP32 results and codes
 // or for BF16 results; 0: the block GEMM is faster
 int gated_few_cuts(int64_t M, int64_t N, int64_t K, bool fp32);
+int64_t gated_few_parts(int64_t M, int64_t N, int64_t K, bool fp32, bool codes);
 struct GatedFewProblem {
   int M;
   int64_t N, K;

@@ -519,11 +519,12 @@ hipError_t few(const GatedFewProblem& p, hipStream_t stream) {
 bool exact_products(const GatedFewProblem& p) {
   return p.M <= kGatedExactTokens && (p.gated.q != nullptr || p.out_fp32);
 }
+int64_t groups_of_64(int64_t M, int64_t N) { return (M + 63) / 64 * (N / 64); }
 // 64 or 128 channels a workgroup: 128 where 64 give more workgroups than CUs (64 tokens,
 // 7168 x 18432: 58 us for 67; 1333 tokens, 2048 x 1408: 16.4 for 16.2, its codes 16.4 for 20.5;
 // 512 tokens, 7168 x 2048, 256 workgroups: 47 for 32)
 bool whole_tiles(const GatedFewProblem& p) {
-  return p.M > 16 && !exact_products(p) && (p.M + 63) / 64 * (p.N / 64) > 256;
+  return p.M > 16 && !exact_products(p) && groups_of_64(p.M, p.N) > 256;
 }
 template <int NT>
 hipError_t few_tokens(const GatedFewProblem& p, hipStream_t stream) {
@@ -759,9 +760,17 @@ int gated_few_cuts(int64_t M, int64_t N, int64_t K, bool fp32) {
   if (M <= 16) return (int)((kb + kMaxLds / kRowBlockLds - 1) / (kMaxLds / kRowBlockLds));
   const int64_t tiles = (M + 127) / 128 * (N / 128), wide = (M + 63) / 64 * (N / 128);
   if (M > 64 && wide > 256 && (tiles <= 256 || wide > 640)) return 0;
-  const int64_t groups = (M + 63) / 64 * (N / 64), worth = fp32 ? kb / 4 : (kb - 8) / 6;
+  const int64_t groups = groups_of_64(M, N), worth = fp32 ? kb / 4 : (kb - 8) / 6;
   const int64_t c = std::min({256 / groups, worth, (int64_t)kGatedMaxCuts});
   return (int)(c > 1 ? c : 1);
+}
+
+// FP32 arrays [M][N] that a call needs: both sums of each cut, or h where its tiles of codes
+// are spread over workgroups
+int64_t gated_few_parts(int64_t M, int64_t N, int64_t K, bool fp32, bool codes) {
+  const int cuts = gated_few_cuts(M, N, K, fp32);
+  if (cuts > 1) return 2 * cuts;
+  return cuts == 1 && codes && (M <= kGatedExactTokens || groups_of_64(M, N) <= 256) ? 1 : 0;
 }
 
 hipError_t launch_gated_few(const GatedFewProblem& p, hipStream_t stream) {

@@ -713,8 +713,8 @@ def _activation(name):
 # what the library answers for these sizes, asked for once (a call into it takes
 # half a microsecond)
 @functools.lru_cache(maxsize=4096)
-def _gated_workspace(M, I, K):
-    return _lib.load_library().fp8_block_gemm_gated_workspace(M, I, K)
+def _gated_workspace(M, I, K, h_type, codes):
+    return _lib.load_library().fp8_block_gemm_gated_workspace(M, I, K, h_type, codes)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -772,7 +772,7 @@ def _gated(A, sA, w13, s13, activation, quant, return_gate_up, out_dtype, out, s
         h_type = _is_fp32(out)
     if return_gate_up:
         gate_up = _made(A, (M, rows), torch.bfloat16, stream)
-    nbytes = _gated_workspace(M, I, K)
+    nbytes = _gated_workspace(M, I, K, h_type, quant)
     if nbytes != 0:
         ws = A.new_empty(max(nbytes, 0), dtype=torch.uint8) if stream is None else _workspace(nbytes, A.device, stream)
     st = lib.fp8_block_gemm_gated(

@@ -584,7 +584,8 @@ fp8_status fp8_block_gemm_gated(int64_t M, int64_t I, int64_t K, const uint8_t* 
                                 fp8_activation act, void* h, fp8_out_dtype h_dtype, int64_t ldh, void* gate_up,
                                 int64_t ld_gu, uint8_t* q, int64_t ldq, float* scales, int64_t ld_s,
                                 void* workspace, int64_t workspace_bytes, void* stream);
-int64_t fp8_block_gemm_gated_workspace(int64_t M, int64_t I, int64_t K);
+/* Bytes of workspace (0: none; -1: refused sizes), for h of h_dtype or (codes != 0) for q. */
+int64_t fp8_block_gemm_gated_workspace(int64_t M, int64_t I, int64_t K, fp8_out_dtype h_dtype, int32_t codes);
 
 /*
  * fp8_gated_backward - gradients of h = act(a) * u, up to the operands of the

@@ -5,6 +5,7 @@
 namespace fp8bs {
 
 int gated_few_cuts(int64_t M, int64_t N, int64_t K, bool) { return M > 64 ? 0 : N <= 2048 && K > 128 ? 2 : 1; }
+int64_t gated_few_parts(int64_t M, int64_t N, int64_t K, bool, bool) { return 2 * gated_few_cuts(M, N, K, true); }
 hipError_t launch_gated_few(const GatedFewProblem&, hipStream_t) { return hipErrorInvalidDeviceFunction; }
 hipError_t launch_gated_backward(const GatedGradProblem&, hipStream_t) { return hipErrorInvalidDeviceFunction; }
 hipError_t launch_head_norm_rotary(const HeadProblem&, hipStream_t) { return hipErrorInvalidDeviceFunction; }

@@ -48,7 +48,8 @@ def test_gated_validation(lib, M):
     def g(**c):
         return gated(lib, **{"M": M, "ld_sa": M, "ld_s": M, "ws": P[9], **c})
     f = lib.fp8_block_gemm_gated_workspace
-    assert f(8, 256, 384) > 0 and f(5000, 2048, 384) == 0 and f(8, 200, 384) == -1 and f(-1, 256, 384) == -1
+    assert f(8, 256, 384, 0, 1) > 0 and f(8, 200, 384, 0, 0) == -1 and f(-1, 256, 384, 0, 1) == -1 and f(8, 256, 384, 2, 0) == -1
+    assert f(5000, 2048, 384, 0, 0) == f(5000, 2048, 384, 1, 0) == f(5000, 2048, 384, 0, 1) == 0
     assert g() in PASSED and g(gu=None) in PASSED and g(ht=1) in PASSED and g(act=1) in PASSED
     codes = dict(h=None, q=P[6], s=P[7])
     assert g(**codes) in PASSED and g(**codes, gu=None) in PASSED
@@ -72,11 +73,15 @@ def test_gated_validation(lib, M):
     for k, v in (("h", P[0]), ("h", P[1]), ("h", P[2] + 4096), ("gu", P[3]), ("gu", P[4] + 256)):
         assert g(**{k: v}) == ALIAS, (k, v)
     assert g(**{**codes, "q": P[5]}) == ALIAS and g(**{**codes, "s": P[6]}) == ALIAS and g(**{**codes, "s": P[1]}) == ALIAS
-    if f(M, 256, 384) > 0:
-        assert g(ws=None) == NULL and g(bytes=64) == SHAPE and g(ws=P[9] + 4) == ALIGN
-        assert g(ws=P[0]) == ALIAS and g(ws=P[4]) == ALIAS
-    else:
-        assert g(ws=None, bytes=0) in PASSED
+    for result, out in ((dict(), P[4]), (dict(ht=1), P[4]), (codes, P[6])):
+        need = f(M, 256, 384, result.get("ht", 0), result is codes)
+        if need > 0:
+            few = {**result, "bytes": need}
+            assert g(**few) in PASSED and g(**{**few, "bytes": need - 1}) == SHAPE
+            assert g(**{**few, "ws": None}) == NULL and g(**{**few, "ws": P[9] + 4}) == ALIGN
+            assert g(**{**few, "ws": P[0]}) == ALIAS and g(**{**few, "ws": out}) == ALIAS
+        else:
+            assert g(**result, ws=None, bytes=0) in PASSED
 
 
 BACK = "T I dh ld_dh gu ld_gu act d ld_d q ldq s ld_s qt ldqt st ld_st ht sht ld_sht stream".split()
