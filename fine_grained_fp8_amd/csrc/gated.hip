@@ -212,7 +212,10 @@ __global__ __launch_bounds__(kRowWaves * 64) void gated_row_kernel(GatedFewProbl
 // waves), 48 tokens, 7168 x 2048 14.3 for 15.6, 64 tokens, 2048 x 1408 10.4 for 10.0; one
 // token, 7168 x 2048 11.8 for 9.8.  kExact: products of the codes as BF16, exact with FP32
 // sums, so that FP32 values, scales and codes do not move with the FP8 instruction's
-// truncation (up to 64 tokens; 64 of them, 7168 x 18432: 70 us for 58).
+// truncation (up to 64 tokens; 64 of them, 7168 x 18432: 76 us for 58).
+// What bounds it: a CU's loads, 25 - 30 bytes a clock of weights and token codes alike,
+// and one wave a SIMD whose products and folds take as long (1333 tokens, 2048 x 1408: loads
+// alone 12 us, products alone 14, both 14.7; 700, 7168 x 2048: 32, 32 and 38).
 template <int NT, int RT, int D, bool kExact>
 __global__ __launch_bounds__(256) void gated_few_kernel(GatedFewProblem p) {
   constexpr int kTokens = NT * 2048, kStage = kTokens + 256 + 4 * 256;   // codes, token scales, each wave's two weight scales
@@ -521,8 +524,8 @@ bool exact_products(const GatedFewProblem& p) {
 }
 int64_t groups_of_64(int64_t M, int64_t N) { return (M + 63) / 64 * (N / 64); }
 // 64 or 128 channels a workgroup: 128 where 64 give more workgroups than CUs (64 tokens,
-// 7168 x 18432: 58 us for 67; 1333 tokens, 2048 x 1408: 16.4 for 16.2, its codes 16.4 for 20.5;
-// 512 tokens, 7168 x 2048, 256 workgroups: 47 for 32)
+// 7168 x 18432: 57 us for 67; 1333 tokens, 2048 x 1408: 15.0 for 15.9; 1024, 7168 x 2048 39 for
+// 44; 256 tokens, 7168 x 4096, 256 workgroups of 64 channels: 37 for 29)
 bool whole_tiles(const GatedFewProblem& p) {
   return p.M > 16 && !exact_products(p) && groups_of_64(p.M, p.N) > 256;
 }
