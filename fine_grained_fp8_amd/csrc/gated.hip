@@ -23,7 +23,7 @@ typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
 
 // ===========================================================================
-// Up to 64 tokens
+// Few tokens, or few tiles
 // ===========================================================================
 
 // 8 E4M3 codes (two dwords) as BF16, exactly
