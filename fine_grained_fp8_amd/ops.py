@@ -700,7 +700,7 @@ def adapter_linear(x: torch.Tensor, w: torch.Tensor, sw: torch.Tensor, lora_a: t
 def _on_current_device(name, t):
     """Launches go to the current device: a tensor of another one is refused."""
     index = t.get_device()
-    if index >= 0 and index != torch.cuda.current_device():
+    if index >= 0 and index != torch._C._cuda_getDevice():      # a tensor there: the runtime is up
         raise ValueError(f"{name}: on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
@@ -739,6 +739,11 @@ def _made(like, shape, dtype, stream):
     return like.new_empty(shape, dtype=dtype) if stream is None else _empty(shape, dtype, like.device, stream)
 
 
+def _scratch(like, nbytes, stream):
+    """_workspace on like's device (the short call on the current stream)."""
+    return like.new_empty(max(nbytes, 0), dtype=torch.uint8) if stream is None else _workspace(nbytes, like.device, stream)
+
+
 def _gated(A, sA, w13, s13, activation, quant, return_gate_up, out_dtype, out, stream):
     lib = _lib.load_library()
     act = _activation(activation)
@@ -774,7 +779,7 @@ def _gated(A, sA, w13, s13, activation, quant, return_gate_up, out_dtype, out, s
         gate_up = _made(A, (M, rows), torch.bfloat16, stream)
     nbytes = _gated_workspace(M, I, K, h_type, quant)
     if nbytes != 0:
-        ws = A.new_empty(max(nbytes, 0), dtype=torch.uint8) if stream is None else _workspace(nbytes, A.device, stream)
+        ws = _scratch(A, nbytes, stream)
     st = lib.fp8_block_gemm_gated(
         M, I, K, A.data_ptr(), A.stride(0), sA.data_ptr(), ld_sa, w13.data_ptr(), s13.data_ptr(), ld_s13, act,
         _ptr(out), h_type, ldh, _ptr(gate_up), rows, _ptr(q), I, _ptr(s), ld_s, _ptr(ws), nbytes, _stream(stream))
@@ -1023,13 +1028,14 @@ def head_norm_rotary_backward(dq: torch.Tensor, dk, q, k, positions=None, freq=N
             raise ValueError(f"{name}: required with a norm")
         else:
             of = _check_heads(name, x, dtype, dev, T, heads, dim)[1]
-            grads[i] = _empty(dim, torch.float32, d.device, stream)
+            grads[i] = _made(d, (dim,), torch.float32, stream)
         o, to = _head_output("out", None if out is None else out[i], d, dev, (T, heads, dim), stream)
         made[i] = o
         sets[i] = _lib.HeadsGrad(x.data_ptr(), heads, of[0], of[1], None if w is None else w.data_ptr(), d.data_ptr(), strides[0],
                                  strides[1], o.data_ptr(), to[0], to[1], _ptr(grads[i]))
-    nbytes = 0 if norm is None else _heads_workspace(T, count[0], count[1], dim)
-    ws = _workspace(nbytes, (dq if dq is not None else dk).device, stream) if nbytes != 0 else None
+    nbytes, ws = 0 if norm is None else _heads_workspace(T, count[0], count[1], dim), None
+    if nbytes != 0:
+        ws = _scratch(dq if dq is not None else dk, nbytes, stream)
     st = lib.fp8_head_norm_rotary_backward(T, dim, _lib.OUT_FP32 if dtype == torch.float32 else _lib.OUT_BF16, sets[0], sets[1],
                                            *args, _ptr(ws), nbytes, _stream(stream))
     if st != 0:

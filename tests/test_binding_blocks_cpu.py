@@ -78,10 +78,11 @@ def test_tensors_of_another_device_than_the_current_one(monkeypatch):
 
         def get_device(self):
             return 1
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     with pytest.raises(ValueError, match="current device"):
         ops._on_current_device("x", Elsewhere())
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
     ops._on_current_device("x", Elsewhere())
 
 
