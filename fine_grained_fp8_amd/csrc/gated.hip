@@ -202,7 +202,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void gated_row_kernel(GatedFewProbl
 
 // From 17 tokens, in blocks of 16 NT, to where the block GEMM takes over.  A wave has RT
 // tiles of 16 channels, the gate rows and the up rows of each, for every token of its
-// block; a workgroup's four waves have neighbouring tiles, and `cuts` workgroups share
+// block; a workgroup's W waves have neighbouring tiles, and `cuts` workgroups share
 // the K blocks.  Weights go from memory straight into MFMA operand
 // registers; the token codes, which the waves share, through LDS by DMA.  Both are
 // asked for D blocks ahead, in the order they are needed (loads return in the
@@ -212,14 +212,15 @@ __global__ __launch_bounds__(kRowWaves * 64) void gated_row_kernel(GatedFewProbl
 // waves), 48 tokens, 7168 x 2048 14.3 for 15.6, 64 tokens, 2048 x 1408 10.4 for 10.0; one
 // token, 7168 x 2048 11.8 for 9.8.  kExact: products of the codes as BF16, exact with FP32
 // sums, so that FP32 values, scales and codes do not move with the FP8 instruction's
-// truncation (up to 64 tokens; 64 of them, 7168 x 18432: 76 us for 58).
+// truncation (up to 64 tokens; 64 of them, 7168 x 18432: 61 us for 49).
 // What bounds it: a CU's loads, 25 - 30 bytes a clock of weights and token codes alike,
 // and one wave a SIMD whose products and folds take as long (1333 tokens, 2048 x 1408: loads
 // alone 12 us, products alone 14, both 14.7; 700, 7168 x 2048: 32, 32 and 38).
-template <int NT, int RT, int D, bool kExact>
-__global__ __launch_bounds__(256) void gated_few_kernel(GatedFewProblem p) {
-  constexpr int kTokens = NT * 2048, kStage = kTokens + 256 + 4 * 256;   // codes, token scales, each wave's two weight scales
-  constexpr int kXOps = (NT * 2 + 3) / 4, kOps = kXOps + 2 + 4 * RT;     // loads of a wave for one block
+template <int NT, int RT, int D, bool kExact, int W>
+__global__ __launch_bounds__(64 * W) void gated_few_kernel(GatedFewProblem p) {
+  static_assert(RT == 1 || W == 4);
+  constexpr int kTokens = NT * 2048, kStage = kTokens + 256 + W * 256;   // codes, token scales, each wave's two weight scales
+  constexpr int kXOps = (NT * 2 + W - 1) / W, kOps = kXOps + 2 + 4 * RT;     // loads of a wave for one block
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];        // [D + 1][kStage]
   using lds_u8 = __attribute__((address_space(3))) uint8_t;
   using lds_ptr = __attribute__((address_space(3))) void*;
@@ -233,7 +234,8 @@ __global__ __launch_bounds__(256) void gated_few_kernel(GatedFewProblem p) {
   const int xcd = blockIdx.x & 7, each = gridDim.x >> 3;
   const int id = blocks == 1 ? blockIdx.x : xcd * each + min(xcd, (int)(gridDim.x & 7)) + (blockIdx.x >> 3);
   const int cut = id % p.cuts, block = id / p.cuts % blocks;
-  const int t0 = (id / p.cuts / blocks * 4 + wave) * RT;                             // the wave's first tile
+  const int first = (id / p.cuts / blocks * W + wave) * RT;                          // the wave's first tile
+  const int t0 = W == 4 ? first : min(first, tiles - 1);                             // past the last one: that one again, not stored
   const int m0 = block * NT * 16, M = min(p.M - m0, NT * 16);
   const int kb0 = (int)((int64_t)kb_n * cut / p.cuts), n = (int)((int64_t)kb_n * (cut + 1) / p.cuts) - kb0;
   // buffers end behind the last token and the last scale: what lies past them reads as zero
@@ -264,7 +266,7 @@ __global__ __launch_bounds__(256) void gated_few_kernel(GatedFewProblem p) {
 #pragma unroll
     for (int q = 0; q < kXOps; ++q) {
       int o = wave * kXOps + q;
-      if constexpr (kXOps * 4 != NT * 2) o = o < NT * 2 ? o : NT * 2 - 1;       // again: every wave counts the same loads
+      if constexpr (kXOps * W != NT * 2) o = o < NT * 2 ? o : NT * 2 - 1;       // again: every wave counts the same loads
       const uint32_t at = x_off + (uint32_t)(kb * 128 + o * 8 * (int)p.lda);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc_x, (lds_ptr)(st + o * 1024), 16, at, 0, 0, 0);
     }
@@ -420,7 +422,7 @@ __global__ __launch_bounds__(256) void gated_few_kernel(GatedFewProblem p) {
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int t = j * 16 + lrow;
-    if (t >= M) continue;
+    if (t >= M || (W != 4 && first >= tiles)) continue;
 #pragma unroll
     for (int i = 0; i < RT; ++i) leave(p, cut, m0 + t, (int64_t)(t0 + i) * 16 + lgrp * 4, acc[i][0][j], acc[i][1][j]);
   }
@@ -513,27 +515,46 @@ hipError_t row(const GatedFewProblem& p, hipStream_t stream) {
   return start<gated_row_kernel<RT, D>>((p.N / 16 + RT - 1) / RT * p.cuts, kRowWaves * 64, codes > sums ? codes : sums, p, stream);
 }
 
-template <int NT, int RT, int D, bool kExact>
+template <int NT, int RT, int D, bool kExact, int W>
 hipError_t few(const GatedFewProblem& p, hipStream_t stream) {
-  const int64_t blocks = (p.M + NT * 16 - 1) / (NT * 16);
-  return start<gated_few_kernel<NT, RT, D, kExact>>(p.N / (64 * RT) * blocks * p.cuts, 256, (D + 1) * (NT * 2048 + 1280), p, stream);
+  const int64_t blocks = (p.M + NT * 16 - 1) / (NT * 16), groups = (p.N / 16 + W * RT - 1) / (W * RT);
+  return start<gated_few_kernel<NT, RT, D, kExact, W>>(groups * blocks * p.cuts, 64 * W, (D + 1) * (NT * 2048 + 256 + W * 256), p,
+                                                       stream);
 }
 // FP32 results and codes of up to 64 tokens
 bool exact_products(const GatedFewProblem& p) {
   return p.M <= kGatedExactTokens && (p.gated.q != nullptr || p.out_fp32);
 }
 int64_t groups_of_64(int64_t M, int64_t N) { return (M + 63) / 64 * (N / 64); }
-// 64 or 128 channels a workgroup: 128 where 64 give more workgroups than CUs (64 tokens,
-// 7168 x 18432: 57 us for 67; 1333 tokens, 2048 x 1408: 15.0 for 15.9; 1024, 7168 x 2048 39 for
-// 44; 256 tokens, 7168 x 4096, 256 workgroups of 64 channels: 37 for 29)
+// Workgroups of four waves with two tiles each, 128 channels, which also have whole 1x128
+// tiles of codes: where four waves of one tile give more workgroups than CUs (1333 tokens,
+// 2048 x 1408: 15.0 us for 15.9; 1024, 7168 x 2048 39 for 44; 256 tokens, 7168 x 4096, 256 workgroups
+// of 64 channels: 37 for 29).  Eight waves of one tile were as fast in one round of the
+// CUs and slower in two (700, 7168 x 5632: 75 for 68).
 bool whole_tiles(const GatedFewProblem& p) {
   return p.M > 16 && !exact_products(p) && groups_of_64(p.M, p.N) > 256;
 }
+// Waves of one tile: five or six where they make one round of the CUs and four do not
+// (us with 4 / 5 / 6, or four of two tiles: 48 tokens, 7168 x 18432 66 / 48 / 49, 57; its codes
+// 71 / 54 / 55; 7168 x 24576 71 / 83 / 63, 75; 700 tokens, 7168 x 2048 38 / 57 / 33, 36).
+int few_waves(const GatedFewProblem& p) {
+  const int64_t blocks = (p.M + 63) / 64;
+  for (const int w : {4, 5, 6})
+    if ((p.N / 16 + w - 1) / w * blocks <= 256) return w;
+  return 4;
+}
+template <int NT, bool kExact>
+hipError_t few_tokens(const GatedFewProblem& p, hipStream_t stream) {
+  const int w = few_waves(p);
+  if constexpr (!kExact) {
+    // of more than 64 tokens, codes need whole tiles or a launch more
+    if (whole_tiles(p) && (w == 4 || p.gated.q != nullptr)) return few<NT, 2, 2, false, 4>(p, stream);
+  }
+  return w == 5 ? few<NT, 1, 3, kExact, 5>(p, stream) : w == 6 ? few<NT, 1, 3, kExact, 6>(p, stream) : few<NT, 1, 3, kExact, 4>(p, stream);
+}
 template <int NT>
 hipError_t few_tokens(const GatedFewProblem& p, hipStream_t stream) {
-  if (exact_products(p)) return few<NT, 1, 3, true>(p, stream);
-  if (whole_tiles(p)) return few<NT, 2, 2, false>(p, stream);
-  return few<NT, 1, 3, false>(p, stream);
+  return exact_products(p) ? few_tokens<NT, true>(p, stream) : few_tokens<NT, false>(p, stream);
 }
 
 // ===========================================================================
