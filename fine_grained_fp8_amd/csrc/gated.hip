@@ -92,7 +92,7 @@ __device__ __forceinline__ void leave(const GatedFewProblem& p, int cut, int t, 
   else *reinterpret_cast<v4bf*>(static_cast<uint16_t*>(p.C) + t * p.ldc + n) = __builtin_convertvector(h, v4bf);
 }
 
-// Up to 16 tokens.  A workgroup has RT tiles of 16 channels, the gate rows and
+// Up to 16 tokens and 8192 channels.  A workgroup has RT tiles of 16 channels, the gate rows and
 // the up rows of each; its eight waves deal the K blocks of its share (all of
 // K, unless its codes would not fit LDS).  The weights go from memory straight
 // into MFMA operand registers, D blocks of a wave in flight.  The token codes are
@@ -100,7 +100,7 @@ __device__ __forceinline__ void leave(const GatedFewProblem& p, int cut, int t, 
 // K), so that the loop's only loads from memory are weights: loads return in the
 // order of their issue, and a token operand asked for in the loop would wait for
 // all weights asked for before it.
-// What bounds it: reading the weights (one token, 7168 x 18432: 264 MB in 51 us, 5.2
+// What bounds it: reading the weights (one token, 7168 x 8192: 117 MB in 24 us, 4.9
 // TB/s), and for small ones the latency of a launch and of the first load (7168 x 2048,
 // 29 MB: 10.4 us; 2048 x 1408: 5.1).
 template <int RT, int D>
@@ -200,7 +200,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void gated_row_kernel(GatedFewProbl
   }
 }
 
-// From 17 tokens, in blocks of 16 NT, to where the block GEMM takes over.  A wave has RT
+// More tokens or channels, in blocks of 16 NT tokens, to where the block GEMM takes over.  A wave has RT
 // tiles of 16 channels, the gate rows and the up rows of each, for every token of its
 // block; a workgroup's W waves have neighbouring tiles, and `cuts` workgroups share
 // the K blocks.  Weights go from memory straight into MFMA operand
@@ -210,9 +210,9 @@ __global__ __launch_bounds__(kRowWaves * 64) void gated_row_kernel(GatedFewProbl
 // K blocks, each with its own token operands (as for up to 16 tokens), us: 64
 // tokens, 7168 x 18432 58 for 99 (a workgroup's tokens are read once for its four
 // waves), 48 tokens, 7168 x 2048 14.3 for 15.6, 64 tokens, 2048 x 1408 10.4 for 10.0; one
-// token, 7168 x 2048 11.8 for 9.8.  kExact: products of the codes as BF16, exact with FP32
+// token, 7168 x 2048 11.8 for 9.8, 7168 x 18432 47.7 for 50 (264 MB: 5.5 TB/s).  kExact: products of the codes as BF16, exact with FP32
 // sums, so that FP32 values, scales and codes do not move with the FP8 instruction's
-// truncation (up to 64 tokens; 64 of them, 7168 x 18432: 61 us for 49).
+// truncation (all results of up to 16 tokens, and up to 64; 64 of them, 7168 x 18432: 61 us for 49).
 // What bounds it: a CU's loads, 25 - 30 bytes a clock of weights and token codes alike,
 // and one wave a SIMD whose products and folds take as long (1333 tokens, 2048 x 1408: loads
 // alone 12 us, products alone 14, both 14.7; 700, 7168 x 2048: 32, 32 and 38).
@@ -503,11 +503,10 @@ hipError_t start(int64_t grid, int block, int64_t lds, const GatedFewProblem& p,
   return hipGetLastError();
 }
 
-// tiles of a workgroup of the kernel for up to 16 tokens: one workgroup for each of the 256 CUs
-int row_tiles(int64_t N) {
-  const int64_t n = (N / 16 + 255) / 256;
-  return (int)(n < 5 ? n : 5);
-}
+// The kernel for up to 16 tokens and the other one, one token, us: 7168 x 8192 24.0 / 25.6; 7168 x
+// 9216 27.2 / 26.5; 7168 x 12288 34.6 / 32.4; 7168 x 18432 50 / 47.7; 7168 x 24576 81 / 62; 2048 x 10240
+// 11.4 / 10.4; 16 tokens, 7168 x 8192 26.1 / 26.7; 7168 x 18432 51.6 / 47.5.
+bool by_rows(int64_t M, int64_t N) { return M <= 16 && N <= 8192; }
 template <int RT, int D>
 hipError_t row(const GatedFewProblem& p, hipStream_t stream) {
   const int64_t share = (p.K / 128 + p.cuts - 1) / p.cuts, sums = (int64_t)kRowWaves * RT * 2048;
@@ -521,9 +520,9 @@ hipError_t few(const GatedFewProblem& p, hipStream_t stream) {
   return start<gated_few_kernel<NT, RT, D, kExact, W>>(groups * blocks * p.cuts, 64 * W, (D + 1) * (NT * 2048 + 256 + W * 256), p,
                                                        stream);
 }
-// FP32 results and codes of up to 64 tokens
+// all results of up to 16 tokens, FP32 results and codes of up to 64
 bool exact_products(const GatedFewProblem& p) {
-  return p.M <= kGatedExactTokens && (p.gated.q != nullptr || p.out_fp32);
+  return p.M <= 16 || (p.M <= kGatedExactTokens && (p.gated.q != nullptr || p.out_fp32));
 }
 int64_t groups_of_64(int64_t M, int64_t N) { return (M + 63) / 64 * (N / 64); }
 // Workgroups of four waves with two tiles each, 128 channels, which also have whole 1x128
@@ -532,7 +531,7 @@ int64_t groups_of_64(int64_t M, int64_t N) { return (M + 63) / 64 * (N / 64); }
 // of 64 channels: 37 for 29).  Eight waves of one tile were as fast in one round of the
 // CUs and slower in two (700, 7168 x 5632: 75 for 68).
 bool whole_tiles(const GatedFewProblem& p) {
-  return p.M > 16 && !exact_products(p) && groups_of_64(p.M, p.N) > 256;
+  return !exact_products(p) && groups_of_64(p.M, p.N) > 256;
 }
 // Waves of one tile: five or six where they make one round of the CUs and four do not
 // (us with 4 / 5 / 6, or four of two tiles: 48 tokens, 7168 x 18432 66 / 48 / 49, 57; its codes
@@ -781,7 +780,7 @@ __global__ __launch_bounds__(2048 / kGR, kWavesPerSimd) void gated_backward_kern
 // 2048 x 1408: 10.5 for 10.9; 17 tokens, 1024 x 1024 7.6 for 6.3).
 int gated_few_cuts(int64_t M, int64_t N, int64_t K, bool fp32) {
   const int64_t kb = K / 128;
-  if (M <= 16) return (int)((kb + kMaxLds / kRowBlockLds - 1) / (kMaxLds / kRowBlockLds));
+  if (by_rows(M, N)) return (int)((kb + kMaxLds / kRowBlockLds - 1) / (kMaxLds / kRowBlockLds));
   const int64_t tiles = (M + 127) / 128 * (N / 128), wide = (M + 63) / 64 * (N / 128);
   if (M > 64 && wide > 256 && (tiles <= 256 || wide > 640)) return 0;
   const int64_t groups = groups_of_64(M, N), worth = fp32 ? kb / 4 : (kb - 8) / 6;
@@ -799,14 +798,10 @@ int64_t gated_few_parts(int64_t M, int64_t N, int64_t K, bool fp32, bool codes) 
 
 hipError_t launch_gated_few(const GatedFewProblem& p, hipStream_t stream) {
   hipError_t e;
-  if (p.M <= 16) {
-    switch (row_tiles(p.N)) {
-      case 1: e = row<1, 2>(p, stream); break;
-      case 2: e = row<2, 1>(p, stream); break;
-      case 3: e = row<3, 1>(p, stream); break;
-      case 4: e = row<4, 1>(p, stream); break;
-      default: e = row<5, 1>(p, stream); break;
-    }
+  if (by_rows(p.M, p.N)) {
+    e = p.N <= 4096 ? row<1, 2>(p, stream) : row<2, 1>(p, stream);     // one workgroup for each of the 256 CUs
+  } else if (p.M <= 16) {
+    e = few_tokens<1, true>(p, stream);
   } else {
     e = p.M <= 32 ? few_tokens<2>(p, stream) : p.M <= 48 ? few_tokens<3>(p, stream) : few_tokens<4>(p, stream);
   }

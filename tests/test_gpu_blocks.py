@@ -99,6 +99,7 @@ GATED = [  # M, K, I, kind
     (65, 4096, 128, "gelu"), (200, 8192, 256, "silu"), (1000, 256, 1920, "gelu"), (65, 128, 128, "silu"), (90, 256, 16384, "silu"), (100, 384, 256, "gelu"), (128, 512, 128, "silu"), (129, 1024, 384, "silu"), (300, 640, 1408, "gelu"),
     (1333, 256, 512, "silu"), (700, 2560, 512, "gelu"), (333, 2944, 256, "silu"),
     (700, 256, 2048, "gelu"), (33, 256, 18432, "silu"), (60, 128, 24576, "gelu"),
+    (1, 512, 9216, "silu"), (16, 384, 18432, "gelu"), (5, 128, 24576, "silu"), (9, 256, 8192, "gelu"),
     (450, 256, 4608, "silu"), (129, 384, 11264, "gelu"), (2300, 640, 1408, "gelu"), (1111, 128, 3840, "silu"),
 ]
 
