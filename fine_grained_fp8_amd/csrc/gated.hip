@@ -779,6 +779,7 @@ __global__ __launch_bounds__(2048 / kGR, kWavesPerSimd) void gated_backward_kern
 // FP32 results follow them, so that the codes are those of that result (64 tokens,
 // 2048 x 1408: 10.5 for 10.9; 17 tokens, 1024 x 1024 7.6 for 6.3).
 int gated_few_cuts(int64_t M, int64_t N, int64_t K, bool fp32) {
+  if (M == 0) return 0;      // no tokens: nothing to share out (the quotients below divide by their groups)
   const int64_t kb = K / 128;
   if (by_rows(M, N)) return (int)((kb + kMaxLds / kRowBlockLds - 1) / (kMaxLds / kRowBlockLds));
   const int64_t tiles = (M + 127) / 128 * (N / 128), wide = (M + 63) / 64 * (N / 128);

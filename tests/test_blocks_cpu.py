@@ -255,6 +255,38 @@ def test_head_norm_rotary_backward_validation(lib):
         assert hback(lib, **c) == ALIAS, c
 
 
+def test_sizes_of_every_workspace_have_an_answer(tmp_path):
+    """The size rules of the built library over their range, an empty batch among them, in a
+    process of their own (an integer division by zero there ends it)."""
+    from fine_grained_fp8_amd import _lib, build
+    if not os.path.exists(_lib.LIB_PATH):
+        build.build()
+    code = """
+from fine_grained_fp8_amd import _lib
+lib = _lib.load_library()
+f, g = lib.fp8_block_gemm_gated_workspace, lib.fp8_head_norm_rotary_backward_workspace
+for I in (128, 2048, 8064, 8192, 8320, 18432, 24576, (1 << 24) - 256):
+    for K in (128, 1024, 7168, 16384, (1 << 23) - 128):
+        fits = (I + 128) * K < 1 << 31
+        for h_dtype, codes in ((0, 0), (1, 0), (0, 1)):
+            print("I", I, "K", K, h_dtype, codes, flush=True)
+            assert f(0, I, K, h_dtype, codes) == (0 if fits else -1)
+            for M in (1, 16, 17, 64, 65, 128, 1333, 4096, 42000, 1 << 31):
+                n = f(M, I, K, h_dtype, codes)
+                unit = M * I * 4
+                assert n == -1 if not fits or M * I // 16384 >= 1 << 31 else n >= 0 and n % unit == 0, (M, n)
+for T in (0, 1, 3, 4096, 1 << 25):
+    for q in (0, 1, 64, 1 << 20):
+        for k in (0, 1, 64, 1 << 20):
+            for dim in (2, 64, 130, 1024):
+                n = g(T, q, k, dim)
+                print("T", T, q, k, dim, n, flush=True)
+                assert n == -1 if q + k == 0 else n == 0 if T == 0 else 0 < n <= 1280 * dim * 4
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT, timeout=300)
+    assert r.returncode == 0, (r.returncode, r.stdout[-200:], r.stderr[-2000:])
+
+
 def test_block_validation_under_asan_ubsan(tmp_path):
     """api_blocks.cpp built on the host with sanitizers, its launchers
     replaced by stubs, runs the validation tests above without a report."""

@@ -213,6 +213,18 @@ def test_gated_empty(gpu_lib):
     assert y.shape == (0, 256) and kept.shape == (0, 512)
 
 
+@pytest.mark.parametrize("I", [8320, 18432])
+def test_gated_empty_and_wide(gpu_lib, I):
+    """No tokens, more channels than the kernel for few of them takes."""
+    A, sA = torch.empty(0, 128, dtype=torch.uint8, device="cuda"), torch.empty(1, 0, device="cuda")
+    w, sw = torch.zeros(2 * I, 128, dtype=torch.uint8, device="cuda"), torch.ones(2 * I // 128, 1, device="cuda")
+    for dtype in (torch.bfloat16, torch.float32):
+        y, kept = gpu_lib.block_gemm_gated(A, sA, w, sw, out_dtype=dtype, return_gate_up=True)
+        assert y.shape == (0, I) and y.dtype == dtype and kept.shape == (0, 2 * I)
+    q, s, kept = gpu_lib.block_gemm_gated_quant(A, sA, w, sw, return_gate_up=True)
+    assert q.shape == (0, I) and s.shape == (I // 128, 0) and kept.shape == (0, 2 * I)
+
+
 # ------------------------------------------------------------- its backward pass
 
 def backward_errors(dh, a, u, kind):
