@@ -13,8 +13,6 @@
 namespace fp8bs {
 
 // ---- the gated product for few tokens or few tiles ----
-constexpr int kGatedExactTokens = 64;    // up to so many: FP32 values and codes from exact products (up to 16: BF16 ones too)
-constexpr int kGatedMaxCuts = 8;
 // Workgroups that share the K blocks of a tile of channels, for FP32 results and codes
 // or for BF16 results; 0: the block GEMM is faster
 int gated_few_cuts(int64_t M, int64_t N, int64_t K, bool fp32);

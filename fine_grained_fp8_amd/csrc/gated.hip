@@ -5,9 +5,9 @@
 //   a = X W1^T, u = X W3^T,  h = act(a) u,  act(a) = a logistic(v(a))
 //   da = dh u act'(a),  du = dh act(a)
 //   act'(a) = z + a z (1 - z) v'(a),  z = logistic(v(a))
-#include <algorithm>
 #include <atomic>
 
+#include "block_rules.hpp"
 #include "blocks.hpp"
 #include "device.hpp"
 #include "gate.hpp"
@@ -35,9 +35,7 @@ __device__ __forceinline__ v8bf codes_to_bf16(int lo, int hi) {
   return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-constexpr int64_t kMaxLds = 163840;
 constexpr int kRowWaves = 8;                     // waves of a workgroup of the kernel for up to 16 tokens
-constexpr int64_t kRowBlockLds = 2048 + 64;      // its LDS for one K block: 16 tokens' codes and scales
 
 // A 128-wide K block of a 16-row operand: a lane's 32 codes (bytes 16 g.. and
 // 64 + 16 g.. for lane group g).
@@ -503,10 +501,6 @@ hipError_t start(int64_t grid, int block, int64_t lds, const GatedFewProblem& p,
   return hipGetLastError();
 }
 
-// The kernel for up to 16 tokens and the other one, one token, us: 7168 x 8192 24.0 / 25.6; 7168 x
-// 9216 27.2 / 26.5; 7168 x 12288 34.6 / 32.4; 7168 x 18432 50 / 47.7; 7168 x 24576 81 / 62; 2048 x 10240
-// 11.4 / 10.4; 16 tokens, 7168 x 8192 26.1 / 26.7; 7168 x 18432 51.6 / 47.5.
-bool by_rows(int64_t M, int64_t N) { return M <= 16 && N <= 8192; }
 template <int RT, int D>
 hipError_t row(const GatedFewProblem& p, hipStream_t stream) {
   const int64_t share = (p.K / 128 + p.cuts - 1) / p.cuts, sums = (int64_t)kRowWaves * RT * 2048;
@@ -520,40 +514,21 @@ hipError_t few(const GatedFewProblem& p, hipStream_t stream) {
   return start<gated_few_kernel<NT, RT, D, kExact, W>>(groups * blocks * p.cuts, 64 * W, (D + 1) * (NT * 2048 + 256 + W * 256), p,
                                                        stream);
 }
-// all results of up to 16 tokens, FP32 results and codes of up to 64
-bool exact_products(const GatedFewProblem& p) {
-  return p.M <= 16 || (p.M <= kGatedExactTokens && (p.gated.q != nullptr || p.out_fp32));
-}
-int64_t groups_of_64(int64_t M, int64_t N) { return (M + 63) / 64 * (N / 64); }
-// Workgroups of four waves with two tiles each, 128 channels, which also have whole 1x128
-// tiles of codes: where four waves of one tile give more workgroups than CUs (1333 tokens,
-// 2048 x 1408: 15.0 us for 15.9; 1024, 7168 x 2048 39 for 44; 256 tokens, 7168 x 4096, 256 workgroups
-// of 64 channels: 37 for 29).  Eight waves of one tile were as fast in one round of the
-// CUs and slower in two (700, 7168 x 5632: 75 for 68).
-bool whole_tiles(const GatedFewProblem& p) {
-  return !exact_products(p) && groups_of_64(p.M, p.N) > 256;
-}
-// Waves of one tile: five or six where they make one round of the CUs and four do not
-// (us with 4 / 5 / 6, or four of two tiles: 48 tokens, 7168 x 18432 66 / 48 / 49, 57; its codes
-// 71 / 54 / 55; 7168 x 24576 71 / 83 / 63, 75; 700 tokens, 7168 x 2048 38 / 57 / 33, 36).
-int few_waves(const GatedFewProblem& p) {
-  const int64_t blocks = (p.M + 63) / 64;
-  for (const int w : {4, 5, 6})
-    if ((p.N / 16 + w - 1) / w * blocks <= 256) return w;
-  return 4;
-}
+// FP32 values leave: an FP32 result, or codes of one
+bool fp32_values(const GatedFewProblem& p) { return p.gated.q != nullptr || p.out_fp32; }
+bool has_whole_tiles(const GatedFewProblem& p) { return whole_tiles(p.M, p.N, fp32_values(p)); }
 template <int NT, bool kExact>
 hipError_t few_tokens(const GatedFewProblem& p, hipStream_t stream) {
-  const int w = few_waves(p);
+  const int w = few_waves(p.M, p.N);
   if constexpr (!kExact) {
     // of more than 64 tokens, codes need whole tiles or a launch more
-    if (whole_tiles(p) && (w == 4 || p.gated.q != nullptr)) return few<NT, 2, 2, false, 4>(p, stream);
+    if (has_whole_tiles(p) && (w == 4 || p.gated.q != nullptr)) return few<NT, 2, 2, false, 4>(p, stream);
   }
   return w == 5 ? few<NT, 1, 3, kExact, 5>(p, stream) : w == 6 ? few<NT, 1, 3, kExact, 6>(p, stream) : few<NT, 1, 3, kExact, 4>(p, stream);
 }
 template <int NT>
 hipError_t few_tokens(const GatedFewProblem& p, hipStream_t stream) {
-  return exact_products(p) ? few_tokens<NT, true>(p, stream) : few_tokens<NT, false>(p, stream);
+  return exact_products(p.M, fp32_values(p)) ? few_tokens<NT, true>(p, stream) : few_tokens<NT, false>(p, stream);
 }
 
 // ===========================================================================
@@ -759,43 +734,8 @@ __global__ __launch_bounds__(2048 / kGR, kWavesPerSimd) void gated_backward_kern
 
 }  // namespace
 
-// Which kernel.  The block GEMM's tiles are 128 tokens x 128 channels, one a CU; with
-// few of them most CUs idle, and just above 256 the second round is a short one.  There
-// workgroups of up to 64 tokens and 64 or 128 channels are faster: while those of 128
-// channels are one round of the CUs, and up to 640 of them where the GEMM takes two.
-// Measured, us, GEMM / these (tiles; workgroups of 128): 128 tokens, 7168 x 2048 (16; 32) 55 / 16;
-// 300, 2048 x 1408 (33; 55) 19 / 10; 1333, 2048 x 1408 (121; 231) 20 / 15; 1024, 7168 x 2048
-// (128; 256) 53 / 39; 300, 7168 x 6400 (150; 250) 55 / 39; 450, 7168 x 4608 (144; 288) 52 / 57;
-// 65, 7168 x 18432 (144; 288) 64 / 83; 1333, 2048 x 2048 (176; 336) 20 / 21; 512, 7168 x 7168
-// (224; 448) 59 / 67; 2700, 2048 x 1408 (242; 473) 22 / 25; 700, 7168 x 5632 (264; 484) 89 / 68;
-// 192, 7168 x 18432 (288; 432) 107 / 82; 1333, 2048 x 3840 (330; 630) 40 / 33; 640, 2048 x 8192
-// (320; 640) 38 / 38; 4096, 2048 x 1408 (352; 704) 36 / 34; 800, 2048 x 8192 (448; 832) 38 / 44.
-// K is cut so that every CU has a workgroup; a cut adds partial sums and the
-// finishing launch, about what 6 to 8 blocks of K take: 48 tokens, 7168 x 2048, with 1 / 2
-// / 4 / 8 cuts 26 / 18 / 15 / 14; 256 tokens 29 / 24 / 24 / 30; 300 tokens, 2048 x 1408 11 / 14 / 18.
-// Codes of tiles that no workgroup has whole take that launch anyway, and cuts of four
-// blocks pay: 48 tokens, 2048 x 1408, 1 / 2 / 4 / 8 cuts 14.9 / 11.4 / 10.5 / 12; 64 tokens, 1024 x 512,
-// 1 / 2 / 4 11.4 / 9.6 / 9.4; 128 tokens, 2048 x 1408 13.4 / 11.8 / 11.9; 300 tokens 13.7 / 14.1 / 18.
-// FP32 results follow them, so that the codes are those of that result (64 tokens,
-// 2048 x 1408: 10.5 for 10.9; 17 tokens, 1024 x 1024 7.6 for 6.3).
-int gated_few_cuts(int64_t M, int64_t N, int64_t K, bool fp32) {
-  if (M == 0) return 0;      // no tokens: nothing to share out (the quotients below divide by their groups)
-  const int64_t kb = K / 128;
-  if (by_rows(M, N)) return (int)((kb + kMaxLds / kRowBlockLds - 1) / (kMaxLds / kRowBlockLds));
-  const int64_t tiles = (M + 127) / 128 * (N / 128), wide = (M + 63) / 64 * (N / 128);
-  if (M > 64 && wide > 256 && (tiles <= 256 || wide > 640)) return 0;
-  const int64_t groups = groups_of_64(M, N), worth = fp32 ? kb / 4 : (kb - 8) / 6;
-  const int64_t c = std::min({256 / groups, worth, (int64_t)kGatedMaxCuts});
-  return (int)(c > 1 ? c : 1);
-}
-
-// FP32 arrays [M][N] that a call needs: both sums of each cut, or h where its tiles of codes
-// are spread over workgroups
-int64_t gated_few_parts(int64_t M, int64_t N, int64_t K, bool fp32, bool codes) {
-  const int cuts = gated_few_cuts(M, N, K, fp32);
-  if (cuts > 1) return 2 * cuts;
-  return cuts == 1 && codes && (M <= kGatedExactTokens || groups_of_64(M, N) <= 256) ? 1 : 0;
-}
+int gated_few_cuts(int64_t M, int64_t N, int64_t K, bool fp32) { return gated_cuts(M, N, K, fp32); }
+int64_t gated_few_parts(int64_t M, int64_t N, int64_t K, bool fp32, bool codes) { return gated_parts(M, N, K, fp32, codes); }
 
 hipError_t launch_gated_few(const GatedFewProblem& p, hipStream_t stream) {
   hipError_t e;
@@ -808,7 +748,7 @@ hipError_t launch_gated_few(const GatedFewProblem& p, hipStream_t stream) {
   }
   if (e != hipSuccess) return e;
   // sums of cut tiles; codes of tiles that no workgroup has whole
-  if (p.cuts > 1 || (p.gated.q != nullptr && !whole_tiles(p))) {
+  if (p.cuts > 1 || (p.gated.q != nullptr && !has_whole_tiles(p))) {
     const int64_t groups = (int64_t)p.M * (p.N / 128);
     hipLaunchKernelGGL(gated_finish_kernel, dim3((unsigned)((groups + 15) / 16)), dim3(256), 0, stream, p);
   }

@@ -15,6 +15,7 @@
 // lane for either order of pairs, so the rotation moves nothing between lanes,
 // and the lane's eight angles serve all heads of the token.  A wave works on 64 / G
 // heads of one token at a time, queries first and then keys.
+#include "block_rules.hpp"
 #include "blocks.hpp"
 #include "device.hpp"
 #include "rows.hpp"
@@ -23,9 +24,7 @@ namespace fp8bs {
 
 namespace {
 
-constexpr int kHB = 256, kHW = kHB / 64;   // threads and waves of a workgroup
-constexpr int kMaxGradParts = 1280;        // workgroups of the backward pass: see divide()
-constexpr int kForwardBlocks = 1280;       // and of the forward pass
+constexpr int kHB = kHW * 64;               // threads of a workgroup
 
 typedef int hv4i __attribute__((ext_vector_type(4)));
 typedef int hv2i __attribute__((ext_vector_type(2)));
@@ -284,9 +283,6 @@ struct Lane {
   }
 };
 
-// passes of a wave over the heads of a set, 64 / G heads each
-__host__ __device__ inline int passes(int64_t heads, int G) { return (int)((heads * G + 63) / 64); }
-
 // A weight into LDS as FP32 (null: ones), by the workgroup; a barrier publishes it.
 __device__ __forceinline__ void stage_weight(const void* w, int is_f32, int dim, float* to) {
   for (int e = threadIdx.x; e < dim; e += kHB)
@@ -300,13 +296,6 @@ __device__ __forceinline__ void lds_barrier() {
   __asm__ volatile("" ::: "memory");
 }
 
-// How a set is divided: a token's passes into `cuts` units of `per`, the units of all
-// tokens dealt to the waves of `blocks` workgroups in the order of memory, so that
-// what is in flight lies close together (8192 tokens of 64 + 8 heads of 128, forward 62 us
-// for 66, backward 91 for 100, where each wave had a token of its own).
-struct Shares {
-  int per, cuts, blocks;
-};
 // A wave's walk over its units: token, unit of the token, pass.
 struct Walk {
   int64_t t;
@@ -339,10 +328,6 @@ struct Walk {
     open();
   }
 };
-struct GradGrid {
-  Shares set[2];
-};
-
 // Forward.  A wave walks over tokens with its share of their heads, queries and then
 // keys; the heads of its next two passes are in flight, across tokens too.  FP32 results
 // are stored past the caches (5003 x 16 + 16 heads of 80: 27.6 us for 29.5; BF16: no
@@ -506,51 +491,6 @@ __global__ __launch_bounds__(1024) void head_grad_sum_kernel(const float* __rest
   }
 }
 
-// A lane has 2 R elements.  With 8 instead of 16 the backward pass's sums, weights and
-// heads in flight take about 100 registers instead of 160 - 190 (8192 tokens of 32 + 8
-// heads of 128, BF16: 56 us for 62; 5003 tokens of 16 + 16 heads of 80, FP32: 39 for 46),
-// and FP32 heads are still moved in 16-byte pieces (their forward pass 26 us for 31).
-// BF16 forward keeps 16, pieces of 16 bytes.  Heads over 512 would take more than a wave
-// with 8.
-int run_of(bool back, bool x_fp32, int64_t dim) { return (back || x_fp32) && dim <= 512 ? 4 : 8; }
-// lanes of a head
-int lanes_of(int64_t dim, int R) {
-  int g = 4;
-  while (g * 2 * R < dim) g *= 2;
-  return g;
-}
-
-// A set of n passes a token for at most `most` workgroups.
-Shares share_out(int64_t T, int64_t n, int64_t most, int64_t per) {
-  if (n * T <= most * kHW) per = 1;
-  const int64_t cuts = (n + per - 1) / per, blocks = (T * cuts + kHW - 1) / kHW;
-  return Shares{(int)per, (int)cuts, (int)(blocks < most ? blocks : most)};
-}
-// The forward pass
-Shares forward_shares(const HeadProblem& p) {
-  const int G = lanes_of(p.dim, run_of(false, p.x_fp32, p.dim));
-  return share_out(p.T, passes(p.set[0].heads, G) + passes(p.set[1].heads, G), kForwardBlocks, 2);
-}
-
-// The backward pass: as many workgroups as run at once on 256 CUs, five a CU by their
-// registers, dealt to the sets by their heads.  Measured with 768 / 1024 / 1280 / 2048, us:
-// BF16, 8192 tokens of 32 + 8 heads of 128 60 / 58 / 54 / 60; 20000 tokens of 16 + 4 heads of 64
-// 52 / 47 / 44 / 49; FP32, 5003 tokens of 16 + 16 heads of 80 39.4 / 39.3 / 38.5 / 38.7.
-GradGrid divide(int64_t T, int64_t q_heads, int64_t k_heads, int64_t dim) {
-  constexpr int64_t all = kMaxGradParts;
-  const int G = lanes_of(dim, run_of(true, true, dim));
-  const int64_t n[2] = {passes(q_heads, G), passes(k_heads, G)};
-  GradGrid g{};
-  for (int i = 0; i < 2; ++i) {
-    if (n[i] == 0 || T == 0) continue;
-    int64_t most = all * n[i] / (n[0] + n[1]);
-    if (most < 1) most = 1;
-    if (most > all - 1 && n[1 - i] > 0) most = all - 1;
-    g.set[i] = share_out(T, n[i], most, 2);
-  }
-  return g;
-}
-
 bool aligned_heads(const void* p, int64_t ld_token, int64_t ld_head, int64_t esz) {
   return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld_token * esz) % 16 == 0 && (ld_head * esz) % 16 == 0;
 }
@@ -562,7 +502,7 @@ void start(const HeadProblem& p, hipStream_t stream) {
     const int64_t parts = g.set[0].blocks + g.set[1].blocks;
     hipLaunchKernelGGL((head_norm_rotary_backward_kernel<T, kMode, G, R>), dim3((unsigned)parts), dim3(kHB), 0, stream, p, g);
   } else {
-    const Shares sh = forward_shares(p);
+    const Shares sh = forward_shares(p.T, p.set[0].heads, p.set[1].heads, p.dim, p.x_fp32);
     hipLaunchKernelGGL((head_norm_rotary_kernel<T, kMode, G, R>), dim3((unsigned)sh.blocks), dim3(kHB), 0, stream, p, sh);
   }
 }

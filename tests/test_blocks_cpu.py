@@ -287,6 +287,21 @@ for T in (0, 1, 3, 4096, 1 << 25):
     assert r.returncode == 0, (r.returncode, r.stdout[-200:], r.stderr[-2000:])
 
 
+def test_size_rules_under_ubsan(tmp_path):
+    """block_rules.hpp built on the host with the undefined-behaviour sanitizer (divisions
+    by zero and overflows end it), swept over the sizes that the checks let through."""
+    gxx = shutil.which("g++")
+    if not gxx:
+        pytest.skip("g++ is not available")
+    exe = str(tmp_path / "check_block_rules")
+    r = subprocess.run([gxx, "-std=c++17", "-O1", "-Wall", "-Werror", "-fsanitize=undefined", "-fno-sanitize-recover=undefined",
+                        "-I", os.path.join(ROOT, "fine_grained_fp8_amd", "csrc"), os.path.join(ROOT, "tests", "c", "check_block_rules.cpp"),
+                        "-o", exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-3000:]
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.endswith("violations=0\n"), r.stdout[-500:] + r.stderr[-2000:]
+
+
 def test_block_validation_under_asan_ubsan(tmp_path):
     """api_blocks.cpp built on the host with sanitizers, its launchers
     replaced by stubs, runs the validation tests above without a report."""
