@@ -570,6 +570,34 @@ def test_heads_into_one_row_and_nothing_else(gpu_lib):
         assert (out[T:] == 7).all() and (out[:, (Hq + Hk) * D:] == 7).all()
 
 
+@pytest.mark.parametrize("what", ["weight", "one_token", "one_head"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_aligned_heads_whatever_is_not_read_in_pieces(gpu_lib, dtype, what):
+    """A weight that starts anywhere, and strides that no step is taken along, change
+    nothing: the same sums in the same order, bit for bit."""
+    dtype = DT[dtype]
+    T, Hq, Hk, D = {"weight": (40, 6, 2, 128), "one_token": (1, 6, 2, 128), "one_head": (40, 1, 1, 128)}[what]
+    rotary = torch.arange(T, device="cuda") + 9, dev(0.9 ** np.arange(D // 2))
+    w = rand(2 * D + 2, 141, dtype, mean=1.0, std=0.3)
+    w = w[1:1 + D], w[D + 1:2 * D + 1]
+    heads = [rand((T, h, D), 142 + i, dtype) for i, h in enumerate((Hq, Hk, Hq, Hk))]
+    plain = [v.clone() for v in w]
+    want = gpu_lib.head_norm_rotary(*heads[:2], *rotary, q_weight=plain[0], k_weight=plain[1])
+    want_grad = gpu_lib.head_norm_rotary_backward(heads[2], heads[3], *heads[:2], *rotary, q_weight=plain[0], k_weight=plain[1])
+    if what != "weight":
+        w = plain
+        odd = (lambda t: t.as_strided(t.shape, (t.numel() + 3, D, 1))) if what == "one_token" else \
+            (lambda t: t.as_strided(t.shape, (D, D + 3, 1)))
+        heads = [odd(t) for t in heads]
+    else:
+        assert all(v.data_ptr() % 16 for v in w)
+    out = [torch.empty_like(t) for t in heads]
+    got = gpu_lib.head_norm_rotary(*heads[:2], *rotary, q_weight=w[0], k_weight=w[1], out=(out[0], out[1]))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    got = gpu_lib.head_norm_rotary_backward(heads[2], heads[3], *heads[:2], *rotary, q_weight=w[0], k_weight=w[1], out=(out[2], out[3]))
+    assert all(torch.equal(a, b) for a, b in zip(got, want_grad))
+
+
 def test_heads_nonfinite_values_stay_apart(gpu_lib):
     T, H, D, rot = 4, 3, 64, 32
     x = rand((T, H, D), 95, torch.float32)
