@@ -101,8 +101,8 @@ struct GradGrid {
 // A lane has 2 R elements.  With 8 instead of 16 the backward pass's sums, weights and
 // heads in flight take about 100 registers instead of 160 - 190 (8192 tokens of 32 + 8
 // heads of 128, BF16: 56 us for 62; 5003 tokens of 16 + 16 heads of 80, FP32: 39 for 46),
-// and FP32 heads are still moved in 16-byte pieces (their forward pass 26 us for 31).
-// BF16 forward keeps 16, pieces of 16 bytes.  Heads over 512 would take more than a wave
+// and FP32 heads are still moved in 16-byte pieces (their forward pass 26 us for 31), BF16 ones
+// in the backward pass in pieces of 8.  BF16 forward keeps 16, pieces of 16 bytes.  Heads over 512 would take more than a wave
 // with 8.
 inline int run_of(bool back, bool x_fp32, int64_t dim) { return (back || x_fp32) && dim <= 512 ? 4 : 8; }
 // lanes of a head

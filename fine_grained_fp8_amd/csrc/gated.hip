@@ -207,10 +207,10 @@ __global__ __launch_bounds__(kRowWaves * 64) void gated_row_kernel(GatedFewProbl
 // order of their issue); one barrier a block.  Measured against the waves dealing the
 // K blocks, each with its own token operands (as for up to 16 tokens), us: 64
 // tokens, 7168 x 18432 58 for 99 (a workgroup's tokens are read once for its four
-// waves), 48 tokens, 7168 x 2048 14.3 for 15.6, 64 tokens, 2048 x 1408 10.4 for 10.0; one
+// waves; with five, few_waves(), 48 to 58 from run to run), 48 tokens, 7168 x 2048 14.3 for 15.6, 64 tokens, 2048 x 1408 10.4 for 10.0; one
 // token, 7168 x 2048 11.8 for 9.8, 7168 x 18432 47.7 for 50 (264 MB: 5.5 TB/s).  kExact: products of the codes as BF16, exact with FP32
 // sums, so that FP32 values, scales and codes do not move with the FP8 instruction's
-// truncation (all results of up to 16 tokens, and up to 64; 64 of them, 7168 x 18432: 61 us for 49).
+// truncation (exact_products(); 64 tokens, 7168 x 18432: 61 us for 49).
 // What bounds it: a CU's loads, 25 - 30 bytes a clock of weights and token codes alike,
 // and one wave a SIMD whose products and folds take as long (1333 tokens, 2048 x 1408: loads
 // alone 12 us, products alone 14, both 14.7; 700, 7168 x 2048: 32, 32 and 38).

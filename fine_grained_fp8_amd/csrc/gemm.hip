@@ -1316,9 +1316,9 @@ __global__ __launch_bounds__(kThreads, 1) void block_gemm_direct_kernel(GemmProb
   // All four waves' 128 columns x 128 rows meet in the staging areas, so that the
   // stores write whole row segments (256 bytes of BF16, 128 of codes) and a row's
   // 1x128 tile, spread over the waves, has its maximum.  The barriers wait for
-  // LDS alone: the next item's loads stay in flight.  4096 tokens, 7168 -> 18432: 899 us, 931
-  // with codes, 1006 with gate and up kept (302 MB more); the plain product of both 908.
-  // K of five blocks, 2422 x 640 -> 8448: 64, 71 and 72 for 60.
+  // LDS alone: the next item's loads stay in flight.  4096 tokens, 7168 -> 18432: 921 us, 946
+  // with codes, 1020 with gate and up kept (302 MB more); the plain product of both 926.
+  // 2048 -> 8192: 141, 154 and 158 for 129.  K of five blocks, 2422 x 640 -> 8448: 62, 71 and 71 for 58.
   auto lds_barrier = [&]() {
     __asm__ volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));   // lgkmcnt(0)

@@ -11,9 +11,9 @@
 // Bound by memory: every head is read once and written once (8192 tokens of 64 + 8 heads of
 // 128, BF16, nothing cached: forward 62 us, 302 MB; a copy of as much 57; without norm and
 // rotation the same).  A head lives in
-// the registers of G lanes, 8 pairs a lane: both elements of a pair meet in one
+// the registers of G lanes, R pairs a lane (8, or 4: run_of()): both elements of a pair meet in one
 // lane for either order of pairs, so the rotation moves nothing between lanes,
-// and the lane's eight angles serve all heads of the token.  A wave works on 64 / G
+// and the lane's R angles serve all heads of the token.  A wave works on 64 / G
 // heads of one token at a time, queries first and then keys.
 #include "block_rules.hpp"
 #include "blocks.hpp"

@@ -798,7 +798,9 @@ def block_gemm_gated(A: torch.Tensor, sA: torch.Tensor, w13: torch.Tensor, s13: 
     I rows of W1 and then the I rows of W3, s13 [2 I/128][>=K/128] their block
     scales.  activation: "silu" or "gelu" (tanh form).  Returns h [M][I] in
     out_dtype (bfloat16 or float32), or with return_gate_up (h, gate_up): the two
-    projections in bfloat16 [M][2 I], which gated_backward_quant takes.
+    projections in bfloat16 [M][2 I], which gated_backward_quant takes.  A call repeats
+    itself bit for bit; a row moved within a batch of more than 64 may differ in FP32's last
+    bits, as the order of its sums follows its place.
     """
     h, _, _, gate_up = _gated(A, sA, w13, s13, activation, False, return_gate_up, out_dtype, out, stream)
     return (h, gate_up) if return_gate_up else h
@@ -971,15 +973,16 @@ def head_norm_rotary(q: torch.Tensor, k, positions=None, freq=None, *, q_weight=
     """Norm of each query and key head and the rotation by the token's position, in one pass.
 
     q [tokens][heads][dim], k [tokens][heads_k][dim] (bfloat16 or float32, either may be
-    None): any strides with contiguous channels, as views of a fused projection have
-    them.  norm: "rms", "layer" or None; q_weight, k_weight: optional [dim] vectors of one
+    None): contiguous channels, and token by token (as views of a fused projection are)
+    or head by head at any strides, nothing twice (expanded tensors are refused).  norm: "rms", "layer" or None; q_weight, k_weight: optional [dim] vectors of one
     type.  freq: float64 device vector of the rotated pairs' frequencies (rot/2 of them;
     rot <= dim, the other channels pass through), usually
     base ** (-2 i / rot); the angle is formed in FP64.  positions: int32 or int64
     [tokens], or [tokens][axes] with sections = how many consecutive pairs follow each
     axis (time, height, width; up to 4).  adjacent: pairs (2 i, 2 i + 1) instead of
     (i, i + rot/2).  positions = freq = None: the norm alone.
-    out: optional (q_out, k_out) of q's and k's shapes and type, any strides.
+    out: optional (q_out, k_out) of q's and k's shapes and type, at strides as q's; the two may
+    lie side by side in a token's row.
     Returns (q_out, k_out), None for a set that is None.
     """
     lib = _lib.load_library()

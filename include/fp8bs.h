@@ -235,7 +235,10 @@ fp8_status fp8_quant_weight_128x128_tiled(const void* w, int64_t rows, int64_t c
  *  The partial sums live in a workspace the library allocates on the first
  *  call on `stream` (128 KB per CU plus 4 bytes per CU, kept until the
  *  process ends, one per stream and device); without one - the stream is
- *  being captured into a graph, or the allocation fails - whole tiles run.
+ *  being captured into a graph and had none before, or the allocation fails -
+ *  whole tiles run.  A launch captured on a stream that has one uses it at every
+ *  replay: graphs captured on the same stream, or such a graph and calls on that
+ *  stream, must not run at the same time.
  */
 fp8_status fp8_block_gemm(fp8_gemm_layout layout, int64_t M, int64_t N, int64_t K,
                           const uint8_t* A, int64_t lda, const float* sA, int64_t ld_sa,
@@ -576,7 +579,12 @@ int64_t fp8_adapter_linear_workspace(int64_t T, int64_t N, int64_t K, int32_t ra
  *  GEMM's persistent kernel (with its per-stream workspace, but while the stream
  *  is being captured).  With up to 16 rows, and with up to 64 where h is FP32 or
  *  codes, the products are exact; otherwise they are the FP8 matrix
- *  instruction's.  M == 0 is a no-op.
+ *  instruction's, as fp8_block_gemm's (FP32 values 3e-5 to 5e-5 off by 2-norm for 1e-7, which
+ *  BF16 rounding hides).  M == 0 is a no-op.
+ *  A call repeats itself bit for bit.  The order of the FP32 sums follows M and, from 65 rows
+ *  on, the row's place (blocks of 64 rows take K in different orders, the GEMM may cut some
+ *  tiles along K): a row moved within a batch, or between batches of other sizes, may
+ *  differ in FP32's last bits.
  */
 typedef enum { FP8_ACT_SILU = 0, FP8_ACT_GELU = 1 } fp8_activation;
 fp8_status fp8_block_gemm_gated(int64_t M, int64_t I, int64_t K, const uint8_t* A, int64_t lda, const float* sA,
@@ -638,9 +646,11 @@ fp8_status fp8_quant_act_cols(const void* x, int64_t rows, int64_t cols, int64_t
  *  freq       FP64 [rot/2]; the angle is formed in FP64, so that positions of millions keep
  *             their last bits
  *  dim        even, 2 .. 1024; eps >= 0.  Any alignment to the element size is taken; 16-byte
- *             aligned heads with dim % 16 == 0 and rot % 16 == 0 are moved in 16-byte
- *             pieces.  No output may overlap an input or another output (the two
- *             outputs may lie side by side within each token's row).
+ *             aligned heads with dim % 16 == 0 and rot % 16 == 0 are moved in pieces of 16
+ *             bytes (BF16 heads of up to 512 channels in the backward pass: 8), others element
+ *             by element, which takes 1.2 (FP32) to 2.7 times as long.  No output may overlap an
+ *             input or another output (the two outputs may lie side by side within each
+ *             token's row, all of the queries beside all of the keys).
  *  tokens == 0 is a no-op.
  */
 typedef enum { FP8_HEAD_NONE = 0, FP8_HEAD_RMS = 1, FP8_HEAD_LAYER = 2 } fp8_head_norm;
