@@ -173,7 +173,9 @@ __device__ __forceinline__ int cols_tile_word(int row, int word) {
   return g * 544 + (row & 15) * 32 + ((word + 8 * (g >> 1)) & 31);
 }
 
-template <bool kTiled>
+// kRagged: rows is no multiple of 128, the rows past the last one count as zeros (a kernel of
+// its own: the guard costs whole blocks 2%, 8192 x 7168 30.4 us for 29.7).
+template <bool kTiled, bool kRagged>
 __global__ __launch_bounds__(256) void quant_cols_kernel(
     const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ldx, int64_t ncb, int64_t nbr,
     int64_t nblocks, uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ scales,
@@ -190,8 +192,8 @@ __global__ __launch_bounds__(256) void quant_cols_kernel(
       const int64_t col = lc0 + cc * 8;
       uint4 val = make_uint4(0, 0, 0, 0);
       const uint16_t* src = x + (lr0 + row) * ldx + col;
-      if (lr0 + row >= rows) {
-        // past the last row (ragged rows): zeros
+      if (kRagged && lr0 + row >= rows) {
+        // past the last row: zeros
       } else if (col + 8 <= cols) {
         val = *reinterpret_cast<const uint4*>(src);
       } else if (col < cols) {               // ragged last chunk: stay inside the row
@@ -566,11 +568,14 @@ hipError_t launch_quant_cols(const uint16_t* x, int64_t rows, int64_t cols, int6
   const int64_t nblocks = ((rows + 127) / 128) * ncb;
   const int64_t nbr = (rows + 127) / 128;
   const int64_t grid = nblocks;                // one block per workgroup (as the dual kernel)
-  if (tiled)
-    hipLaunchKernelGGL(quant_cols_kernel<true>, dim3((unsigned)grid), dim3(256), 0, stream,
+  if (rows % 128 != 0)                         // tiled only: the validation requires whole blocks otherwise
+    hipLaunchKernelGGL((quant_cols_kernel<true, true>), dim3((unsigned)grid), dim3(256), 0, stream,
+                       x, rows, cols, ldx, ncb, nbr, nblocks, q, ldq, scales, ld_s, amax_out);
+  else if (tiled)
+    hipLaunchKernelGGL((quant_cols_kernel<true, false>), dim3((unsigned)grid), dim3(256), 0, stream,
                        x, rows, cols, ldx, ncb, nbr, nblocks, q, ldq, scales, ld_s, amax_out);
   else
-    hipLaunchKernelGGL(quant_cols_kernel<false>, dim3((unsigned)grid), dim3(256), 0, stream,
+    hipLaunchKernelGGL((quant_cols_kernel<false, false>), dim3((unsigned)grid), dim3(256), 0, stream,
                        x, rows, cols, ldx, ncb, nbr, nblocks, q, ldq, scales, ld_s, amax_out);
   return hipGetLastError();
 }
