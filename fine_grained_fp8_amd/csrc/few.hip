@@ -17,34 +17,20 @@
 // dependent launch costs 4 - 5 us.
 #include "device.hpp"
 #include "layers.hpp"
+#include "operands.hpp"
 
 namespace fp8bs {
 
 namespace {
 
 typedef int fv4i __attribute__((ext_vector_type(4)));
-typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
 constexpr int kB = 512;         // threads of a workgroup
 constexpr int kW = kB / 64;     // and its waves
 
 __device__ __forceinline__ v8bf as_bf16x8(const fv4i& v) { return __builtin_bit_cast(v8bf, v); }
 
-// 8 E4M3 codes (two dwords) as BF16, exactly
-__device__ __forceinline__ v8bf codes_to_bf16(int lo, int hi) {
-  const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
-  const v2bf b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
-  const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
-  const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
-  return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
-// One 128-wide K block of a 16-row operand: a lane's 32 codes (bytes 16 g.. and
-// 64 + 16 g.. of the block for lane group g), as the framework's tiles and
-// its FP8 MFMA order them.
-struct Block {
-  fv4i lo, hi;
-};
+// a lane's part of an operand tile
 __device__ __forceinline__ Block load_tile(const uint8_t* tile, int lane) {
   return Block{*reinterpret_cast<const fv4i*>(tile + lane * 16), *reinterpret_cast<const fv4i*>(tile + 1024 + lane * 16)};
 }
@@ -55,20 +41,6 @@ __device__ __forceinline__ Block load_row(const uint8_t* block, uint32_t lane_of
 }
 __device__ __forceinline__ v8i as_operand(const Block& b) {
   return v8i{b.lo[0], b.lo[1], b.lo[2], b.lo[3], b.hi[0], b.hi[1], b.hi[2], b.hi[3]};
-}
-struct Bf16Block {
-  v8bf f[4];
-};
-__device__ __forceinline__ Bf16Block to_bf16(const Block& b) {
-  return Bf16Block{{codes_to_bf16(b.lo[0], b.lo[1]), codes_to_bf16(b.lo[2], b.lo[3]),
-                    codes_to_bf16(b.hi[0], b.hi[1]), codes_to_bf16(b.hi[2], b.hi[3])}};
-}
-// partial sums of one K block with exact products and FP32 additions
-__device__ __forceinline__ v4f block_product(const Bf16Block& a, const Bf16Block& b) {
-  v4f c = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) c = mfma_bf16_16x16x32(a.f[i], b.f[i], c);
-  return c;
 }
 
 __device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }

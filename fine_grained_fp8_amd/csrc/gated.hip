@@ -11,6 +11,7 @@
 #include "blocks.hpp"
 #include "device.hpp"
 #include "gate.hpp"
+#include "operands.hpp"
 #include "rows.hpp"
 
 namespace fp8bs {
@@ -19,42 +20,13 @@ namespace {
 
 typedef int gv4i __attribute__((ext_vector_type(4)));
 typedef int gv2i __attribute__((ext_vector_type(2)));
-typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
 
 // ===========================================================================
 // Few tokens, or few tiles
 // ===========================================================================
 
-// 8 E4M3 codes (two dwords) as BF16, exactly
-__device__ __forceinline__ v8bf codes_to_bf16(int lo, int hi) {
-  const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
-  const v2bf b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
-  const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
-  const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
-  return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
 constexpr int kRowWaves = 8;                     // waves of a workgroup of the kernel for up to 16 tokens
-
-// A 128-wide K block of a 16-row operand: a lane's 32 codes (bytes 16 g.. and
-// 64 + 16 g.. for lane group g).
-struct Block {
-  gv4i lo, hi;
-};
-struct Bf16Block {
-  v8bf f[4];
-};
-__device__ __forceinline__ Bf16Block to_bf16(const Block& b) {
-  return Bf16Block{{codes_to_bf16(b.lo[0], b.lo[1]), codes_to_bf16(b.lo[2], b.lo[3]),
-                    codes_to_bf16(b.hi[0], b.hi[1]), codes_to_bf16(b.hi[2], b.hi[3])}};
-}
-__device__ __forceinline__ v4f block_product(const Bf16Block& a, const Bf16Block& b) {
-  v4f c = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) c = mfma_bf16_16x16x32(a.f[i], b.f[i], c);
-  return c;
-}
 
 __device__ __forceinline__ float gated(float a, float u, int gelu) {
   return a * logistic(gelu ? gelu_argument(a) : a) * u;
